@@ -275,8 +275,33 @@ int moe_lm_argmax(const moe_lm_head* lm, const uint16_t* x, uint32_t flags, floa
    [n_rows][K]) = bf16(q * scale + bias) for matrix 0 of m.  K % 64 == 0. */
 int moe_dequant(const moe_q4mat* m, int32_t n_rows, int32_t K, uint16_t* w_out, void* stream);
 
+/* Residual addition and root-mean-square norm of T token rows, the step
+   between two layers: with v = x + residual (fp32 sum, rounded once to the
+   residual's type; v = x without a residual)
+     residual_out = v
+     y            = v * w / sqrt(mean(v^2) + eps), w = weight (+ 1 with
+                    MOE_NORM_PLUS_ONE)
+   computed in fp32 from the rounded v, one row per token.
+     x: bf16 [T][d];  weight: bf16 [d]
+     residual: bf16 [T][d], or fp32 with MOE_NORM_RESIDUAL_FLOAT, or NULL
+     residual_out: as residual; may be residual itself; NULL: not stored;
+       without a residual it has to be NULL
+     y: bf16 [T][d] (one rounding), or NULL
+     y8, y8_scale: the row in 8 bits, or both NULL: y8 e4m3 (OCP) [T][d] and one
+       fp32 scale per 64 columns, [T][d/64]: scale = max|y| / 448 over the group,
+       y8 = e4m3(y / scale), to nearest even, from the unrounded y.  A group of
+       zeros has scale 0; a NaN makes its whole group's codes and scale NaN.
+   At least one of y and y8.  y may be x or a bf16 residual; other overlaps of
+   outputs with inputs are not allowed.  1 <= T <= MOE_MAX_TOKENS, d a multiple
+   of 64, <= MOE_MAX_D; eps finite, >= 0.  One kernel, no workspace. */
+#define MOE_NORM_PLUS_ONE 1u
+#define MOE_NORM_RESIDUAL_FLOAT 2u
+int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
+                 void* residual_out, const uint16_t* weight, float eps, uint32_t flags,
+                 uint16_t* y, uint8_t* y8, float* y8_scale, void* stream);
+
 /* Timing hook.  While `events` is non-NULL, every moe_route, moe_prefill,
-   moe_decode, moe_decode_tokens and moe_lm_argmax call made on this host thread records events[0] on its stream
+   moe_decode, moe_decode_tokens, moe_lm_argmax and moe_add_norm call made on this host thread records events[0] on its stream
    before its first kernel and events[i] right after its i-th kernel, for
    i < n (moe_route: router logits (with MOE_LOGITS_IN: the clearing of
    the histogram), top-k + histogram, scan + scatter + maps;
@@ -284,7 +309,8 @@ int moe_dequant(const moe_q4mat* m, int32_t n_rows, int32_t K, uint16_t* w_out, 
    shared down + combine; moe_decode and moe_decode_tokens: router
    partial sums + shared gate/up, logits + top-k + routed gate/up, down +
    combine; moe_lm_argmax: output head (with MOE_LOGITS_IN: the scan of the
-   given logits), pick + embedding row).  The
+   given logits), pick + embedding row).  The one-kernel calls record events[0]
+   and events[1]: moe_add_norm.  The
    elapsed time between consecutive events is one kernel's duration.  events
    are hipEvent_t handles created and owned by the caller; pass NULL to stop. */
 void moe_trace_events(void* const* events, int32_t n);

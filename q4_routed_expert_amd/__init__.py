@@ -288,5 +288,73 @@ def lm_argmax(lm: DeviceLmHead, x: torch.Tensor | None, ws: torch.Tensor,
     return logits, token, x_next
 
 
+def _launch_on(where: str, stream, **tensors):
+    """Stream handle for a call whose tensors are `tensors` (None: absent).  All of
+    them have to be on one GPU; that GPU has to be the current one, because the
+    library launches on the current device."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on the GPU")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{where}: {name} is on {t.device}, other arguments on {dev}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: the tensors are on {dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device != dev:
+        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {dev}")
+    return stream.cuda_stream
+
+
+def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+             eps: float = 1e-6, plus_one: bool = False, residual_out: torch.Tensor | None = None,
+             y: torch.Tensor | None = None, e4m3: bool = False, y8: torch.Tensor | None = None,
+             y8_scale: torch.Tensor | None = None, stream=None):
+    """Residual addition and RMS norm of the rows of x [T, d] (bf16): (y, y8, y8_scale).
+
+    residual: bf16 or fp32 [T, d]; x + residual goes to residual_out (which may be
+    residual itself; None: not stored).  plus_one: the weight used is weight + 1.
+    y (bf16) is written when given, and by default when no 8-bit output is asked
+    for; e4m3=True (or y8 and y8_scale given) asks for e4m3 codes [T, d] with one
+    fp32 scale per 64 columns [T, d / 64]."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, d], not {tuple(x.shape)}")
+    T, d = x.shape
+    flags = _abi.MOE_NORM_PLUS_ONE if plus_one else 0
+    _need(x, "x", torch.bfloat16, T * d)
+    _need(weight, "weight", torch.bfloat16, d)
+    if residual is not None:
+        rt = torch.float32 if residual.dtype == torch.float32 else torch.bfloat16
+        _need(residual, "residual", rt, T * d)
+        if residual_out is not None:
+            _need(residual_out, "residual_out", rt, T * d)
+        if rt == torch.float32:
+            flags |= _abi.MOE_NORM_RESIDUAL_FLOAT
+    e4m3 = e4m3 or y8 is not None or y8_scale is not None
+    if e4m3:
+        if y8 is None:
+            y8 = torch.empty((T, d), dtype=torch.float8_e4m3fn, device=x.device)
+        if y8_scale is None:
+            y8_scale = torch.empty((T, d // 64), dtype=torch.float32, device=x.device)
+        _need(y8, "y8", torch.float8_e4m3fn, T * d)
+        _need(y8_scale, "y8_scale", torch.float32, T * (d // 64))
+    elif y is None:
+        y = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
+    if y is not None:
+        _need(y, "y", torch.bfloat16, T * d)
+    s = _launch_on("add_norm", stream, x=x, weight=weight, residual=residual,
+                   residual_out=residual_out, y=y, y8=y8, y8_scale=y8_scale)
+    _check(_abi.lib().moe_add_norm(_ptr(x), T, d, _ptr(residual), _ptr(residual_out), _ptr(weight),
+                                   eps, flags, _ptr(y), _ptr(y8), _ptr(y8_scale), s),
+           "moe_add_norm")
+    return y, y8, y8_scale
+
+
 def library_path() -> str:
     return _abi.LIB_PATH

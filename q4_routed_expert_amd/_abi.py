@@ -9,6 +9,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libq4moe.so
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, -1, -2, -3, -4
 MOE_LOGITS_IN = 1
 MOE_ITEM_ROWS_64, MOE_ITEM_ROWS_32, MOE_ITEM_ROWS_16 = 2, 4, 8
+MOE_NORM_PLUS_ONE, MOE_NORM_RESIDUAL_FLOAT = 1, 2
 MOE_BLOCK_ROWS = 32
 MOE_TILE_ROWS = 128
 MOE_ROUTE_BLOCK = 256
@@ -22,7 +23,8 @@ MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_MAX_TOKENS, MOE_MAX_D, MOE_MAX_INTER = 256, 8
 EXPORTS = ("moe_block_map_capacity", "moe_workspace_bytes", "moe_route", "moe_prefill",
            "moe_prefill_ex", "moe_trace_events",
            "moe_decode", "moe_decode_tokens", "moe_dequant", "moe_strerror", "moe_last_error",
-           "moe_lm_workspace_bytes", "moe_lm_argmax", "moe_decode_tokens_static")
+           "moe_lm_workspace_bytes", "moe_lm_argmax", "moe_decode_tokens_static",
+           "moe_add_norm")
 
 
 class Q4Mat(C.Structure):
@@ -79,8 +81,9 @@ def lib():
         L.moe_lm_workspace_bytes.argtypes = [vp]
         L.moe_lm_workspace_bytes.restype = C.c_size_t
         L.moe_lm_argmax.argtypes = [vp, vp, C.c_uint32, vp, vp, vp, vp, C.c_size_t, vp]
+        L.moe_add_norm.argtypes = [vp, i32, i32, vp, vp, vp, C.c_float, C.c_uint32, vp, vp, vp, vp]
         for f in ("moe_route", "moe_prefill", "moe_prefill_ex", "moe_decode", "moe_decode_tokens", "moe_dequant",
-                  "moe_lm_argmax", "moe_decode_tokens_static"):
+                  "moe_lm_argmax", "moe_decode_tokens_static", "moe_add_norm"):
             getattr(L, f).restype = C.c_int
         L.moe_trace_events.argtypes = [vp, i32]
         L.moe_trace_events.restype = None

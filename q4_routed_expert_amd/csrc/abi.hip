@@ -9,6 +9,7 @@
 
 #include "internal.h"
 #include "lmhead.h"
+#include "ops.h"
 
 namespace {
 
@@ -441,6 +442,44 @@ int moe_lm_argmax(const moe_lm_head* lm, const uint16_t* x, uint32_t flags, floa
     a.part = (int2*)base;
     trace_begin((hipStream_t)stream);
     return hip_status(q4moe::launch_lm_argmax(a, logits_in, (hipStream_t)stream), "lm argmax");
+}
+
+int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
+                 void* residual_out, const uint16_t* weight, float eps, uint32_t flags,
+                 uint16_t* y, uint8_t* y8, float* y8_scale, void* stream) {
+    int rc;
+    if ((rc = check_tokens(T))) return rc;
+    if (d <= 0) return fail(MOE_EINVAL, "d=%d must be positive", d);
+    if (d % MOE_GROUP || d > MOE_MAX_D)
+        return fail(MOE_EUNSUPPORTED, "d=%d must be a multiple of %d and <= %d", d, MOE_GROUP,
+                    MOE_MAX_D);
+    if (flags & ~(MOE_NORM_PLUS_ONE | MOE_NORM_RESIDUAL_FLOAT))
+        return fail(MOE_EINVAL, "unknown flags 0x%x", flags);
+    if (!(eps >= 0.0f) || eps > 3.4e38f) return fail(MOE_EINVAL, "eps must be finite and >= 0");
+    if ((rc = check_ptr(x, "x")) || (rc = check_ptr(weight, "weight")) ||
+        (rc = check_ptr(residual, "residual", true)) ||
+        (rc = check_ptr(residual_out, "residual_out", true)) || (rc = check_ptr(y, "y", true)) ||
+        (rc = check_ptr(y8, "y8", true)) || (rc = check_ptr(y8_scale, "y8_scale", true)))
+        return rc;
+    if (residual_out && !residual)
+        return fail(MOE_EINVAL, "residual_out without a residual");
+    if (!y && !y8) return fail(MOE_EINVAL, "neither y nor y8 is given");
+    if (!y8 != !y8_scale) return fail(MOE_EINVAL, "y8 and y8_scale come together");
+    q4moe::NormArgs a;
+    a.x = x;
+    a.residual = residual;
+    a.residual_out = residual_out;
+    a.weight = weight;
+    a.y = y;
+    a.y8 = y8;
+    a.y8_scale = y8_scale;
+    a.T = T;
+    a.d = d;
+    a.eps = eps;
+    a.w_add = (flags & MOE_NORM_PLUS_ONE) ? 1.0f : 0.0f;
+    a.res_f32 = (flags & MOE_NORM_RESIDUAL_FLOAT) != 0;
+    trace_begin((hipStream_t)stream);
+    return hip_status(q4moe::launch_add_norm(a, (hipStream_t)stream), "add norm");
 }
 
 const char* moe_strerror(int code) {

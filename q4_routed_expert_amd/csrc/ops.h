@@ -1,0 +1,24 @@
+// ops.h -- launchers of the operators around the MoE layer (scored routing,
+// 4-bit products for a few rows, sampling, residual + RMS norm), shared by
+// abi.hip and their translation units.
+#pragma once
+#include "internal.h"
+
+namespace q4moe {
+
+// y = norm(x + residual) (moe_add_norm).
+struct NormArgs {
+    const uint16_t* x;        // bf16 [T][d]
+    const void* residual;     // bf16 or fp32 [T][d], or NULL
+    void* residual_out;       // the same type, or NULL; may be residual
+    const uint16_t* weight;   // bf16 [d]
+    uint16_t* y;              // bf16 [T][d], or NULL
+    uint8_t* y8;              // e4m3 [T][d], or NULL
+    float* y8_scale;          // [T][d/64], with y8
+    int T, d;
+    float eps, w_add;         // the weight used is weight + w_add
+    bool res_f32;
+};
+hipError_t launch_add_norm(const NormArgs& a, hipStream_t s);
+
+}  // namespace q4moe
