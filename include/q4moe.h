@@ -275,6 +275,47 @@ int moe_lm_argmax(const moe_lm_head* lm, const uint16_t* x, uint32_t flags, floa
    [n_rows][K]) = bf16(q * scale + bias) for matrix 0 of m.  K % 64 == 0. */
 int moe_dequant(const moe_q4mat* m, int32_t n_rows, int32_t K, uint16_t* w_out, void* stream);
 
+/* Routing with other scores than moe_route's, for the same expert products:
+   moe_route_scored fills the same moe_routing, so moe_prefill follows it as it
+   follows moe_route, and moe_decode / moe_decode_tokens use its selection with
+   MOE_ROUTING_IN.  Per token with logits l:
+     s_e = softmax(l)_e or 1 / (1 + exp(-l_e))
+     v_e = s_e + balance_e            (the selection value; balance NULL: s_e)
+   An expert is out when its logit is NaN or -inf or its balance is not finite:
+   s_e = 0 and v_e = -inf.  With n_groups > 1 the experts fall into n_groups
+   runs of E / n_groups; a group's value is the sum of its group_top (1 or 2)
+   largest v_e that are not out (-inf without any), and only the top_groups
+   groups with the largest values take part.  idx = the top_k experts with the
+   largest v_e among them, larger first; equal values: the lower expert, the
+   lower group.  The weight of a slot is s_idx, divided by the sum over the k
+   slots with renorm (0 if that sum is 0), times scale; experts that are out
+   fill slots only when nothing else is left, with weight 0, so a token whose
+   logits are all -inf contributes 0.  Scores and comparisons are in 64 bits. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_MAX_GROUPS 64
+typedef struct {
+    int32_t score;        /* MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID */
+    int32_t n_groups;     /* 1 <= n_groups <= MOE_MAX_GROUPS, divides n_experts */
+    int32_t top_groups;   /* 1 <= top_groups <= n_groups, top_groups * E / n_groups >= top_k */
+    int32_t group_top;    /* 1 or 2 (read when n_groups > 1) */
+    int32_t renorm;       /* 0 or 1 */
+    float scale;          /* finite */
+    const float* balance; /* fp32 [E], 16-byte aligned, or NULL */
+} moe_router_spec;
+/* Arguments and outputs are moe_route's; of L only the sizes, and without
+   MOE_LOGITS_IN w_router and router_bias, are used (the expert matrices may be
+   NULL). */
+int moe_route_scored(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t flags,
+                     const moe_router_spec* spec, const moe_routing* r, void* stream);
+
+/* moe_decode, moe_decode_tokens and moe_decode_tokens_static: the selection is
+   given in r->topk_idx [T][k] and r->topk_w [T][k] (r is required), as
+   moe_route or moe_route_scored wrote them; no logits are read or written.
+   Indices outside 0 .. E - 1 are brought into that range.  Not together with
+   MOE_LOGITS_IN. */
+#define MOE_ROUTING_IN 32u
+
 /* Residual addition and root-mean-square norm of T token rows, the step
    between two layers: with v = x + residual (fp32 sum, rounded once to the
    residual's type; v = x without a residual)
@@ -300,11 +341,12 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
                  void* residual_out, const uint16_t* weight, float eps, uint32_t flags,
                  uint16_t* y, uint8_t* y8, float* y8_scale, void* stream);
 
-/* Timing hook.  While `events` is non-NULL, every moe_route, moe_prefill,
+/* Timing hook.  While `events` is non-NULL, every moe_route, moe_route_scored, moe_prefill,
    moe_decode, moe_decode_tokens, moe_lm_argmax and moe_add_norm call made on this host thread records events[0] on its stream
    before its first kernel and events[i] right after its i-th kernel, for
    i < n (moe_route: router logits (with MOE_LOGITS_IN: the clearing of
-   the histogram), top-k + histogram, scan + scatter + maps;
+   the histogram), top-k + histogram, scan + scatter + maps; moe_route_scored
+   the same with its selection in the place of the top-k;
    moe_prefill: gate/up, routed down,
    shared down + combine; moe_decode and moe_decode_tokens: router
    partial sums + shared gate/up, logits + top-k + routed gate/up, down +

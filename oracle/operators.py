@@ -1,0 +1,68 @@
+"""The operators around the layer in 64 bits, one row at a time, from their
+definitions (numpy only; test infrastructure like the rest of this package)."""
+from __future__ import annotations
+
+import numpy as np
+
+
+def sort_assignments(idx, E: int) -> dict:
+    """counts, offsets, perm, inv_perm of selections idx [T, k] in stable expert order."""
+    flat = np.asarray(idx).reshape(-1)
+    counts = np.bincount(flat, minlength=E)
+    perm = np.argsort(flat, kind="stable")
+    inv = np.empty_like(perm)
+    inv[perm] = np.arange(flat.size)
+    return {"counts": counts, "offsets": np.concatenate([[0], np.cumsum(counts)]), "perm": perm,
+            "inv_perm": inv}
+
+
+def tiles(counts, rows: int) -> np.ndarray:
+    """(expert, first sorted row) of every tile of `rows` rows, experts ascending."""
+    out, row = [], 0
+    for e, c in enumerate(counts):
+        out += [(e, row + j) for j in range(0, int(c), rows)]
+        row += int(c)
+    return np.array(out, np.int64).reshape(-1, 2)
+
+
+def route_scored(logits, k: int, score="softmax", balance=None, n_groups=1, top_groups=1,
+                 group_top=1, renorm=True, scale=1.0):
+    """(idx [T, k], w [T, k]) of the scored routing."""
+    logits = np.asarray(logits, np.float32)
+    T, E = logits.shape
+    bal = np.zeros(E) if balance is None else np.asarray(balance, np.float64)
+    idx, w = np.empty((T, k), np.int32), np.zeros((T, k))
+    for t in range(T):
+        l = logits[t].astype(np.float64)
+        live = l > -np.inf  # (NaN compares false)
+        s = np.zeros(E)
+        if score == "sigmoid":
+            with np.errstate(over="ignore"):
+                s[live] = 1.0 / (1.0 + np.exp(-l[live]))
+        elif live.any():
+            m = l[live].max()
+            z = np.array([0.0 if not ok else 1.0 if v == m else np.exp(v - m)
+                          for v, ok in zip(l, live)])
+            s = z / z.sum()
+        live &= np.isfinite(bal)
+        v = np.where(live, s + np.where(np.isfinite(bal), bal, 0.0), -np.inf)
+        part = np.ones(E, bool)
+        if n_groups > 1:
+            per = E // n_groups
+            g = []
+            for j in range(n_groups):
+                best = np.sort(v[j * per:(j + 1) * per])[::-1][:group_top]
+                best = best[best > -np.inf]
+                g.append(best.sum() if best.size else -np.inf)
+            keep = np.argsort(-np.array(g), kind="stable")[:top_groups]
+            part[:] = False
+            for j in keep:
+                part[j * per:(j + 1) * per] = True
+        cand = np.flatnonzero(part)
+        pick = cand[np.argsort(-v[cand], kind="stable")][:k]
+        idx[t] = pick
+        wt = np.where(v[pick] > -np.inf, s[pick], 0.0)
+        if renorm:
+            wt = wt / wt.sum() if wt.sum() > 0 else np.zeros(k)
+        w[t] = wt * scale
+    return idx, w

@@ -156,6 +156,55 @@ def route(layer: DeviceLayer, x: torch.Tensor, routing: DeviceRouting | None = N
     return r
 
 
+class RouterSpec:
+    """How route_scored scores and selects: score "softmax" or "sigmoid"; balance (fp32
+    [E] on the GPU, or None) is added to the scores for the selection only; the
+    experts fall into n_groups runs, of which the top_groups best by the sum of
+    their group_top (1 or 2) largest values take part; renorm divides the weights by
+    their sum; scale multiplies them."""
+
+    def __init__(self, score: str = "softmax", n_groups: int = 1, top_groups: int = 1,
+                 group_top: int = 1, renorm: bool = True, scale: float = 1.0,
+                 balance: torch.Tensor | None = None):
+        kinds = {"softmax": _abi.MOE_SCORE_SOFTMAX, "sigmoid": _abi.MOE_SCORE_SIGMOID}
+        if score not in kinds:
+            raise ValueError(f"score must be one of {sorted(kinds)}, not {score!r}")
+        if balance is not None:
+            _need(balance, "balance", torch.float32, 1)
+        self.balance = balance  # keep the tensor alive
+        self.struct = _abi.RouterSpec(kinds[score], n_groups, top_groups, group_top, int(renorm),
+                                      scale, _ptr(balance))
+
+
+def route_scored(layer: DeviceLayer, x: torch.Tensor | None, spec: RouterSpec,
+                 routing: DeviceRouting | None = None, logits_in: bool = False,
+                 stream=None) -> DeviceRouting:
+    """Routing with the scores and the selection of `spec`.  Follow it with prefill,
+    or with decode / decode_tokens and routing_in=True.  With logits_in the T =
+    routing.T rows of routing.logits are routed; x is not used."""
+    if logits_in:
+        if routing is None:
+            raise ValueError("logits_in needs a routing that holds the logits")
+        T = routing.T
+    else:
+        T = x.shape[0]
+        _need(x, "x", torch.bfloat16, T * layer.d)
+        if routing is None:
+            routing = DeviceRouting(T, layer.n_experts, layer.top_k, x.device)
+    r = routing
+    if r.T < T or r.E != layer.n_experts or r.k != layer.top_k:
+        raise ValueError(f"routing is for T={r.T} E={r.E} k={r.k}, the call for T={T} "
+                         f"E={layer.n_experts} k={layer.top_k}")
+    if spec.balance is not None:
+        _need(spec.balance, "balance", torch.float32, layer.n_experts)
+    s = _launch_on("route_scored", stream, x=None if logits_in else x, logits=r.logits,
+                   balance=spec.balance)
+    _check(_abi.lib().moe_route_scored(C.addressof(layer.struct), None if logits_in else _ptr(x), T,
+                                       MOE_LOGITS_IN if logits_in else 0, C.addressof(spec.struct),
+                                       C.addressof(r.struct), s), "moe_route_scored")
+    return r
+
+
 _ITEM_ROWS_FLAGS = {128: 0, 64: _abi.MOE_ITEM_ROWS_64, 32: _abi.MOE_ITEM_ROWS_32,
                     16: _abi.MOE_ITEM_ROWS_16}
 
@@ -189,18 +238,27 @@ def prefill(layer: DeviceLayer, x: torch.Tensor, routing: DeviceRouting,
     return y
 
 
+def _decode_flags(routing, logits_in: bool, routing_in: bool) -> int:
+    if routing_in and routing is None:
+        raise ValueError("routing_in needs a routing")
+    return (MOE_LOGITS_IN if logits_in else 0) | (_abi.MOE_ROUTING_IN if routing_in else 0)
+
+
 def decode(layer: DeviceLayer, x: torch.Tensor, ws: torch.Tensor, y: torch.Tensor | None = None,
            routing: DeviceRouting | None = None, logits_in: bool = False,
-           stream=None) -> torch.Tensor:
+           stream=None, routing_in: bool = False) -> torch.Tensor:
+    """The layer for one token.  routing_in: the selection in routing (from route or
+    route_scored) is used instead of the layer's own routing."""
     if y is None:
         y = torch.empty((1, layer.d), dtype=torch.bfloat16, device=x.device)
-    flags = MOE_LOGITS_IN if logits_in else 0
+    flags = _decode_flags(routing, logits_in, routing_in)
     rs = C.addressof(routing.struct) if routing is not None else None
     _need(x, "x", torch.bfloat16, layer.d)
     _need(y, "y", torch.bfloat16, layer.d)
     if routing is not None:
         _need(routing.logits, "routing.logits", torch.float32, layer.n_experts)
         _need(routing.topk_idx, "routing.topk_idx", torch.int32, layer.top_k)
+        _need(routing.topk_w, "routing.topk_w", torch.float32, layer.top_k)
     _on_gpu(x=x, y=y, ws=ws)
     _check(_abi.lib().moe_decode(C.addressof(layer.struct), _ptr(x), flags, rs, _ptr(ws), ws.numel(),
                                  _ptr(y), _stream(stream)), "moe_decode")
@@ -209,18 +267,21 @@ def decode(layer: DeviceLayer, x: torch.Tensor, ws: torch.Tensor, y: torch.Tenso
 
 def decode_tokens(layer: DeviceLayer, x: torch.Tensor, ws: torch.Tensor,
                   y: torch.Tensor | None = None, routing: DeviceRouting | None = None,
-                  logits_in: bool = False, stream=None) -> torch.Tensor:
-    """The decode layer for T = x.shape[0] tokens (1 <= T <= MAX_DECODE_TOKENS)."""
+                  logits_in: bool = False, stream=None,
+                  routing_in: bool = False) -> torch.Tensor:
+    """The decode layer for T = x.shape[0] tokens (1 <= T <= MAX_DECODE_TOKENS).
+    routing_in: as decode's."""
     T = x.shape[0]
     if y is None:
         y = torch.empty((T, layer.d), dtype=torch.bfloat16, device=x.device)
-    flags = MOE_LOGITS_IN if logits_in else 0
+    flags = _decode_flags(routing, logits_in, routing_in)
     rs = C.addressof(routing.struct) if routing is not None else None
     _need(x, "x", torch.bfloat16, T * layer.d)
     _need(y, "y", torch.bfloat16, T * layer.d)
     if routing is not None:
         _need(routing.logits, "routing.logits", torch.float32, T * layer.n_experts)
         _need(routing.topk_idx, "routing.topk_idx", torch.int32, T * layer.top_k)
+        _need(routing.topk_w, "routing.topk_w", torch.float32, T * layer.top_k)
     _on_gpu(x=x, y=y, ws=ws)
     _check(_abi.lib().moe_decode_tokens(C.addressof(layer.struct), _ptr(x), T, flags, rs, _ptr(ws),
                                         ws.numel(), _ptr(y), _stream(stream)), "moe_decode_tokens")

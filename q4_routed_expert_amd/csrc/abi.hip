@@ -51,7 +51,7 @@ int check_mat(const moe_q4mat& m, const char* name) {
     return check_ptr(m.bias, buf);
 }
 
-int check_layer(const moe_layer* L) {
+int check_layer_sizes(const moe_layer* L) {
     if (!L) return fail(MOE_EINVAL, "layer is NULL");
     if (L->d <= 0 || L->inter <= 0 || L->n_experts <= 0 || L->top_k <= 0)
         return fail(MOE_EINVAL, "non-positive layer size (d=%d inter=%d E=%d k=%d)", L->d,
@@ -67,7 +67,12 @@ int check_layer(const moe_layer* L) {
     if (L->top_k > MOE_MAX_TOPK || L->top_k > L->n_experts)
         return fail(MOE_EUNSUPPORTED, "top_k=%d must be <= min(%d, n_experts=%d)", L->top_k,
                     MOE_MAX_TOPK, L->n_experts);
+    return MOE_OK;
+}
+
+int check_layer(const moe_layer* L) {
     int rc;
+    if ((rc = check_layer_sizes(L))) return rc;
     if ((rc = check_ptr(L->w_router, "w_router"))) return rc;
     if ((rc = check_ptr(L->router_bias, "router_bias", true))) return rc;
     if ((rc = check_mat(L->gate, "gate")) || (rc = check_mat(L->up, "up")) ||
@@ -209,6 +214,60 @@ int moe_route(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t flags,
                       "route sort");
 }
 
+int moe_route_scored(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t flags,
+                     const moe_router_spec* spec, const moe_routing* r, void* stream) {
+    int rc;
+    if ((rc = check_layer_sizes(L)) || (rc = check_tokens(T)) || (rc = check_routing(r))) return rc;
+    if (flags & ~MOE_LOGITS_IN) return fail(MOE_EINVAL, "unknown flags 0x%x", flags);
+    const bool logits_in = flags & MOE_LOGITS_IN;
+    if (!logits_in && ((rc = check_ptr(x, "x")) || (rc = check_ptr(L->w_router, "w_router")) ||
+                       (rc = check_ptr(L->router_bias, "router_bias", true))))
+        return rc;
+    if (!spec) return fail(MOE_EINVAL, "spec is NULL");
+    if ((rc = check_ptr(spec->balance, "spec.balance", true))) return rc;
+    if (spec->score != MOE_SCORE_SOFTMAX && spec->score != MOE_SCORE_SIGMOID)
+        return fail(MOE_EINVAL, "spec.score=%d", spec->score);
+    if (spec->renorm != 0 && spec->renorm != 1) return fail(MOE_EINVAL, "spec.renorm=%d", spec->renorm);
+    if (!(spec->scale > -3.4e38f && spec->scale < 3.4e38f))
+        return fail(MOE_EINVAL, "spec.scale must be finite");
+    const int G = spec->n_groups;
+    if (G < 1 || spec->top_groups < 1 || spec->top_groups > G)
+        return fail(MOE_EINVAL, "spec.n_groups=%d spec.top_groups=%d", G, spec->top_groups);
+    if (G > MOE_MAX_GROUPS || L->n_experts % G)
+        return fail(MOE_EUNSUPPORTED, "n_groups=%d must be <= %d and divide n_experts=%d", G,
+                    MOE_MAX_GROUPS, L->n_experts);
+    if (G > 1 && spec->group_top != 1 && spec->group_top != 2)
+        return fail(MOE_EUNSUPPORTED, "spec.group_top=%d must be 1 or 2", spec->group_top);
+    if (spec->top_groups * (L->n_experts / G) < L->top_k)
+        return fail(MOE_EUNSUPPORTED, "%d groups of %d experts hold fewer than top_k=%d",
+                    spec->top_groups, L->n_experts / G, L->top_k);
+    hipStream_t s = (hipStream_t)stream;
+    trace_begin(s);
+    if ((rc = hip_status(q4moe::launch_router_logits(logits_in ? nullptr : x, T, L->d, L->w_router,
+                                                     L->router_bias, L->n_experts, r->logits,
+                                                     r->blk_counts, s),
+                         "router logits")))
+        return rc;
+    q4moe::ScoreArgs a;
+    a.logits = r->logits;
+    a.balance = spec->balance;
+    a.T = T;
+    a.E = L->n_experts;
+    a.k = L->top_k;
+    a.n_groups = G;
+    a.top_groups = spec->top_groups;
+    a.group_top = spec->group_top;
+    a.sigmoid = spec->score == MOE_SCORE_SIGMOID;
+    a.renorm = spec->renorm != 0;
+    a.scale = spec->scale;
+    a.idx = r->topk_idx;
+    a.w = r->topk_w;
+    a.blk_counts = r->blk_counts;
+    if ((rc = hip_status(q4moe::launch_select(a, s), "select"))) return rc;
+    return hip_status(q4moe::launch_route_sort(r->topk_idx, T, L->top_k, L->n_experts, r, s),
+                      "route sort");
+}
+
 int moe_prefill(const moe_layer* L, const uint16_t* x, int32_t T, const moe_routing* r, void* ws,
                 size_t ws_bytes, uint16_t* y, void* stream) {
     return moe_prefill_ex(L, x, T, r, ws, ws_bytes, y, 0u, stream);
@@ -279,9 +338,14 @@ int check_decode(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t flag
     if (T < 1 || T > MOE_MAX_DECODE_TOKENS)
         return fail(MOE_EUNSUPPORTED, "decode takes 1..%d tokens, not T=%d", MOE_MAX_DECODE_TOKENS,
                     T);
-    if (flags & ~MOE_LOGITS_IN) return fail(MOE_EINVAL, "unknown flags 0x%x", flags);
-    const bool logits_in = flags & MOE_LOGITS_IN;
+    if (flags & ~(MOE_LOGITS_IN | MOE_ROUTING_IN))
+        return fail(MOE_EINVAL, "unknown flags 0x%x", flags);
+    const bool logits_in = flags & MOE_LOGITS_IN, routing_in = flags & MOE_ROUTING_IN;
     if ((rc = check_ptr(x, "x"))) return rc;
+    if (routing_in && logits_in)
+        return fail(MOE_EINVAL, "MOE_ROUTING_IN and MOE_LOGITS_IN exclude each other");
+    if (routing_in && (!r || !r->topk_idx || !r->topk_w))
+        return fail(MOE_EINVAL, "MOE_ROUTING_IN needs routing->topk_idx and topk_w");
     if (logits_in && (!r || !r->logits))
         return fail(MOE_EINVAL, "MOE_LOGITS_IN needs routing->logits");
     if (r) {
@@ -313,6 +377,7 @@ int decode_launch(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t fla
     a.sh_up = q4(L->sh_up);
     a.sh_down = q4(L->sh_down);
     a.logits_in = (flags & MOE_LOGITS_IN) != 0;
+    a.routing_in = (flags & MOE_ROUTING_IN) != 0;
     a.logits = (r && r->logits) ? r->logits : (float*)(base + dw.logits);
     a.out_idx = r ? r->topk_idx : nullptr;
     a.out_w = r ? r->topk_w : nullptr;

@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kRtThreads) void decode_router_shared_kernel(const 
         if (j < a.I) shared_gate_up_rows<NS>(a, s_x, t0, n_tok, j, lane);
         return;
     }
-    if (a.logits_in) return;  // uniform
+    if (a.logits_in || a.routing_in) return;  // uniform
     float* s_q = (float*)s_mem;                                     // [4 waves][NT][64]
     uint16_t* s_xr = (uint16_t*)(s_mem + 4 * NT * kRtExperts * 4);  // [NT][128]
     const int E = a.E, d = a.d;
@@ -304,7 +304,7 @@ __global__ __launch_bounds__(kRtThreads) void decode_router_shared_kernel(const 
 }
 
 // Token t's logits (partial sums added in order, + bias; or the given
-// logits), its top-k, then R x 16 gate/up rows of its routed slot s, for the
+// logits), its top-k (or the given selection), then R x 16 gate/up rows of its routed slot s, for the
 // assignment blockIdx.y = t * k + s (R grows with T so that the grid stays
 // about one work group per CU).  Work group (0, t * k) also writes token t's
 // logits, selection and scores for the down kernel and the caller.
@@ -318,7 +318,7 @@ __global__ __launch_bounds__(1024) void decode_topk_gate_up_kernel(const DecodeA
     const bool first = blockIdx.x == 0 && slot == 0;
     float* logits = a.logits + (size_t)t * E;
     stage_x(a, s_x, t, 1, tid, 1024);  // covered by the barrier after the logits
-    if (tid < E) {
+    if (!a.routing_in && tid < E) {
         float v;
         if (a.logits_in) {
             v = logits[tid];
@@ -389,15 +389,20 @@ __global__ __launch_bounds__(1024) void decode_topk_gate_up_kernel(const DecodeA
     if (wave == 0) {
         int se;
         float sw;
-        wave_topk(s_logits, E, k, lane, &se, &sw);
+        const size_t o = (size_t)t * k + (lane < k ? lane : 0);
+        if (a.routing_in) {
+            se = min(max(a.out_idx[o], 0), E - 1);
+            sw = a.out_w[o];
+        } else {
+            wave_topk(s_logits, E, k, lane, &se, &sw);
+        }
         if (lane < k) {
             s_sel[lane] = se;
             if (first) {
-                const size_t o = (size_t)t * k + lane;
                 a.sel_idx[o] = se;
                 a.sel_w[o] = sw;
-                if (a.out_idx) a.out_idx[o] = se;
-                if (a.out_w) a.out_w[o] = sw;
+                if (!a.routing_in && a.out_idx) a.out_idx[o] = se;
+                if (!a.routing_in && a.out_w) a.out_w[o] = sw;
             }
         }
     }

@@ -56,9 +56,10 @@ struct DecodeArgs {
     const float* router_bias;
     Q4 gate, up, down, sh_gate, sh_up, sh_down;
     bool logits_in;
+    bool routing_in;     // the selection is given in out_idx, out_w; no logits at all
     float* logits;       // [T][E]: written, or read when logits_in
-    int32_t* out_idx;    // [T][k] or NULL
-    float* out_w;        // [T][k] or NULL
+    int32_t* out_idx;    // [T][k] or NULL; read when routing_in
+    float* out_w;        // [T][k] or NULL; read when routing_in
     float* partial;      // [ceil(d/MOE_DECODE_ROUTER_ROWS)][T][E] router partial sums
     int32_t* sel_idx;    // [T][k]
     float* sel_w;        // [T][k]

@@ -21,4 +21,18 @@ struct NormArgs {
 };
 hipError_t launch_add_norm(const NormArgs& a, hipStream_t s);
 
+// Expert selection of moe_route_scored (the top-k step of routing).
+struct ScoreArgs {
+    const float* logits;      // [T][E]
+    const float* balance;     // [E] or NULL
+    int T, E, k;
+    int n_groups, top_groups, group_top;
+    bool sigmoid, renorm;
+    float scale;
+    int32_t* idx;             // [T][k]
+    float* w;                 // [T][k]
+    int32_t* blk_counts;      // [ceil(T/MOE_ROUTE_BLOCK)][E], cleared; counts are added
+};
+hipError_t launch_select(const ScoreArgs& a, hipStream_t s);
+
 }  // namespace q4moe

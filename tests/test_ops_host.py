@@ -51,3 +51,90 @@ def test_add_norm_binding_refuses():
         a.update(kw)
         with pytest.raises(ValueError, match=what):
             q4.add_norm(a.pop("x"), a.pop("weight"), **a)
+
+
+def _spec(**kw):
+    a = dict(score=0, n_groups=1, top_groups=1, group_top=1, renorm=1, scale=1.0, balance=None)
+    a.update(kw)
+    return _abi.RouterSpec(*[a[n] for n, _ in _abi.RouterSpec._fields_])
+
+
+def _layer(E=256, k=8, d=128, inter=64, w_router=FAKE):
+    return _abi.Layer(d, inter, E, k, w_router, None, *[_abi.Q4Mat() for _ in range(6)])
+
+
+def _route(spec, layer=None, T=4, x=FAKE, flags=0, missing=None):
+    L = layer or _layer()
+    r = _abi.Routing(*[FAKE] * len(_abi.Routing._fields_))
+    if missing:
+        setattr(r, missing, None)
+    return _abi.lib().moe_route_scored(C.addressof(L), x, T, flags,
+                                       None if spec is None else C.addressof(spec),
+                                       C.addressof(r), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(score=2), _abi.MOE_EINVAL), (dict(renorm=2), _abi.MOE_EINVAL),
+    (dict(scale=float("nan")), _abi.MOE_EINVAL), (dict(scale=float("inf")), _abi.MOE_EINVAL),
+    (dict(balance=FAKE + 4), _abi.MOE_EINVAL), (dict(n_groups=0), _abi.MOE_EINVAL),
+    (dict(n_groups=8, top_groups=0), _abi.MOE_EINVAL),
+    (dict(n_groups=8, top_groups=9), _abi.MOE_EINVAL),
+    (dict(n_groups=128, top_groups=128), _abi.MOE_EUNSUPPORTED),
+    (dict(n_groups=7, top_groups=7), _abi.MOE_EUNSUPPORTED),        # does not divide 256
+    (dict(n_groups=8, top_groups=4, group_top=3), _abi.MOE_EUNSUPPORTED),
+    (dict(n_groups=64, top_groups=1), _abi.MOE_EUNSUPPORTED),       # 4 experts, top-8
+])
+def test_route_scored_refuses_specs(kw, code):
+    assert _route(_spec(**kw)) == code
+    assert _abi.lib().moe_last_error()
+
+
+def test_route_scored_refuses_arguments():
+    s = _spec()
+    assert _route(None) == _abi.MOE_EINVAL
+    assert _route(s, T=0) == _abi.MOE_EINVAL
+    assert _route(s, T=_abi.MOE_MAX_TOKENS + 1) == _abi.MOE_EUNSUPPORTED
+    assert _route(s, flags=2) == _abi.MOE_EINVAL
+    assert _route(s, flags=_abi.MOE_ROUTING_IN) == _abi.MOE_EINVAL
+    assert _route(s, x=None) == _abi.MOE_EINVAL
+    assert _route(s, layer=_layer(w_router=None)) == _abi.MOE_EINVAL
+    assert _route(s, layer=_layer(E=257)) == _abi.MOE_EUNSUPPORTED
+    assert _route(s, missing="blk_counts") == _abi.MOE_EINVAL
+
+
+def test_decode_refuses_a_missing_selection():
+    lib = _abi.lib()
+    m = _abi.Q4Mat(FAKE, FAKE, FAKE)
+    L = _abi.Layer(128, 64, 8, 2, FAKE, None, *[m] * 6)
+    r = _abi.Routing(*[FAKE] * len(_abi.Routing._fields_))
+    call = lambda flags, rr: lib.moe_decode_tokens(  # noqa: E731
+        C.addressof(L), FAKE, 2, flags, rr, FAKE, 1 << 30, FAKE, None)
+    assert call(_abi.MOE_ROUTING_IN, None) == _abi.MOE_EINVAL
+    assert call(_abi.MOE_ROUTING_IN | _abi.MOE_LOGITS_IN, C.addressof(r)) == _abi.MOE_EINVAL
+    r.topk_w = None
+    assert call(_abi.MOE_ROUTING_IN, C.addressof(r)) == _abi.MOE_EINVAL
+    assert b"topk_w" in lib.moe_last_error()
+
+
+def test_route_scored_binding_refuses():
+    import types
+    L = types.SimpleNamespace(d=128, n_experts=8, top_k=2, inter=64, struct=None)
+    with pytest.raises(ValueError, match="score"):
+        q4.RouterSpec(score="tanh")
+    with pytest.raises(ValueError, match="balance"):
+        q4.RouterSpec(balance=torch.zeros(8, dtype=torch.float64))
+    with pytest.raises(ValueError, match="logits_in"):
+        q4.route_scored(L, None, q4.RouterSpec(), logits_in=True)
+    r = q4.DeviceRouting(4, 8, 3, "cpu")
+    with pytest.raises(ValueError, match="routing is for"):
+        q4.route_scored(L, None, q4.RouterSpec(), r, logits_in=True)
+    r = q4.DeviceRouting(4, 8, 2, "cpu")
+    with pytest.raises(ValueError, match="routing is for"):
+        q4.route_scored(L, torch.zeros(5, 128, dtype=bf16), q4.RouterSpec(), r)
+    with pytest.raises(ValueError, match="balance"):
+        q4.route_scored(L, None, q4.RouterSpec(balance=torch.zeros(7)), r, logits_in=True)
+    with pytest.raises(ValueError, match="GPU"):
+        q4.route_scored(L, None, q4.RouterSpec(), r, logits_in=True)
+    ws = torch.empty(16, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="routing_in"):
+        q4.decode_tokens(L, torch.zeros(2, 128, dtype=bf16), ws, routing_in=True)
