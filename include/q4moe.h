@@ -316,6 +316,21 @@ int moe_route_scored(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t 
    MOE_LOGITS_IN. */
 #define MOE_ROUTING_IN 32u
 
+/* Products of a few token rows with one 4-bit matrix, for the projections around
+   the layer and for an output head over several tokens:
+     y[t][n] = sum_k w(n, k) * x[t][k]      w = bf16(q * scale + bias), fp32 sums
+   for matrix 0 of m, N rows by K columns.  x: bf16 [T][K]; y: fp32 [T][N], or
+   bf16 (one rounding of the fp32 sum) with MOE_OUT_BF16.  Each weight is read
+   and dequantised once for all rows.  1 <= T <= MOE_MAX_LINEAR_TOKENS,
+   1 <= N <= MOE_MAX_VOCAB, K a multiple of 64, <= MOE_MAX_D.  y must not overlap
+   x or m.  A row's result does not depend on the other rows of x or on their
+   number: T rows at once give what T calls of one row give.  One kernel, no
+   workspace. */
+#define MOE_MAX_LINEAR_TOKENS 64
+#define MOE_OUT_BF16 1u
+int moe_linear(const moe_q4mat* m, int32_t N, int32_t K, const uint16_t* x, int32_t T,
+               uint32_t flags, void* y, void* stream);
+
 /* Residual addition and root-mean-square norm of T token rows, the step
    between two layers: with v = x + residual (fp32 sum, rounded once to the
    residual's type; v = x without a residual)
@@ -342,7 +357,7 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
                  uint16_t* y, uint8_t* y8, float* y8_scale, void* stream);
 
 /* Timing hook.  While `events` is non-NULL, every moe_route, moe_route_scored, moe_prefill,
-   moe_decode, moe_decode_tokens, moe_lm_argmax and moe_add_norm call made on this host thread records events[0] on its stream
+   moe_decode, moe_decode_tokens, moe_lm_argmax, moe_linear and moe_add_norm call made on this host thread records events[0] on its stream
    before its first kernel and events[i] right after its i-th kernel, for
    i < n (moe_route: router logits (with MOE_LOGITS_IN: the clearing of
    the histogram), top-k + histogram, scan + scatter + maps; moe_route_scored
@@ -352,7 +367,7 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
    partial sums + shared gate/up, logits + top-k + routed gate/up, down +
    combine; moe_lm_argmax: output head (with MOE_LOGITS_IN: the scan of the
    given logits), pick + embedding row).  The one-kernel calls record events[0]
-   and events[1]: moe_add_norm.  The
+   and events[1]: moe_linear, moe_add_norm.  The
    elapsed time between consecutive events is one kernel's duration.  events
    are hipEvent_t handles created and owned by the caller; pass NULL to stop. */
 void moe_trace_events(void* const* events, int32_t n);

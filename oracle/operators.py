@@ -66,3 +66,10 @@ def route_scored(logits, k: int, score="softmax", balance=None, n_groups=1, top_
             wt = wt / wt.sum() if wt.sum() > 0 else np.zeros(k)
         w[t] = wt * scale
     return idx, w
+
+
+def linear(q, scale, bias, x):
+    """x [T, K] (float64) times the transposed matrix of bf16 weights bf16(q * scale + bias)."""
+    from . import dequant
+    w = (dequant(q, scale, bias).astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+    return np.asarray(x, np.float64) @ w.T

@@ -23,6 +23,7 @@ from . import _abi
 
 MOE_LOGITS_IN = _abi.MOE_LOGITS_IN
 MAX_DECODE_TOKENS = _abi.MOE_MAX_DECODE_TOKENS
+MAX_LINEAR_TOKENS = _abi.MOE_MAX_LINEAR_TOKENS
 BLOCK_ROWS = _abi.MOE_BLOCK_ROWS
 TILE_ROWS = _abi.MOE_TILE_ROWS
 MATS = ("gate", "up", "down", "sh_gate", "sh_up", "sh_down")
@@ -371,6 +372,35 @@ def _launch_on(where: str, stream, **tensors):
     if stream.device != dev:
         raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {dev}")
     return stream.cuda_stream
+
+
+def linear(q: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor, x: torch.Tensor,
+           out_dtype: torch.dtype = torch.float32, y: torch.Tensor | None = None,
+           stream=None) -> torch.Tensor:
+    """y [T, N] = x [T, K] times the transposed Q4 matrix (q int32 [N, K/8], scale and
+    bias bf16 or their bits [N, K/64]), 1 <= T <= MAX_LINEAR_TOKENS; out_dtype fp32
+    or bf16."""
+    if x.dim() != 2 or q.dim() != 2:
+        raise ValueError(f"x must be [T, K] and q [N, K/8], not {tuple(x.shape)}, {tuple(q.shape)}")
+    T, K = x.shape
+    N = q.shape[0]
+    if q.shape[1] * 8 != K:
+        raise ValueError(f"q has {q.shape[1] * 8} columns, x has {K}")
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, not {out_dtype}")
+    if y is None:
+        y = torch.empty((T, N), dtype=out_dtype, device=x.device)
+    _need(x, "x", torch.bfloat16, T * K)
+    _need(q, "q", torch.int32, N * K // 8)
+    for name, t in (("scale", scale), ("bias", bias)):
+        _need(t, name, torch.int16 if t.dtype == torch.int16 else torch.bfloat16, N * (K // 64))
+    _need(y, "y", out_dtype, T * N)
+    s = _launch_on("linear", stream, q=q, scale=scale, bias=bias, x=x, y=y)
+    m = _abi.Q4Mat(_ptr(q), _ptr(scale), _ptr(bias))
+    _check(_abi.lib().moe_linear(C.addressof(m), N, K, _ptr(x), T,
+                                 _abi.MOE_OUT_BF16 if out_dtype == torch.bfloat16 else 0, _ptr(y),
+                                 s), "moe_linear")
+    return y
 
 
 def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,

@@ -13,6 +13,8 @@ MOE_NORM_PLUS_ONE, MOE_NORM_RESIDUAL_FLOAT = 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_ROUTING_IN = 32
 MOE_MAX_GROUPS = 64
+MOE_OUT_BF16 = 1
+MOE_MAX_LINEAR_TOKENS = 64
 MOE_BLOCK_ROWS = 32
 MOE_TILE_ROWS = 128
 MOE_ROUTE_BLOCK = 256
@@ -27,7 +29,7 @@ EXPORTS = ("moe_block_map_capacity", "moe_workspace_bytes", "moe_route", "moe_pr
            "moe_prefill_ex", "moe_trace_events",
            "moe_decode", "moe_decode_tokens", "moe_dequant", "moe_strerror", "moe_last_error",
            "moe_lm_workspace_bytes", "moe_lm_argmax", "moe_decode_tokens_static",
-           "moe_add_norm", "moe_route_scored")
+           "moe_add_norm", "moe_route_scored", "moe_linear")
 
 
 class Q4Mat(C.Structure):
@@ -91,10 +93,11 @@ def lib():
         L.moe_lm_workspace_bytes.restype = C.c_size_t
         L.moe_lm_argmax.argtypes = [vp, vp, C.c_uint32, vp, vp, vp, vp, C.c_size_t, vp]
         L.moe_route_scored.argtypes = [vp, vp, i32, C.c_uint32, vp, vp, vp]
+        L.moe_linear.argtypes = [vp, i32, i32, vp, i32, C.c_uint32, vp, vp]
         L.moe_add_norm.argtypes = [vp, i32, i32, vp, vp, vp, C.c_float, C.c_uint32, vp, vp, vp, vp]
         for f in ("moe_route", "moe_prefill", "moe_prefill_ex", "moe_decode", "moe_decode_tokens", "moe_dequant",
                   "moe_lm_argmax", "moe_decode_tokens_static", "moe_add_norm",
-                  "moe_route_scored"):
+                  "moe_route_scored", "moe_linear"):
             getattr(L, f).restype = C.c_int
         L.moe_trace_events.argtypes = [vp, i32]
         L.moe_trace_events.restype = None

@@ -509,6 +509,31 @@ int moe_lm_argmax(const moe_lm_head* lm, const uint16_t* x, uint32_t flags, floa
     return hip_status(q4moe::launch_lm_argmax(a, logits_in, (hipStream_t)stream), "lm argmax");
 }
 
+int moe_linear(const moe_q4mat* m, int32_t N, int32_t K, const uint16_t* x, int32_t T,
+               uint32_t flags, void* y, void* stream) {
+    int rc;
+    if (!m) return fail(MOE_EINVAL, "matrix is NULL");
+    if ((rc = check_mat(*m, "m")) || (rc = check_ptr(x, "x")) || (rc = check_ptr(y, "y"))) return rc;
+    if (N <= 0 || K <= 0 || T <= 0) return fail(MOE_EINVAL, "N=%d K=%d T=%d must be positive", N, K, T);
+    if (K % MOE_GROUP || K > MOE_MAX_D)
+        return fail(MOE_EUNSUPPORTED, "K=%d must be a multiple of %d and <= %d", K, MOE_GROUP,
+                    MOE_MAX_D);
+    if (N > MOE_MAX_VOCAB) return fail(MOE_EUNSUPPORTED, "N=%d > %d", N, MOE_MAX_VOCAB);
+    if (T > MOE_MAX_LINEAR_TOKENS)
+        return fail(MOE_EUNSUPPORTED, "T=%d > %d", T, MOE_MAX_LINEAR_TOKENS);
+    if (flags & ~MOE_OUT_BF16) return fail(MOE_EINVAL, "unknown flags 0x%x", flags);
+    q4moe::LinearArgs a;
+    a.w = q4(*m);
+    a.x = x;
+    a.y = y;
+    a.T = T;
+    a.N = N;
+    a.K = K;
+    a.out_bf16 = (flags & MOE_OUT_BF16) != 0;
+    trace_begin((hipStream_t)stream);
+    return hip_status(q4moe::launch_linear(a, (hipStream_t)stream), "linear");
+}
+
 int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
                  void* residual_out, const uint16_t* weight, float eps, uint32_t flags,
                  uint16_t* y, uint8_t* y8, float* y8_scale, void* stream) {

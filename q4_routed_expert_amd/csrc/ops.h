@@ -35,4 +35,14 @@ struct ScoreArgs {
 };
 hipError_t launch_select(const ScoreArgs& a, hipStream_t s);
 
+// y = W x for a few token rows (moe_linear).
+struct LinearArgs {
+    Q4 w;                     // [N][K]
+    const uint16_t* x;        // bf16 [T][K]
+    void* y;                  // fp32 or bf16 [T][N]
+    int T, N, K;
+    bool out_bf16;
+};
+hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
+
 }  // namespace q4moe

@@ -138,3 +138,41 @@ def test_route_scored_binding_refuses():
     ws = torch.empty(16, dtype=torch.uint8)
     with pytest.raises(ValueError, match="routing_in"):
         q4.decode_tokens(L, torch.zeros(2, 128, dtype=bf16), ws, routing_in=True)
+
+
+def _linear(**kw):
+    a = dict(q=FAKE, s=FAKE, b=FAKE, N=100, K=128, x=FAKE, T=4, flags=0, y=FAKE)
+    a.update(kw)
+    m = _abi.Q4Mat(a["q"], a["s"], a["b"])
+    return _abi.lib().moe_linear(C.addressof(m), a["N"], a["K"], a["x"], a["T"], a["flags"], a["y"],
+                                 None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(N=0), _abi.MOE_EINVAL), (dict(K=0), _abi.MOE_EINVAL), (dict(T=0), _abi.MOE_EINVAL),
+    (dict(K=100), _abi.MOE_EUNSUPPORTED), (dict(K=_abi.MOE_MAX_D + 64), _abi.MOE_EUNSUPPORTED),
+    (dict(N=_abi.MOE_MAX_VOCAB + 1), _abi.MOE_EUNSUPPORTED),
+    (dict(T=_abi.MOE_MAX_LINEAR_TOKENS + 1), _abi.MOE_EUNSUPPORTED),
+    (dict(flags=2), _abi.MOE_EINVAL), (dict(q=None), _abi.MOE_EINVAL),
+    (dict(s=FAKE + 2), _abi.MOE_EINVAL), (dict(b=None), _abi.MOE_EINVAL),
+    (dict(x=FAKE + 8), _abi.MOE_EINVAL), (dict(y=None), _abi.MOE_EINVAL),
+    (dict(y=FAKE + 4), _abi.MOE_EINVAL),
+])
+def test_linear_refuses(kw, code):
+    assert _linear(**kw) == code
+    assert _abi.lib().moe_last_error()
+
+
+def test_linear_binding_refuses():
+    q = torch.zeros(10, 16, dtype=i32)
+    s, x = torch.zeros(10, 2, dtype=bf16), torch.zeros(3, 128, dtype=bf16)
+    for kw, what in ((dict(x=x[0]), "x must be"), (dict(x=x[:, :64]), "columns"),
+                     (dict(x=x.float()), "x"), (dict(q=q.long()), "q"),
+                     (dict(scale=s[:5]), "scale"), (dict(bias=s.float()), "bias"),
+                     (dict(out_dtype=torch.float16), "out_dtype"),
+                     (dict(y=torch.zeros(29)), "y"), (dict(q=q.t().contiguous().t()), "q"),
+                     (dict(), "GPU")):
+        a = dict(q=q, scale=s, bias=s, x=x)
+        a.update(kw)
+        with pytest.raises(ValueError, match=what):
+            q4.linear(a.pop("q"), a.pop("scale"), a.pop("bias"), a.pop("x"), **a)
