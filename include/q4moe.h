@@ -316,6 +316,47 @@ int moe_route_scored(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t 
    MOE_LOGITS_IN. */
 #define MOE_ROUTING_IN 32u
 
+/* Sampling: one token for each of B rows of logits (fp32 [B][V], contiguous), from
+   one given uniform number a row.  Per row, with parameters from the per-row
+   arrays or, where an array is NULL, from the *_all value:
+     order      larger logit first, equal logits by the lower index
+     weights    w_i = exp((l_i - l_max) / temperature), a multiple of 2^-43;
+                NaN and -inf logits have weight 0 and are never drawn
+     top-k      keeps the first top_k tokens (top_k <= 0 or > V: all)
+     top-p      of those, the fewest first tokens whose weights reach top_p times
+                their sum, at least one (top_p >= 1 or NaN: all; <= 0: one)
+     min-p      of those, the tokens with w_i >= min_p (min_p <= 0 or NaN: all;
+                above 1 counts as 1)
+     token      the first kept token, in index order, at which the running sum of
+                the kept weights exceeds u times their sum
+     prob       its share of the kept weights (NULL: not stored)
+     x_next     bf16 row `token` of embed (NULL: not stored)
+   temperature <= 0 or NaN is greedy: top_k = 1, whatever the others say.  u is
+   taken into [0, 1).  A row without a live logit gives token 0 and prob 0.  The
+   result is a function of the row alone: it does not depend on B or on the other
+   rows, and equal calls give equal results.
+   Of lm only V, and with x_next also d and embed, are used.  logits and x_next
+   are 16-byte aligned, the other arrays 4-byte.  1 <= B <= MOE_MAX_SAMPLE_ROWS.
+   ws must hold moe_sample_workspace_bytes(V, B) bytes (no initialisation, not
+   preserved). */
+#define MOE_MAX_SAMPLE_ROWS 1024
+typedef struct {
+    const float* u;             /* [B] uniform numbers */
+    const float* temperature;   /* [B] or NULL */
+    const int32_t* top_k;       /* [B] or NULL */
+    const float* top_p;         /* [B] or NULL */
+    const float* min_p;         /* [B] or NULL */
+    float temperature_all;
+    int32_t top_k_all;
+    float top_p_all;
+    float min_p_all;
+} moe_sampling;
+/* Workspace bytes of moe_sample; 0 on invalid arguments. */
+size_t moe_sample_workspace_bytes(int32_t V, int32_t B);
+int moe_sample(const moe_lm_head* lm, const float* logits, int32_t B, const moe_sampling* p,
+               int32_t* token, float* prob, uint16_t* x_next, void* ws, size_t ws_bytes,
+               void* stream);
+
 /* Products of a few token rows with one 4-bit matrix, for the projections around
    the layer and for an output head over several tokens:
      y[t][n] = sum_k w(n, k) * x[t][k]      w = bf16(q * scale + bias), fp32 sums
@@ -357,7 +398,7 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
                  uint16_t* y, uint8_t* y8, float* y8_scale, void* stream);
 
 /* Timing hook.  While `events` is non-NULL, every moe_route, moe_route_scored, moe_prefill,
-   moe_decode, moe_decode_tokens, moe_lm_argmax, moe_linear and moe_add_norm call made on this host thread records events[0] on its stream
+   moe_decode, moe_decode_tokens, moe_lm_argmax, moe_sample, moe_linear and moe_add_norm call made on this host thread records events[0] on its stream
    before its first kernel and events[i] right after its i-th kernel, for
    i < n (moe_route: router logits (with MOE_LOGITS_IN: the clearing of
    the histogram), top-k + histogram, scan + scatter + maps; moe_route_scored

@@ -2,6 +2,9 @@
 definitions (numpy only; test infrastructure like the rest of this package)."""
 from __future__ import annotations
 
+import math
+from fractions import Fraction
+
 import numpy as np
 
 
@@ -73,3 +76,37 @@ def linear(q, scale, bias, x):
     from . import dequant
     w = (dequant(q, scale, bias).astype(np.uint32) << 16).view(np.float32).astype(np.float64)
     return np.asarray(x, np.float64) @ w.T
+
+
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """(token, prob) of one row, with weights in units of 2^-43 as exact integers; the
+    parameters are fp32 values."""
+    l = np.asarray(logits, np.float32).astype(np.float64)
+    u, temperature, top_p, min_p = (float(np.float32(v)) for v in (u, temperature, top_p, min_p))
+    V = l.size
+    greedy = not temperature > 0
+    t = 1.0 if greedy else float(temperature)
+    k = 1 if greedy else V if top_k <= 0 or top_k > V else int(top_k)
+    live = l > -np.inf
+    if not live.any():
+        return 0, 0.0
+    m = l[live].max()
+    w = np.zeros(V)
+    with np.errstate(invalid="ignore", over="ignore"):
+        w[live] = np.where(l[live] == m, 1.0, np.exp(-np.where(l[live] == m, 0.0, m - l[live]) / t))
+    w = np.where(np.isnan(w), 0.0, w)
+    w = np.floor(w * 2.0 ** 43 + 0.5).astype(np.uint64)
+    order = np.lexsort((np.arange(V), -np.where(live, l, -np.inf)))
+    order = order[w[order] > 0][:k]
+    if not greedy and top_p < 1:
+        cum = np.cumsum(w[order])
+        need = max(1, math.ceil(Fraction(max(float(top_p), 0.0)) * int(cum[-1])))
+        order = order[:int(np.searchsorted(cum, np.uint64(int(need)), side="left")) + 1]
+    if min_p > 0:
+        order = order[w[order] >= np.ceil(min(float(min_p), 1.0) * 2.0 ** 43)]
+    kept = np.sort(order)
+    cum = np.cumsum(w[kept])
+    total = int(cum[-1])
+    draw = min(int(Fraction(max(float(u), 0.0)) * total), total - 1)
+    at = int(np.searchsorted(cum, np.uint64(draw), side="right"))
+    return int(kept[at]), int(w[kept[at]]) / total

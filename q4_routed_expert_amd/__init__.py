@@ -374,6 +374,61 @@ def _launch_on(where: str, stream, **tensors):
     return stream.cuda_stream
 
 
+def sample_workspace(B: int, V: int, device="cuda") -> torch.Tensor:
+    """A workspace for sample: B rows of V logits."""
+    n = _abi.lib().moe_sample_workspace_bytes(V, B)
+    if n == 0:
+        raise MoEError(_abi.MOE_EINVAL, "moe_sample_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+           lm: DeviceLmHead | None = None, token: torch.Tensor | None = None,
+           prob: torch.Tensor | None = None, x_next: torch.Tensor | None = None,
+           ws: torch.Tensor | None = None, stream=None):
+    """One token for each row of logits [B, V] (fp32) from uniform numbers u [B] (fp32):
+    (token int32 [B], prob fp32 [B], x_next or None).  temperature (0: greedy), top_k
+    (0: off), top_p (1: off) and min_p (0: off) are numbers for all rows or tensors [B]
+    on the GPU (fp32; top_k int32).  x_next [B, d] needs lm, whose embedding rows it
+    gets.  ws: sample_workspace(B, V) or larger."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [B, V], not {tuple(logits.shape)}")
+    B, V = logits.shape
+    _need(logits, "logits", torch.float32, B * V)
+    _need(u, "u", torch.float32, B)
+    p = _abi.Sampling(_ptr(u))
+    rows = {"u": u}
+    for name, v, dt in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if isinstance(v, torch.Tensor):
+            _need(v, name, dt, B)
+            rows[name] = v
+            setattr(p, name, v.data_ptr())
+        else:
+            setattr(p, name + "_all", v)
+    if token is None:
+        token = torch.empty(B, dtype=torch.int32, device=logits.device)
+    if prob is None:
+        prob = torch.empty(B, dtype=torch.float32, device=logits.device)
+    _need(token, "token", torch.int32, B)
+    _need(prob, "prob", torch.float32, B)
+    if x_next is not None:
+        if lm is None or lm.V != V or lm.embed is None:
+            raise ValueError(f"x_next needs an lm head of V={V} with an embedding table")
+        _need(x_next, "x_next", torch.bfloat16, B * lm.d)
+        head = lm.struct
+    else:
+        head = _abi.LmHead(V)
+    if ws is None:
+        ws = sample_workspace(B, V, logits.device)
+    _need(ws, "ws", torch.uint8, 1)
+    s = _launch_on("sample", stream, logits=logits, token=token, prob=prob, x_next=x_next, ws=ws,
+                   **rows)
+    _check(_abi.lib().moe_sample(C.addressof(head), _ptr(logits), B, C.addressof(p), _ptr(token),
+                                 _ptr(prob), _ptr(x_next), _ptr(ws), ws.numel(), s), "moe_sample")
+    return token, prob, x_next
+
+
 def linear(q: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor, x: torch.Tensor,
            out_dtype: torch.dtype = torch.float32, y: torch.Tensor | None = None,
            stream=None) -> torch.Tensor:

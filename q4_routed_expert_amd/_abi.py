@@ -15,6 +15,7 @@ MOE_ROUTING_IN = 32
 MOE_MAX_GROUPS = 64
 MOE_OUT_BF16 = 1
 MOE_MAX_LINEAR_TOKENS = 64
+MOE_MAX_SAMPLE_ROWS = 1024
 MOE_BLOCK_ROWS = 32
 MOE_TILE_ROWS = 128
 MOE_ROUTE_BLOCK = 256
@@ -29,7 +30,8 @@ EXPORTS = ("moe_block_map_capacity", "moe_workspace_bytes", "moe_route", "moe_pr
            "moe_prefill_ex", "moe_trace_events",
            "moe_decode", "moe_decode_tokens", "moe_dequant", "moe_strerror", "moe_last_error",
            "moe_lm_workspace_bytes", "moe_lm_argmax", "moe_decode_tokens_static",
-           "moe_add_norm", "moe_route_scored", "moe_linear")
+           "moe_add_norm", "moe_route_scored", "moe_linear",
+           "moe_sample_workspace_bytes", "moe_sample")
 
 
 class Q4Mat(C.Structure):
@@ -51,6 +53,12 @@ class RouterSpec(C.Structure):
     _fields_ = [("score", C.c_int32), ("n_groups", C.c_int32), ("top_groups", C.c_int32),
                 ("group_top", C.c_int32), ("renorm", C.c_int32), ("scale", C.c_float),
                 ("balance", C.c_void_p)]
+
+
+class Sampling(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("u", "temperature", "top_k", "top_p", "min_p")] + [
+        ("temperature_all", C.c_float), ("top_k_all", C.c_int32), ("top_p_all", C.c_float),
+        ("min_p_all", C.c_float)]
 
 
 class Routing(C.Structure):
@@ -94,10 +102,13 @@ def lib():
         L.moe_lm_argmax.argtypes = [vp, vp, C.c_uint32, vp, vp, vp, vp, C.c_size_t, vp]
         L.moe_route_scored.argtypes = [vp, vp, i32, C.c_uint32, vp, vp, vp]
         L.moe_linear.argtypes = [vp, i32, i32, vp, i32, C.c_uint32, vp, vp]
+        L.moe_sample_workspace_bytes.argtypes = [i32, i32]
+        L.moe_sample_workspace_bytes.restype = C.c_size_t
+        L.moe_sample.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, C.c_size_t, vp]
         L.moe_add_norm.argtypes = [vp, i32, i32, vp, vp, vp, C.c_float, C.c_uint32, vp, vp, vp, vp]
         for f in ("moe_route", "moe_prefill", "moe_prefill_ex", "moe_decode", "moe_decode_tokens", "moe_dequant",
                   "moe_lm_argmax", "moe_decode_tokens_static", "moe_add_norm",
-                  "moe_route_scored", "moe_linear"):
+                  "moe_route_scored", "moe_linear", "moe_sample"):
             getattr(L, f).restype = C.c_int
         L.moe_trace_events.argtypes = [vp, i32]
         L.moe_trace_events.restype = None

@@ -159,6 +159,43 @@ int check_lm(const moe_lm_head* lm) {
 // Hand-off workspace: per-work-group best (logit, row) pairs.
 size_t lm_part_bytes(int32_t V) { return align256(8 * (size_t)q4moe::lm_partials(V, false)); }
 
+// Sampling workspace of B rows of V logits.
+struct SampleWs {
+    size_t part_max, chunk_w, hist_n, hist_w, list_p, list_w, list_n, state, total;
+    int chunk, n_chunks;
+};
+SampleWs sample_ws(int32_t V, int32_t B) {
+    SampleWs w;
+    w.chunk = q4moe::sample_chunk(V, B);
+    w.n_chunks = (V + w.chunk - 1) / w.chunk;
+    const size_t rows = (size_t)B, parts = rows * (size_t)w.n_chunks;
+    size_t o = 0;
+    w.part_max = o; o += align256(sizeof(float) * parts);
+    w.chunk_w = o; o += align256(sizeof(uint64_t) * parts);
+    w.hist_n = o; o += align256(sizeof(uint32_t) * rows * q4moe::kSampleBins);
+    w.hist_w = o; o += align256(sizeof(uint64_t) * rows * q4moe::kSampleBins);
+    w.list_p = o; o += align256(sizeof(uint64_t) * rows * q4moe::kSampleList);
+    w.list_w = o; o += align256(sizeof(uint64_t) * rows * q4moe::kSampleList);
+    w.list_n = o; o += align256(sizeof(uint32_t) * rows);
+    w.state = o; o += align256(sizeof(q4moe::SampleState) * rows);
+    w.total = o;
+    return w;
+}
+
+int check_sample_sizes(int32_t V, int32_t B) {
+    if (V <= 0 || B <= 0) return fail(MOE_EINVAL, "V=%d and B=%d must be positive", V, B);
+    if (V > MOE_MAX_VOCAB) return fail(MOE_EUNSUPPORTED, "V=%d > %d", V, MOE_MAX_VOCAB);
+    if (B > MOE_MAX_SAMPLE_ROWS) return fail(MOE_EUNSUPPORTED, "B=%d > %d", B, MOE_MAX_SAMPLE_ROWS);
+    return MOE_OK;
+}
+
+// A per-row array: only 4-byte alignment is asked for.
+int check_row_array(const void* p, const char* what, bool allow_null) {
+    if (!p) return allow_null ? MOE_OK : fail(MOE_EINVAL, "%s is NULL", what);
+    if ((uintptr_t)p & 3u) return fail(MOE_EINVAL, "%s is not 4-byte aligned", what);
+    return MOE_OK;
+}
+
 int hip_status(hipError_t e, const char* what) {
     if (e != hipSuccess) return fail(MOE_EHIP, "%s: %s", what, hipGetErrorString(e));
     return MOE_OK;
@@ -507,6 +544,65 @@ int moe_lm_argmax(const moe_lm_head* lm, const uint16_t* x, uint32_t flags, floa
     a.part = (int2*)base;
     trace_begin((hipStream_t)stream);
     return hip_status(q4moe::launch_lm_argmax(a, logits_in, (hipStream_t)stream), "lm argmax");
+}
+
+size_t moe_sample_workspace_bytes(int32_t V, int32_t B) {
+    if (check_sample_sizes(V, B)) return 0;
+    return sample_ws(V, B).total;
+}
+
+int moe_sample(const moe_lm_head* lm, const float* logits, int32_t B, const moe_sampling* p,
+               int32_t* token, float* prob, uint16_t* x_next, void* ws, size_t ws_bytes,
+               void* stream) {
+    int rc;
+    if (!lm) return fail(MOE_EINVAL, "lm head is NULL");
+    if (!p) return fail(MOE_EINVAL, "sampling is NULL");
+    if ((rc = check_sample_sizes(lm->V, B)) || (rc = check_ptr(logits, "logits")) ||
+        (rc = check_row_array(p->u, "u", false)) ||
+        (rc = check_row_array(p->temperature, "temperature", true)) ||
+        (rc = check_row_array(p->top_k, "top_k", true)) ||
+        (rc = check_row_array(p->top_p, "top_p", true)) ||
+        (rc = check_row_array(p->min_p, "min_p", true)) ||
+        (rc = check_row_array(token, "token", false)) ||
+        (rc = check_row_array(prob, "prob", true)) || (rc = check_ptr(ws, "workspace")))
+        return rc;
+    if (x_next && ((rc = check_lm(lm)) || (rc = check_ptr(x_next, "x_next")) ||
+                   (rc = check_mat(lm->embed, "embed"))))
+        return rc;
+    const SampleWs w = sample_ws(lm->V, B);
+    if (ws_bytes < w.total)
+        return fail(MOE_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, w.total);
+    unsigned char* base = (unsigned char*)ws;
+    q4moe::SampleArgs a;
+    a.logits = logits;
+    a.B = B;
+    a.V = lm->V;
+    a.d = lm->d;
+    a.chunk = w.chunk;
+    a.n_chunks = w.n_chunks;
+    a.temperature = p->temperature;
+    a.top_k = p->top_k;
+    a.top_p = p->top_p;
+    a.min_p = p->min_p;
+    a.temperature_all = p->temperature_all;
+    a.top_k_all = p->top_k_all;
+    a.top_p_all = p->top_p_all;
+    a.min_p_all = p->min_p_all;
+    a.u = p->u;
+    a.token = token;
+    a.prob = prob;
+    a.x_next = x_next;
+    a.embed = q4(lm->embed);
+    a.part_max = (float*)(base + w.part_max);
+    a.chunk_w = (uint64_t*)(base + w.chunk_w);
+    a.hist_n = (uint32_t*)(base + w.hist_n);
+    a.hist_w = (uint64_t*)(base + w.hist_w);
+    a.list_p = (uint64_t*)(base + w.list_p);
+    a.list_w = (uint64_t*)(base + w.list_w);
+    a.list_n = (uint32_t*)(base + w.list_n);
+    a.state = (q4moe::SampleState*)(base + w.state);
+    trace_begin((hipStream_t)stream);
+    return hip_status(q4moe::launch_sample(a, (hipStream_t)stream), "sample");
 }
 
 int moe_linear(const moe_q4mat* m, int32_t N, int32_t K, const uint16_t* x, int32_t T,

@@ -176,3 +176,62 @@ def test_linear_binding_refuses():
         a.update(kw)
         with pytest.raises(ValueError, match=what):
             q4.linear(a.pop("q"), a.pop("scale"), a.pop("bias"), a.pop("x"), **a)
+
+
+def _sample(V=100, B=4, d=0, logits=FAKE, token=FAKE, prob=None, x_next=None, ws=FAKE,
+            ws_bytes=1 << 30, embed=None, **kw):
+    lm = _abi.LmHead(V, d, _abi.Q4Mat(), embed or _abi.Q4Mat())
+    p = _abi.Sampling(u=kw.pop("u", FAKE), **kw)
+    return _abi.lib().moe_sample(C.addressof(lm), logits, B, C.addressof(p), token, prob, x_next, ws,
+                                 ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(V=0), _abi.MOE_EINVAL), (dict(B=0), _abi.MOE_EINVAL),
+    (dict(V=_abi.MOE_MAX_VOCAB + 1), _abi.MOE_EUNSUPPORTED),
+    (dict(B=_abi.MOE_MAX_SAMPLE_ROWS + 1), _abi.MOE_EUNSUPPORTED),
+    (dict(logits=None), _abi.MOE_EINVAL), (dict(logits=FAKE + 4), _abi.MOE_EINVAL),
+    (dict(u=None), _abi.MOE_EINVAL), (dict(u=FAKE + 2), _abi.MOE_EINVAL),
+    (dict(temperature=FAKE + 1), _abi.MOE_EINVAL), (dict(top_k=FAKE + 2), _abi.MOE_EINVAL),
+    (dict(top_p=FAKE + 2), _abi.MOE_EINVAL), (dict(min_p=FAKE + 3), _abi.MOE_EINVAL),
+    (dict(token=None), _abi.MOE_EINVAL), (dict(token=FAKE + 2), _abi.MOE_EINVAL),
+    (dict(prob=FAKE + 2), _abi.MOE_EINVAL), (dict(ws=None), _abi.MOE_EINVAL),
+    (dict(ws_bytes=1000), _abi.MOE_EWORKSPACE),
+    (dict(x_next=FAKE), _abi.MOE_EINVAL),                                    # d = 0
+    (dict(x_next=FAKE, d=100), _abi.MOE_EUNSUPPORTED),
+    (dict(x_next=FAKE, d=128), _abi.MOE_EINVAL),                             # no table
+    (dict(x_next=FAKE + 8, d=128, embed=_abi.Q4Mat(FAKE, FAKE, FAKE)), _abi.MOE_EINVAL),
+    # 4-byte aligned arrays are enough: these get as far as the workspace
+    (dict(u=FAKE + 4, token=FAKE + 4, prob=FAKE + 12, top_k=FAKE + 8, ws_bytes=0),
+     _abi.MOE_EWORKSPACE),
+])
+def test_sample_refuses(kw, code):
+    assert _sample(**kw) == code
+    assert _abi.lib().moe_last_error()
+
+
+def test_sample_workspace_bytes():
+    lib = _abi.lib()
+    for V, B in ((1, 1), (248320, 64), (_abi.MOE_MAX_VOCAB, _abi.MOE_MAX_SAMPLE_ROWS)):
+        assert lib.moe_sample_workspace_bytes(V, B) > 0
+    for V, B in ((0, 1), (1, 0), (_abi.MOE_MAX_VOCAB + 1, 1), (10, _abi.MOE_MAX_SAMPLE_ROWS + 1)):
+        assert lib.moe_sample_workspace_bytes(V, B) == 0
+
+
+def test_sample_binding_refuses():
+    import types
+    l, u = torch.zeros(3, 50), torch.zeros(3)
+    lm = types.SimpleNamespace(V=50, d=128, embed={}, struct=None)
+    for kw, what in ((dict(logits=l[0]), "logits"), (dict(logits=l.double()), "logits"),
+                     (dict(logits=l.t()), "logits"), (dict(u=u[:2]), "u"), (dict(u=u.double()), "u"),
+                     (dict(temperature=u[:1]), "temperature"), (dict(top_k=u), "top_k"),
+                     (dict(top_p=u.half()), "top_p"), (dict(min_p=u.int()), "min_p"),
+                     (dict(token=u), "token"), (dict(prob=u.double()), "prob"),
+                     (dict(x_next=torch.zeros(3, 128, dtype=bf16)), "x_next"),
+                     (dict(x_next=torch.zeros(2, 128, dtype=bf16), lm=lm), "x_next"),
+                     (dict(ws=u), "ws"),
+                     (dict(ws=torch.empty(10, dtype=torch.uint8)), "GPU")):
+        a = dict(logits=l, u=u)
+        a.update(kw)
+        with pytest.raises(ValueError, match=what):
+            q4.sample(a.pop("logits"), a.pop("u"), **a)
