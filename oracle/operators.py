@@ -93,8 +93,8 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     m = l[live].max()
     w = np.zeros(V)
     with np.errstate(invalid="ignore", over="ignore"):
-        w[live] = np.where(l[live] == m, 1.0, np.exp(-np.where(l[live] == m, 0.0, m - l[live]) / t))
-    w = np.where(np.isnan(w), 0.0, w)
+        x = np.where(l[live] == m, 0.0, (m - l[live]) / t)
+    w[live] = np.where(x < 30.4, np.exp(-x), 0.0)  # (NaN, infinity / infinity, has no weight)
     w = np.floor(w * 2.0 ** 43 + 0.5).astype(np.uint64)
     order = np.lexsort((np.arange(V), -np.where(live, l, -np.inf)))
     order = order[w[order] > 0][:k]

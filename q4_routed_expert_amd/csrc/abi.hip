@@ -161,21 +161,19 @@ size_t lm_part_bytes(int32_t V) { return align256(8 * (size_t)q4moe::lm_partials
 
 // Sampling workspace of B rows of V logits.
 struct SampleWs {
-    size_t part_max, chunk_w, hist_n, hist_w, list_p, list_w, list_n, state, total;
-    int chunk, n_chunks;
+    size_t part_max, chunk_w, hist, list, list_n, state, total;
+    int chunk_sh, n_chunks;
 };
 SampleWs sample_ws(int32_t V, int32_t B) {
     SampleWs w;
-    w.chunk = q4moe::sample_chunk(V, B);
-    w.n_chunks = (V + w.chunk - 1) / w.chunk;
+    w.chunk_sh = q4moe::sample_chunk_sh(V, B);
+    w.n_chunks = (V + (1 << w.chunk_sh) - 1) >> w.chunk_sh;
     const size_t rows = (size_t)B, parts = rows * (size_t)w.n_chunks;
     size_t o = 0;
     w.part_max = o; o += align256(sizeof(float) * parts);
     w.chunk_w = o; o += align256(sizeof(uint64_t) * parts);
-    w.hist_n = o; o += align256(sizeof(uint32_t) * rows * q4moe::kSampleBins);
-    w.hist_w = o; o += align256(sizeof(uint64_t) * rows * q4moe::kSampleBins);
-    w.list_p = o; o += align256(sizeof(uint64_t) * rows * q4moe::kSampleList);
-    w.list_w = o; o += align256(sizeof(uint64_t) * rows * q4moe::kSampleList);
+    w.hist = o; o += align256(sizeof(uint64_t) * rows * q4moe::kSampleBins);
+    w.list = o; o += align256(sizeof(uint64_t) * rows * q4moe::kSampleList);
     w.list_n = o; o += align256(sizeof(uint32_t) * rows);
     w.state = o; o += align256(sizeof(q4moe::SampleState) * rows);
     w.total = o;
@@ -578,7 +576,7 @@ int moe_sample(const moe_lm_head* lm, const float* logits, int32_t B, const moe_
     a.B = B;
     a.V = lm->V;
     a.d = lm->d;
-    a.chunk = w.chunk;
+    a.chunk_sh = w.chunk_sh;
     a.n_chunks = w.n_chunks;
     a.temperature = p->temperature;
     a.top_k = p->top_k;
@@ -595,10 +593,8 @@ int moe_sample(const moe_lm_head* lm, const float* logits, int32_t B, const moe_
     a.embed = q4(lm->embed);
     a.part_max = (float*)(base + w.part_max);
     a.chunk_w = (uint64_t*)(base + w.chunk_w);
-    a.hist_n = (uint32_t*)(base + w.hist_n);
-    a.hist_w = (uint64_t*)(base + w.hist_w);
-    a.list_p = (uint64_t*)(base + w.list_p);
-    a.list_w = (uint64_t*)(base + w.list_w);
+    a.hist = (uint64_t*)(base + w.hist);
+    a.list = (uint64_t*)(base + w.list);
     a.list_n = (uint32_t*)(base + w.list_n);
     a.state = (q4moe::SampleState*)(base + w.state);
     trace_begin((hipStream_t)stream);

@@ -49,18 +49,17 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 constexpr int kSampleBins = 2048;       // histogram bins of a row
 constexpr int kSampleList = 4096;       // tokens a row's list holds
 constexpr int kSampleMaxChunks = 512;   // chunks of a row
+constexpr int kSampleRowMax = 16384;    // rows up to here take the one-kernel form
 struct SampleState {     // what a row's histogram says about its cut
-    uint64_t total;      // mass of all tokens
-    uint64_t base_w;     // count and mass before the listed bins
-    uint32_t base_n;
-    uint32_t n;          // tokens in the listed bins lo .. hi (lo = kSampleBins: no cut)
-    int32_t lo, hi;
-    int32_t k_on;        // top-k cuts inside the listed bins
+    uint64_t total;      // sum of the histogram (its mass, or with top-k its count)
+    uint64_t before;     // mass before the listed bins
+    int32_t lo, hi;      // the listed bins
+    int32_t reached;     // the target lies in bin hi
     int32_t pad;
 };
 struct SampleArgs {
     const float* logits;      // [B][V]
-    int B, V, d, chunk, n_chunks;
+    int B, V, d, chunk_sh, n_chunks;
     const float* temperature; // [B] or NULL (then temperature_all), and so on
     const int32_t* top_k;
     const float* top_p;
@@ -73,17 +72,15 @@ struct SampleArgs {
     float* prob;              // [B] or NULL
     uint16_t* x_next;         // bf16 [B][d] or NULL
     Q4 embed;                 // [V][d]
-    // workspace
+    // workspace (unused by short rows)
     float* part_max;          // [B][n_chunks]
     uint64_t* chunk_w;        // [B][n_chunks]
-    uint32_t* hist_n;         // [B][kSampleBins]
-    uint64_t* hist_w;         // [B][kSampleBins]
-    uint64_t* list_p;         // [B][kSampleList]
-    uint64_t* list_w;         // [B][kSampleList]
+    uint64_t* hist;           // [B][kSampleBins]
+    uint64_t* list;           // [B][kSampleList]
     uint32_t* list_n;         // [B]
     SampleState* state;       // [B]
 };
-int sample_chunk(int V, int B);  // logits per chunk
+int sample_chunk_sh(int V, int B);  // log2 of the logits per chunk
 hipError_t launch_sample(const SampleArgs& a, hipStream_t s);
 
 }  // namespace q4moe
