@@ -320,8 +320,9 @@ int moe_route_scored(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t 
    one given uniform number a row.  Per row, with parameters from the per-row
    arrays or, where an array is NULL, from the *_all value:
      order      larger logit first, equal logits by the lower index
-     weights    w_i = exp((l_i - l_max) / temperature), a multiple of 2^-43;
-                NaN and -inf logits have weight 0 and are never drawn
+     weights    w_i = exp((l_i - l_max) / temperature), a multiple of 2^-43 (below
+                exp(-30.4): 0); +inf logits weigh as the largest finite value, NaN
+                and -inf logits have weight 0 and are never drawn
      top-k      keeps the first top_k tokens (top_k <= 0 or > V: all)
      top-p      of those, the fewest first tokens whose weights reach top_p times
                 their sum, at least one (top_p >= 1 or NaN: all; <= 0: one)

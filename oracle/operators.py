@@ -90,11 +90,12 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     live = l > -np.inf
     if not live.any():
         return 0, 0.0
-    m = l[live].max()
+    big = float(np.finfo(np.float32).max)
+    m = min(l[live].max(), big)
     w = np.zeros(V)
     with np.errstate(invalid="ignore", over="ignore"):
-        x = np.where(l[live] == m, 0.0, (m - l[live]) / t)
-    w[live] = np.where(x < 30.4, np.exp(-x), 0.0)  # (NaN, infinity / infinity, has no weight)
+        x = (m - np.minimum(l[live], big)) / t
+    w[live] = np.where(x < 30.4, np.exp(-x), 0.0)
     w = np.floor(w * 2.0 ** 43 + 0.5).astype(np.uint64)
     order = np.lexsort((np.arange(V), -np.where(live, l, -np.inf)))
     order = order[w[order] > 0][:k]

@@ -161,7 +161,7 @@ size_t lm_part_bytes(int32_t V) { return align256(8 * (size_t)q4moe::lm_partials
 
 // Sampling workspace of B rows of V logits.
 struct SampleWs {
-    size_t part_max, chunk_w, hist, list, list_n, state, total;
+    size_t part_max, chunk_w, hist, list, list_n, state, row, total;
     int chunk_sh, n_chunks;
 };
 SampleWs sample_ws(int32_t V, int32_t B) {
@@ -176,6 +176,7 @@ SampleWs sample_ws(int32_t V, int32_t B) {
     w.list = o; o += align256(sizeof(uint64_t) * rows * q4moe::kSampleList);
     w.list_n = o; o += align256(sizeof(uint32_t) * rows);
     w.state = o; o += align256(sizeof(q4moe::SampleState) * rows);
+    w.row = o; o += align256(sizeof(q4moe::SampleRow) * rows);
     w.total = o;
     return w;
 }
@@ -597,6 +598,7 @@ int moe_sample(const moe_lm_head* lm, const float* logits, int32_t B, const moe_
     a.list = (uint64_t*)(base + w.list);
     a.list_n = (uint32_t*)(base + w.list_n);
     a.state = (q4moe::SampleState*)(base + w.state);
+    a.row = (q4moe::SampleRow*)(base + w.row);
     trace_begin((hipStream_t)stream);
     return hip_status(q4moe::launch_sample(a, (hipStream_t)stream), "sample");
 }

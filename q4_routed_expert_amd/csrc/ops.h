@@ -57,6 +57,14 @@ struct SampleState {     // what a row's histogram says about its cut
     int32_t reached;     // the target lies in bin hi
     int32_t pad;
 };
+struct SampleRow {       // one row's parameters
+    double inv_t;        // 1 / temperature
+    double p;            // top-p
+    uint64_t w_min;      // min-p: the smallest kept weight, >= 1
+    uint32_t k;          // tokens top-k keeps, 1 .. V
+    float u;
+    int32_t cut_k, cut_p;  // top-k / top-p are on
+};
 struct SampleArgs {
     const float* logits;      // [B][V]
     int B, V, d, chunk_sh, n_chunks;
@@ -79,6 +87,7 @@ struct SampleArgs {
     uint64_t* list;           // [B][kSampleList]
     uint32_t* list_n;         // [B]
     SampleState* state;       // [B]
+    SampleRow* row;           // [B]
 };
 int sample_chunk_sh(int V, int B);  // log2 of the logits per chunk
 hipError_t launch_sample(const SampleArgs& a, hipStream_t s);

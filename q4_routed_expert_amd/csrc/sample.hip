@@ -27,14 +27,16 @@
 // narrows over the whole row instead.
 // Short rows (sample_row_kernel): one work group does all of it with the row in its
 // registers.
+#include <float.h>
+
 #include "ops.h"
 
 namespace q4moe {
 namespace {
 
 constexpr int kThreads = 256;       // of kernels 1 to 3
-constexpr int kPickThreads = 1024;  // of kernel 4 and of the short rows' kernel
-constexpr int kPickWaves = kPickThreads / 64;
+constexpr int kPickThreads = 512;   // of kernel 4
+constexpr int kRowThreads = 1024;   // of the short rows' kernel, at most
 constexpr int kBins = kSampleBins;
 constexpr int kList = kSampleList;
 constexpr int kRank = 256;          // tokens ranked against each other at once
@@ -43,29 +45,22 @@ constexpr int kIdxBits = 20;        // MOE_MAX_VOCAB = 2^20
 constexpr double kOne = 8796093022208.0;  // 2^43: the weight of the largest logit
 constexpr double kRange = 30.4;           // beyond this depth a weight is 0
 
-// One row's parameters.
-struct Row {
-    double inv_t;      // 1 / temperature
-    uint32_t k;        // tokens top-k keeps, 1 .. V
-    bool cut_k, cut_p; // top-k / top-p are on
-    double p;
-    uint64_t w_min;    // min-p: the smallest kept weight, >= 1
-};
-
-__device__ __forceinline__ float param(const float* a, float all, int b) { return a ? a[b] : all; }
-
-__device__ __forceinline__ Row row_params(const SampleArgs& a, int b) {
-    Row r;
-    const float t = param(a.temperature, a.temperature_all, b);
+// One row's parameters from the caller's arrays.
+__device__ __forceinline__ SampleRow row_params(const SampleArgs& a, int b) {
+    float t = a.temperature_all, p = a.top_p_all, mp = a.min_p_all;
+    int k = a.top_k_all;
+    if (a.temperature) t = a.temperature[b];  // all the loads before any use
+    if (a.top_k) k = a.top_k[b];
+    if (a.top_p) p = a.top_p[b];
+    if (a.min_p) mp = a.min_p[b];
+    SampleRow r;
+    r.u = a.u[b];
     const bool greedy = !(t > 0.0f);
     r.inv_t = greedy ? 1.0 : 1.0 / (double)t;
-    const int k = a.top_k ? a.top_k[b] : a.top_k_all;
     r.k = greedy ? 1u : (k <= 0 || k > a.V) ? (uint32_t)a.V : (uint32_t)k;
     r.cut_k = r.k < (uint32_t)a.V;
-    const float p = param(a.top_p, a.top_p_all, b);
     r.cut_p = p < 1.0f && !greedy;
     r.p = p > 0.0f ? (double)p : 0.0;
-    float mp = param(a.min_p, a.min_p_all, b);
     mp = mp > 0.0f ? fminf(mp, 1.0f) : 0.0f;  // (NaN: off)
     const double m = ceil((double)mp * kOne);
     r.w_min = m < 1.0 ? 1ull : (uint64_t)m;
@@ -78,44 +73,63 @@ __device__ __forceinline__ uint64_t p_target(double p, uint64_t total) {
     return t < 1.0 ? 1ull : (uint64_t)t;
 }
 
-// Depth x of a logit; infinite for a masked logit or a NaN (never NaN itself:
-// infinity - infinity is taken out, and 0 * infinity, which the temperature
-// infinity gives, counts as out of range below).
-__device__ __forceinline__ double depth(float l, float m, double inv_t) {
-    if (!(l > -INFINITY)) return INFINITY;
-    return l == m ? 0.0 : ((double)m - (double)l) * inv_t;
+// Depth x of a logit below the row's largest: 0 .. infinity, or NaN for a NaN logit (and
+// for 0 * infinity, which a masked logit gives at the temperature infinity).  Infinite
+// logits count as the largest finite value; m is finite.
+__device__ __forceinline__ double depth(float l, double m, double inv_t) {
+    return (m - (double)(l > FLT_MAX ? FLT_MAX : l)) * inv_t;
 }
+
+// Adding 1.5 * 2^52 to a double of moderate size leaves the nearest integer in the low
+// bits of the sum: no conversion instruction.
+constexpr double kMagic = 6755399441055744.0;
+__device__ __forceinline__ int magic_int(double v) { return (int)(uint32_t)(uint64_t)__double_as_longlong(v); }
 
 // Bin of a depth below kRange; deeper logits have higher bins.
 __device__ __forceinline__ int bin_of(double x) {
-    return min(kBins - 1, (int)(x * (kBins / kRange)));
+    return min(kBins - 1, magic_int(__builtin_fma(x, kBins / kRange, kMagic - 0.5)));
 }
 
-// round(2^43 exp(-x)) for 0 <= x < kRange, else 0.  x = n ln 2 - r with |r| <= ln 2 / 2,
-// exp(r) by its Taylor series to r^11 / 11! (next term below 2^-47), and the rounding
-// by adding 2^52, which leaves the integer in the low bits of the sum.
-__device__ __forceinline__ uint64_t weight_at(double x) {
-    if (!(x < kRange)) return 0;
-    const double n = __builtin_rint(x * 1.4426950408889634);
-    double r = __builtin_fma(n, 0.69314718055994529, -x);  // ln 2 in two parts
-    r = __builtin_fma(n, 2.3190468138462996e-17, r);
-    double e = 1.0 / 39916800.0;
-    e = __builtin_fma(e, r, 1.0 / 3628800.0);
-    e = __builtin_fma(e, r, 1.0 / 362880.0);
-    e = __builtin_fma(e, r, 1.0 / 40320.0);
-    e = __builtin_fma(e, r, 1.0 / 5040.0);
-    e = __builtin_fma(e, r, 1.0 / 720.0);
-    e = __builtin_fma(e, r, 1.0 / 120.0);
-    e = __builtin_fma(e, r, 1.0 / 24.0);
-    e = __builtin_fma(e, r, 1.0 / 6.0);
-    e = __builtin_fma(e, r, 0.5);
+// a * b + c with c in scalar registers (the compiler keeps such constants in vector
+// registers and copies them for its two-operand form, one more instruction a step).
+__device__ __forceinline__ double fma_const(double a, double b, double c) {
+    double d;
+    #if defined(__HIP_DEVICE_COMPILE__)
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+#else
+    d = __builtin_fma(a, b, c);
+#endif
+    return d;
+}
+
+// round(2^43 exp(-x)) for 0 <= x < kRange.  x = n ln 2 - r with |r| <= ln 2 / 2; exp(r) =
+// 1 + r g(r), g the polynomial of degree 8 through (exp(r) - 1) / r at the nine Chebyshev
+// nodes of the interval (relative error below 2^-44 = half a unit of the largest
+// weight); 2^(43 - n) by the exponent field; and the rounding by adding 2^52, which
+// leaves the integer in the low bits of the sum.  Only full-rate 64-bit arithmetic.
+__device__ __forceinline__ uint64_t weight_in(double x) {
+    const double t = fma_const(x, 1.4426950408889634, kMagic);
+    const double n = t - kMagic;
+    const double r = __builtin_fma(n, 0.69314718055994529, -x);
+    double e = 2.7625104765945114e-06;
+    e = fma_const(e, r, 2.487616679288376e-05);
+    e = fma_const(e, r, 0.00019841208751916224);
+    e = fma_const(e, r, 0.0013888821672636716);
+    e = fma_const(e, r, 0.008333333353719753);
+    e = fma_const(e, r, 0.04166666689098201);
+    e = fma_const(e, r, 0.166666666666483);
+    e = fma_const(e, r, 0.49999999999797906);
     e = __builtin_fma(e, r, 1.0);
     e = __builtin_fma(e, r, 1.0);
-    const double v = __builtin_ldexp(e, 43 - (int)n) + 4503599627370496.0;
+    const uint64_t u = (uint64_t)__double_as_longlong(e) + ((uint64_t)(uint32_t)(43 - magic_int(t)) << 52);
+    const double v = __longlong_as_double((long long)u) + 4503599627370496.0;
     return (uint64_t)__double_as_longlong(v) & 0xFFFFFFFFFFFFFull;
 }
 
-__device__ __forceinline__ uint64_t weight(float l, float m, double inv_t) {
+// The weight at any depth: 0 beyond the range and for NaN.
+__device__ __forceinline__ uint64_t weight_at(double x) { return x < kRange ? weight_in(x) : 0; }
+
+__device__ __forceinline__ uint64_t weight(float l, double m, double inv_t) {
     return weight_at(depth(l, m, inv_t));
 }
 
@@ -128,26 +142,55 @@ __device__ __forceinline__ int place_index(uint64_t p) {
 }
 __device__ __forceinline__ float place_logit(uint64_t p) { return key_logit((uint32_t)(p >> kIdxBits)); }
 
-__device__ __forceinline__ float wave_max_f(float v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
+// Wave-wide operations on the vector ALUs (DPP), without the LDS round trips of
+// shuffles.
+__device__ __forceinline__ float wave_max_f(float v) {  // (NaN is passed over)
+    v = fmaxf(v, dpp_f32<0xB1>(v));   // quad_perm 1,0,3,2
+    v = fmaxf(v, dpp_f32<0x4E>(v));   // quad_perm 2,3,0,1
+    v = fmaxf(v, dpp_f32<0x141>(v));  // row_half_mirror
+    v = fmaxf(v, dpp_f32<0x140>(v));  // row_mirror
+    auto lane = [&](int i) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i)); };
+    return fmaxf(fmaxf(lane(0), lane(16)), fmaxf(lane(32), lane(48)));
+}
+
+// The value kCtrl moves to this lane, 0 where it moves none (rows not in kRows).
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, kCtrl, kRows, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), kCtrl, kRows, 0xF, true);
+    return ((uint64_t)hi << 32) | lo;
+}
+
+__device__ __forceinline__ uint64_t readlane_u64(uint64_t v, int lane) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+    return ((uint64_t)hi << 32) | lo;
+}
+
+// Inclusive running sum over the wave's lanes: within rows of 16, then each row's total
+// to the next one (rows 1 and 3), then row 1's total to rows 2 and 3.
+__device__ __forceinline__ uint64_t wave_scan_u64(uint64_t v) {
+    v += dpp_u64<0x111, 0xF>(v);  // row_shr 1
+    v += dpp_u64<0x112, 0xF>(v);
+    v += dpp_u64<0x114, 0xF>(v);
+    v += dpp_u64<0x118, 0xF>(v);
+    v += dpp_u64<0x142, 0xA>(v);  // row_bcast 15
+    v += dpp_u64<0x143, 0xC>(v);  // row_bcast 31
     return v;
 }
 
-__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-    return v;
-}
+__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) { return readlane_u64(wave_scan_u64(v), 63); }
 
-// Inclusive running sum over the wave's lanes.
-__device__ __forceinline__ uint64_t wave_scan_u64(uint64_t v, int lane) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint64_t y = __shfl_up(v, o, kWave);
-        if (lane >= o) v += y;
-    }
-    return v;
+// Largest of the wave (0 is the smallest value), returned to every lane.
+__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
+    auto step = [&](uint64_t o) { v = o > v ? o : v; };
+    step(dpp_u64<0x111, 0xF>(v));
+    step(dpp_u64<0x112, 0xF>(v));
+    step(dpp_u64<0x114, 0xF>(v));
+    step(dpp_u64<0x118, 0xF>(v));
+    step(dpp_u64<0x142, 0xA>(v));
+    step(dpp_u64<0x143, 0xC>(v));
+    return readlane_u64(v, 63);
 }
 
 // Sum over the work group, returned to every thread.  s holds one entry per wave.
@@ -174,73 +217,98 @@ __device__ __forceinline__ float group_max_f(float m, float* s) {
     return m;
 }
 
-// The row's largest logit from the chunks' (every thread; s: one entry per wave).
-template <int NT>
-__device__ __forceinline__ float row_max(const SampleArgs& a, int b, float* s) {
+// The row's largest logit from the chunks', by every wave for itself; infinity as the
+// largest finite value.  -infinity: no live logit (then every depth is NaN or infinite).
+__device__ __forceinline__ double row_max(const SampleArgs& a, int b) {
+    const float* part = a.part_max + (size_t)b * a.n_chunks;
     float m = -INFINITY;
-    for (int c = threadIdx.x; c < a.n_chunks; c += NT) m = fmaxf(m, a.part_max[(size_t)b * a.n_chunks + c]);
-    return group_max_f<NT>(m, s);
+    for (int c = threadIdx.x & 63; c < a.n_chunks; c += 64) m = fmaxf(m, part[c]);
+    return (double)fminf(wave_max_f(m), FLT_MAX);
 }
 
-// Calls f(logit, index) for this thread's elements of row b in [i0, i1).  The logits
-// come in aligned 16-byte pieces whatever V is: a piece at an end of the range may hold
-// elements outside it, which are passed over, and the piece that would cross the end of
-// the whole array is read element by element.
-template <int NT, typename F>
-__device__ __forceinline__ void each_logit(const SampleArgs& a, int b, int i0, int i1, F f) {
-    const int64_t o = (int64_t)b * a.V, total = (int64_t)a.B * a.V;
-    const int64_t g1 = (o + i1 + 3) >> 2;
-    for (int64_t g0 = ((o + i0) >> 2) + threadIdx.x; g0 < g1; g0 += 4 * NT) {
-        f32x4 v[4];
+// This thread's logits of the range [i0, i1) of row b, kPieces aligned 16-byte pieces at
+// a time (aligned whatever V is: a piece at an end of the range may hold elements outside
+// it, which read as minus infinity, and the piece that would cross the end of the whole
+// array is read element by element).
+constexpr int kPieces = 4;
+struct Logits {
+    const float* p;     // the array
+    int64_t o, g1, n;   // the row's first element, the range's last piece + 1, the array's size
+    int i0, i1;
+    int64_t g;          // this thread's next piece
+    f32x4 v[kPieces];
+
+    __device__ __forceinline__ Logits(const SampleArgs& a, int b, int from, int to)
+        : p(a.logits), o((int64_t)b * a.V), n((int64_t)a.B * a.V), i0(from), i1(to) {
+        g = ((o + i0) >> 2) + threadIdx.x;
+        g1 = (o + i1 + 3) >> 2;
+        load();
+    }
+    __device__ __forceinline__ void load() {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {  // four pieces in flight
-            const int64_t g = g0 + u * NT;
-            if (g < g1) {
-                if (4 * g + 4 <= total) {
-                    v[u] = *(const f32x4*)(a.logits + 4 * g);
+        for (int u = 0; u < kPieces; ++u) {
+            const int64_t at = g + u * kThreads;
+            if (at < g1) {
+                if (4 * at + 4 <= n) {
+                    v[u] = *(const f32x4*)(p + 4 * at);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[u][j] = 4 * g + j < total ? a.logits[4 * g + j] : 0.0f;
+                    for (int j = 0; j < 4; ++j) v[u][j] = 4 * at + j < n ? p[4 * at + j] : 0.0f;
                 }
             }
         }
+    }
+    // f(logit, index) for all of them; the first pieces were loaded by the constructor
+    template <typename F>
+    __device__ __forceinline__ void each(F f) {
+        while (g < g1) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int64_t g = g0 + u * NT;
-            if (g >= g1) break;
+            for (int u = 0; u < kPieces; ++u) {
+                const int64_t at = g + u * kThreads;
+                if (at >= g1) break;
+                const int base = (int)(4 * at - o);
+                if (base < i0 || base + 4 > i1) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = (int)(4 * g + j - o);
-                if (i >= i0 && i < i1) f(v[u][j], i);
+                    for (int j = 0; j < 4; ++j)
+                        if ((uint32_t)(base + j - i0) >= (uint32_t)(i1 - i0)) v[u][j] = -INFINITY;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f(v[u][j], base + j);
             }
+            g += kPieces * kThreads;
+            load();
         }
     }
-}
+};
 
 __global__ __launch_bounds__(kThreads) void sample_max_kernel(const SampleArgs a) {
     __shared__ float s[kThreads / 64];
     const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
     // the row's histogram and counter, shared out over its chunks
     for (int i = c * kThreads + tid; i < kBins; i += a.n_chunks * kThreads) a.hist[(size_t)b * kBins + i] = 0;
-    if (c == 0 && tid == 0) a.list_n[b] = 0;
-    const int i0 = c << a.chunk_sh, i1 = min(a.V, i0 + (1 << a.chunk_sh));
+    if (c == 0 && tid == 0) {
+        a.list_n[b] = 0;
+        a.row[b] = row_params(a, b);
+    }
+    const int i0 = c << a.chunk_sh;
+    Logits in(a, b, i0, min(a.V, i0 + (1 << a.chunk_sh)));
     float m = -INFINITY;
-    each_logit<kThreads>(a, b, i0, i1, [&](float l, int) { m = fmaxf(m, l); });  // (NaN is passed over)
+    in.each([&](float l, int) { m = fmaxf(m, l); });  // (NaN is passed over)
     m = group_max_f<kThreads>(m, s);
     if (tid == 0) a.part_max[(size_t)b * a.n_chunks + c] = m;
 }
 
 __global__ __launch_bounds__(kThreads) void sample_hist_kernel(const SampleArgs a) {
     __shared__ unsigned long long s_h[kBins];
-    __shared__ float s_m[kThreads / 64];
     __shared__ uint64_t s_sum[kThreads / 64];
     const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-    const Row p = row_params(a, b);
-    const float m = row_max<kThreads>(a, b, s_m);
-    const int i0 = c << a.chunk_sh, i1 = min(a.V, i0 + (1 << a.chunk_sh));
+    const int i0 = c << a.chunk_sh;
+    Logits in(a, b, i0, min(a.V, i0 + (1 << a.chunk_sh)));  // its first loads go ahead of all else
+    const SampleRow p = a.row[b];
+    const double m = row_max(a, b);
     if (!p.cut_k && !p.cut_p) {  // uniform over the work group
         uint64_t sum = 0;
-        each_logit<kThreads>(a, b, i0, i1, [&](float l, int) {
+        in.each([&](float l, int) {
             const uint64_t w = weight(l, m, p.inv_t);
             sum += w >= p.w_min ? w : 0;
         });
@@ -250,10 +318,17 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(const SampleArgs 
     }
     for (int i = tid; i < kBins; i += kThreads) s_h[i] = 0;
     __syncthreads();
-    each_logit<kThreads>(a, b, i0, i1, [&](float l, int) {
-        const double x = depth(l, m, p.inv_t);
-        if (x < kRange) atomicAdd(&s_h[bin_of(x)], p.cut_k ? 1ull : (unsigned long long)weight_at(x));
-    });
+    if (p.cut_k) {  // (two loops: the choice stays out of them)
+        in.each([&](float l, int) {
+            const double x = depth(l, m, p.inv_t);
+            if (x < kRange) atomicAdd(&s_h[bin_of(x)], 1ull);
+        });
+    } else {
+        in.each([&](float l, int) {
+            const double x = depth(l, m, p.inv_t);
+            if (x < kRange) atomicAdd(&s_h[bin_of(x)], (unsigned long long)weight_in(x));
+        });
+    }
     __syncthreads();
     for (int i = tid; i < kBins; i += kThreads)
         if (s_h[i]) atomicAdd((unsigned long long*)&a.hist[(size_t)b * kBins + i], s_h[i]);
@@ -268,7 +343,7 @@ struct Cut {
     uint64_t total;
 };
 struct CutScratch {
-    uint64_t wave[kPickWaves];
+    uint64_t wave[kRowThreads / 64];
     Cut cut;
 };
 
@@ -282,7 +357,7 @@ __device__ __forceinline__ Cut find_cut(const uint64_t* h, CutScratch& s, Of of)
         v[j] = h[tid * PER + j];
         sum += v[j];
     }
-    const uint64_t inc = wave_scan_u64(sum, lane);
+    const uint64_t inc = wave_scan_u64(sum);
     __syncthreads();  // the scratch may still be read from the previous use
     if (lane == 63) s.wave[wave] = inc;
     if (tid == 0) s.cut.bin = kBins;
@@ -306,15 +381,17 @@ __device__ __forceinline__ Cut find_cut(const uint64_t* h, CutScratch& s, Of of)
 }
 
 __global__ __launch_bounds__(kThreads) void sample_gather_kernel(const SampleArgs a) {
-    __shared__ unsigned long long s_list[kList];
+    constexpr uint32_t kLocal = 1024;  // entries collected in LDS; more go out one by one
+    __shared__ unsigned long long s_list[kLocal];
     __shared__ uint32_t s_n, s_base;
-    __shared__ float s_m[kThreads / 64];
     __shared__ uint64_t s_sum[kThreads / 64];
     __shared__ CutScratch s_cut;
     const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-    const Row p = row_params(a, b);
+    const SampleRow p = a.row[b];
     if (!p.cut_k && !p.cut_p) return;  // uniform
-    const float m = row_max<kThreads>(a, b, s_m);
+    const int i0 = c << a.chunk_sh;
+    Logits in(a, b, i0, min(a.V, i0 + (1 << a.chunk_sh)));
+    const double m = row_max(a, b);
     // with top-k the list takes every token down to the bin of the last one it keeps
     // (top-p's mass is a share of what top-k keeps, so both cuts lie in there); if top-k
     // keeps every token with a weight, that is all of them.  top-p alone: only the bin
@@ -327,140 +404,203 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(const SampleArg
         a.state[b] = SampleState{cut.total, p.cut_k ? 0 : cut.before, lo, hi, cut.bin < kBins, 0};
     if (tid == 0) s_n = 0;
     __syncthreads();
-    const int i0 = c << a.chunk_sh, i1 = min(a.V, i0 + (1 << a.chunk_sh));
     uint64_t sum = 0;
-    each_logit<kThreads>(a, b, i0, i1, [&](float l, int i) {
+    in.each([&](float l, int i) {
         const double x = depth(l, m, p.inv_t);
         if (!(x < kRange)) return;
         const int bin = bin_of(x);
         if (bin < lo) {
-            const uint64_t w = weight_at(x);
+            const uint64_t w = weight_in(x);
             sum += w >= p.w_min ? w : 0;
         } else if (bin <= hi) {
-            const uint32_t at = atomicAdd(&s_n, 1u);
-            if (at < (uint32_t)kList) s_list[at] = place(l, i);
+            uint32_t at = atomicAdd(&s_n, 1u);
+            if (at < kLocal) {
+                s_list[at] = place(l, i);
+            } else {
+                at = atomicAdd(&a.list_n[b], 1u);
+                if (at < (uint32_t)kList) a.list[(size_t)b * kList + at] = place(l, i);
+            }
         }
     });
     sum = group_sum_u64<kThreads>(sum, s_sum);  // (its barriers also complete the list)
-    const uint32_t n = s_n;
+    const uint32_t n = min(s_n, kLocal);
     if (tid == 0) {
         a.chunk_w[(size_t)b * a.n_chunks + c] = sum;
         s_base = n ? atomicAdd(&a.list_n[b], n) : 0;
     }
     __syncthreads();
     // a list that overflows is not used: list_n says so
-    if (n <= (uint32_t)kList && s_base + n <= (uint32_t)kList)
-        for (uint32_t i = tid; i < n; i += kThreads) a.list[(size_t)b * kList + s_base + i] = s_list[i];
+    for (uint32_t i = tid; i < n; i += kThreads)
+        if (s_base + i < (uint32_t)kList) a.list[(size_t)b * kList + s_base + i] = s_list[i];
 }
 
 // Shared memory of the work group that makes a row's cut and draw.
 struct Draw {
     uint64_t hist[kBins];
-    uint64_t rank_p[kRank], rank_q[kRank];
-    unsigned long long lo, hi, cut;
+    ulonglong2 rank[kRank];  // (place, weight) of the tokens that are ranked
+    unsigned long long lo, hi, cut, cut_k, mass;
     uint32_t n;
     CutScratch cs;
-    uint64_t seg[16 * kPickWaves];  // sums of 64 neighbouring elements, in index order
-    uint64_t sum[kPickWaves];
-    float m[kPickWaves];
+    uint64_t sum[kRowThreads / 64];
+    float m[kRowThreads / 64];
     int token;
     uint64_t wt;
 };
 
+// Collects the region's tokens with lo <= place <= hi for ranking; false if there are
+// more than kRank.  s.n has to be 0 before; a barrier completes it here.
+template <typename Each>
+__device__ __forceinline__ bool collect(Draw& s, uint64_t lo, uint64_t hi, Each each) {
+    each([&](uint64_t p, uint64_t q) {
+        if (p >= lo && p <= hi && s.n <= (uint32_t)kRank) {
+            const uint32_t at = atomicAdd(&s.n, 1u);
+            if (at < (uint32_t)kRank) s.rank[at] = ulonglong2{p, q};
+        }
+    });
+    __syncthreads();
+    return s.n <= (uint32_t)kRank;
+}
+
+// Ranks the n collected tokens by comparing each with each: 2^sh threads a token, as many
+// as the work group has.  leader: this thread holds the result for token *me, of which
+// *count tokens with the mass *mass lie before.
+template <int NT>
+__device__ __forceinline__ bool rank_tokens(const Draw& s, int n, ulonglong2* me, uint32_t* count,
+                                            uint64_t* mass) {
+    const int tid = threadIdx.x;
+    int sh = 0;
+    while (sh < 5 && (n << (sh + 1)) <= NT) ++sh;
+    const int i = tid >> sh, q = 1 << sh, part = tid & (q - 1);
+    const ulonglong2 mine = s.rank[i < n ? i : 0];
+    uint32_t c = 0;
+    uint64_t w = 0;
+    if (i < n) {
+#pragma unroll 4
+        for (int j = part; j < n; j += q) {
+            const ulonglong2 o = s.rank[j];
+            const bool before = o.x > mine.x;
+            c += before;
+            w += before ? o.y : 0;
+        }
+    }
+    for (int o = 1; o < q; o <<= 1) {
+        c += __shfl_xor(c, o, kWave);
+        w += __shfl_xor(w, o, kWave);
+    }
+    *me = mine;
+    *count = c;
+    *mass = w;
+    return i < n && part == 0;
+}
+
 // The last kept token of a region: the first, in the row's order, at which the running
 // sum of a quantity reaches the target (some token does).  each(f) calls f(place,
 // quantity) for this thread's tokens of the region.  Tokens are narrowed down by their
-// place, a factor of 2048 a time, until kRank of them are left, which are ranked by
-// comparing each with each.  Returns the token's place.
-template <typename Each>
+// place, a factor of 2048 a time, until kRank of them are left, which are ranked.
+// Returns the token's place.
+template <int NT, typename Each>
 __device__ __forceinline__ uint64_t narrow_cut(Draw& s, uint64_t target, Each each) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    uint64_t lo = 0, hi = ~0ull;
-    for (bool first = true;; first = false) {
-        __syncthreads();
-        if (tid == 0) {
-            s.n = 0;
-            s.cut = 0;  // (not reached: everything is kept)
-            s.lo = ~0ull;
-            s.hi = 0;
-        }
-        __syncthreads();
-        each([&](uint64_t p, uint64_t q) {
-            if (p >= lo && p <= hi && s.n <= (uint32_t)kRank) {
-                const uint32_t at = atomicAdd(&s.n, 1u);
-                if (at < (uint32_t)kRank) {
-                    s.rank_p[at] = p;
-                    s.rank_q[at] = q;
-                }
-            }
-        });
-        __syncthreads();
-        const int n = (int)min(s.n, (uint32_t)kRank + 1);
-        if (n <= kRank) {
-            // four threads per token, each over a quarter of the others
-            const int i = tid >> 2;
-            if (i < n) {
-                const uint64_t p = s.rank_p[i];
-                uint64_t run = 0;
-                for (int j = tid & 3; j < n; j += 4) run += s.rank_p[j] > p ? s.rank_q[j] : 0;
-                run += __shfl_xor(run, 1, kWave);
-                run += __shfl_xor(run, 2, kWave);
-                if (run < target && run + s.rank_q[i] >= target) s.cut = p;
-            }
-            __syncthreads();
-            return s.cut;
-        }
-        if (first) {
-            uint64_t l = ~0ull, h = 0;
-            each([&](uint64_t p, uint64_t) {
-                l = p < l ? p : l;
-                h = p > h ? p : h;
-            });
-            if (h >= l) {
-                atomicMin(&s.lo, l);
-                atomicMax(&s.hi, h);
-            }
-            __syncthreads();
-            lo = s.lo;
-            hi = s.hi;
-        }
-        const int bits = 64 - __builtin_clzll(hi - lo);  // (more than kRank places: hi > lo)
+    const int tid = threadIdx.x;
+    __syncthreads();
+    if (tid == 0) {
+        s.cut = 0;  // (not reached: everything is kept)
+        s.lo = ~0ull;
+        s.hi = 0;
+    }
+    __syncthreads();
+    uint64_t l = 0, h = 0;  // ~smallest and largest place (0: no token)
+    each([&](uint64_t p, uint64_t) {
+        l = ~p > l ? ~p : l;
+        h = p > h ? p : h;
+    });
+    l = ~wave_max_u64(l);
+    h = wave_max_u64(h);
+    if ((tid & 63) == 0 && h >= l) {
+        atomicMin(&s.lo, l);
+        atomicMax(&s.hi, h);
+    }
+    __syncthreads();
+    uint64_t lo = s.lo, hi = s.hi;
+    if (hi < lo) return 0;  // (uniform; no tokens at all)
+    for (;;) {
+        const int bits = hi > lo ? 64 - __builtin_clzll(hi - lo) : 0;
         const int shift = bits > 11 ? bits - 11 : 0;
-        for (int i = tid; i < kBins; i += kPickThreads) s.hist[i] = 0;
+        for (int i = tid; i < kBins; i += NT) s.hist[i] = 0;
+        if (tid == 0) s.n = 0;
         __syncthreads();
         each([&](uint64_t p, uint64_t q) {
             if (p >= lo && p <= hi)
                 atomicAdd((unsigned long long*)&s.hist[(int)((hi - p) >> shift)], (unsigned long long)q);
         });
         __syncthreads();
-        const Cut c = find_cut<kPickThreads>(s.hist, s.cs, [&](uint64_t) { return target; });
+        const Cut c = find_cut<NT>(s.hist, s.cs, [&](uint64_t) { return target; });
         if (c.bin >= kBins) return 0;
         target -= c.before;
         hi -= (uint64_t)c.bin << shift;
         if (shift == 0) return hi;
         const uint64_t bottom = hi - ((1ull << shift) - 1);
         lo = bottom > lo ? bottom : lo;
+        if (collect(s, lo, hi, each)) {
+            ulonglong2 me;
+            uint32_t count;
+            uint64_t run;
+            if (rank_tokens<NT>(s, (int)s.n, &me, &count, &run) && run < target && run + me.y >= target)
+                s.cut = me.x;
+            __syncthreads();
+            return s.cut;
+        }
+        __syncthreads();  // s.n is read above and cleared in the next round
     }
-    (void)lane;
 }
 
 // The cut of a row whose region's tokens each(f) visits as f(place, weight): top-k (if
 // its target lies in the region), then top-p.  base: mass before the region, total: the
-// mass top-p refers to without top-k.
-template <typename Each>
-__device__ __forceinline__ uint64_t row_cut(Draw& s, const Row& p, bool k_reached, uint64_t base,
-                                            uint64_t total, Each each) {
+// mass top-p refers to without top-k.  few: the region may hold kRank tokens or fewer.
+template <int NT, typename Each>
+__device__ __forceinline__ uint64_t row_cut(Draw& s, const SampleRow& p, bool k_reached, uint64_t base,
+                                            uint64_t total, bool few, Each each) {
+    const int tid = threadIdx.x;
+    if (few) {
+        if (tid == 0) {
+            s.n = 0;
+            s.cut = s.cut_k = 0;
+            s.mass = 0;
+        }
+        __syncthreads();
+        if (collect(s, 0, ~0ull, each)) {  // one ranking serves both cuts
+            const int n = (int)s.n;
+            ulonglong2 me;
+            uint32_t count;
+            uint64_t run;
+            const bool leader = rank_tokens<NT>(s, n, &me, &count, &run);
+            if (p.cut_k) {
+                // the last token that top-k keeps and the mass up to it
+                if (leader && count + 1 == min(p.k, (uint32_t)n)) {
+                    s.cut_k = k_reached ? me.x : 0;
+                    s.mass = run + me.y;
+                }
+                __syncthreads();
+                if (!p.cut_p) return s.cut_k;
+                total = s.mass;
+                base = 0;
+            }
+            const uint64_t target = p_target(p.p, total) - base;
+            if (leader && run < target && run + me.y >= target) s.cut = me.x;
+            __syncthreads();
+            return p.cut_k && s.cut_k > s.cut ? s.cut_k : s.cut;
+        }
+    }
     uint64_t last = 0;
     if (p.cut_k) {
         if (k_reached)
-            last = narrow_cut(s, p.k, [&](auto f) { each([&](uint64_t pl, uint64_t) { f(pl, 1ull); }); });
+            last = narrow_cut<NT>(s, p.k, [&](auto f) { each([&](uint64_t pl, uint64_t) { f(pl, 1ull); }); });
         if (!p.cut_p) return last;
         uint64_t mass = 0;
         each([&](uint64_t pl, uint64_t w) { mass += pl >= last ? w : 0; });
-        total = group_sum_u64<kPickThreads>(mass, s.sum);
+        total = group_sum_u64<NT>(mass, s.sum);
         base = 0;
     }
-    const uint64_t cut = narrow_cut(s, p_target(p.p, total) - base, each);
+    const uint64_t cut = narrow_cut<NT>(s, p_target(p.p, total) - base, each);
     return cut > last ? cut : last;
 }
 
@@ -472,60 +612,41 @@ __device__ __forceinline__ uint64_t drawn_mass(float u, uint64_t total) {
 }
 
 // The element at which the running sum of w, in index order, exceeds `draw`: element
-// 1024 j + tid has weight w[j] in thread tid.  s.token = its number or -1, s.wt = its
-// weight; visible after the call.  total: the sum of all w.
-template <int PER>
+// PER tid + j has weight w[j] in thread tid.  s.token = its number or -1, s.wt = its
+// weight; visible after the call.
+template <int NT, int PER>
 __device__ __forceinline__ void find_drawn(Draw& s, const uint64_t (&w)[PER], uint64_t draw) {
+    constexpr int NW = NT / 64;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    uint64_t sum = 0;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const uint64_t t = wave_sum_u64(w[j]);
-        if (lane == 0) s.seg[j * kPickWaves + wave] = t;
-    }
+    for (int j = 0; j < PER; ++j) sum += w[j];
+    const uint64_t inc = wave_scan_u64(sum);
+    __syncthreads();  // s.sum may still be read
+    if (lane == 63) s.sum[wave] = inc;
     if (tid == 0) {
         s.token = -1;
         s.wt = 0;
     }
     __syncthreads();
-    // every wave finds the segment; the one that holds it looks through its lanes
-    constexpr int SEG = PER * kPickWaves, EACH = (SEG + 63) / 64;
-    uint64_t v[EACH], sum = 0;
+    uint64_t run = inc - sum;
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-        v[e] = lane * EACH + e < SEG ? s.seg[lane * EACH + e] : 0;
-        sum += v[e];
-    }
-    uint64_t run = wave_scan_u64(sum, lane) - sum;
-    int seg = -1;
-    uint64_t before = 0;
+    for (int v = 0; v < NW; ++v) run += v < wave ? s.sum[v] : 0;
+    if (run <= draw && run + sum > draw) {  // one thread
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-        if (run <= draw && run + v[e] > draw) {
-            seg = lane * EACH + e;
-            before = run;
-        }
-        run += v[e];
-    }
-    const uint64_t who = __ballot(seg >= 0);
-    if (who) {  // uniform
-        const int from = (int)__builtin_ctzll(who);
-        seg = __shfl(seg, from, kWave);
-        before = __shfl(before, from, kWave);
-        if (seg % kPickWaves == wave) {
-            uint64_t mine = 0;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) mine = seg / kPickWaves == j ? w[j] : mine;
-            const uint64_t inc = before + wave_scan_u64(mine, lane);
-            if (mine && inc > draw && inc - mine <= draw) {
-                s.token = seg * 64 + lane;
-                s.wt = mine;
+        for (int j = 0; j < PER; ++j) {
+            if (run <= draw && run + w[j] > draw) {
+                s.token = PER * tid + j;
+                s.wt = w[j];
             }
+            run += w[j];
         }
     }
     __syncthreads();
 }
 
 // The chosen token's outputs.
+template <int NT>
 __device__ __forceinline__ void write_token(const SampleArgs& a, int b, int token, uint64_t wt,
                                             uint64_t total) {
     const int tid = threadIdx.x;
@@ -536,7 +657,7 @@ __device__ __forceinline__ void write_token(const SampleArgs& a, int b, int toke
     if (!a.x_next) return;
     const int d = a.d;
     const size_t r = (size_t)token;
-    for (int wd = tid; wd < d / 8; wd += kPickThreads) {
+    for (int wd = tid; wd < d / 8; wd += NT) {
         const uint32_t code = a.embed.q[r * (size_t)(d / 8) + wd];
         const size_t g = r * (size_t)(d / kGroup) + wd / 8;
         *(bf16x8*)(a.x_next + (size_t)b * d + 8 * (size_t)wd) =
@@ -544,32 +665,38 @@ __device__ __forceinline__ void write_token(const SampleArgs& a, int b, int toke
     }
 }
 
-// PER: elements of a chunk per thread, chunk / 1024.
+// PER: elements of a chunk per thread.
 template <int PER>
 __global__ __launch_bounds__(kPickThreads) void sample_pick_kernel(const SampleArgs a) {
-    constexpr int LPT = kList / kPickThreads;  // list entries per thread
+    constexpr int NT = kPickThreads, NW = NT / 64;
+    constexpr int LPT = kList / NT;  // list entries per thread
+    static_assert(kMaxChunks <= NT, "one chunk a thread");
     __shared__ Draw s;
     __shared__ unsigned long long s_chunk[kMaxChunks];
     __shared__ int s_at;
     __shared__ uint64_t s_before;
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const Row p = row_params(a, b);
+    // everything that the earlier kernels left, in one round trip (entries past the
+    // list's end are read, inside the workspace, and not used)
+    const SampleRow p = a.row[b];
     const uint32_t n = a.list_n[b];
-    const float u = a.u[b];
-    const float m = row_max<kPickThreads>(a, b, s.m);
-    for (int c = tid; c < a.n_chunks; c += kPickThreads) s_chunk[c] = a.chunk_w[(size_t)b * a.n_chunks + c];
+    const SampleState st = a.state[b];
+    const int cc = tid < a.n_chunks ? tid : 0;
+    const float pm = a.part_max[(size_t)b * a.n_chunks + cc];
+    const uint64_t cw = a.chunk_w[(size_t)b * a.n_chunks + cc];
+    uint64_t lp[LPT], lw[LPT];
+#pragma unroll
+    for (int j = 0; j < LPT; ++j) lp[j] = a.list[(size_t)b * kList + tid + j * NT];
+    const double m = (double)fminf(group_max_f<NT>(pm, s.m), FLT_MAX);
+    if (tid < a.n_chunks) s_chunk[tid] = cw;
     const float* row = a.logits + (size_t)b * a.V;
     uint64_t last = 0;  // kept: place >= last
     if (m > -INFINITY && (p.cut_k || p.cut_p)) {
-        const SampleState st = a.state[b];
         const bool listed = n <= (uint32_t)kList;
-        uint64_t lp[LPT], lw[LPT];
 #pragma unroll
         for (int j = 0; j < LPT; ++j) {
-            const uint32_t i = tid + j * kPickThreads;
-            const bool live = listed && i < n;
-            lp[j] = live ? a.list[(size_t)b * kList + i] : 0;
-            lw[j] = live ? weight(place_logit(lp[j]), m, p.inv_t) : 0;
+            lw[j] = 0;
+            if (listed && tid + j * NT < (int)n) lw[j] = weight(place_logit(lp[j]), m, p.inv_t);
         }
         auto each = [&](auto f) {
             if (listed) {
@@ -577,15 +704,15 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick_kernel(const SampleA
                 for (int j = 0; j < LPT; ++j)
                     if (lw[j]) f(lp[j], lw[j]);
             } else {
-                for (int i = tid; i < a.V; i += kPickThreads) {
+                for (int i = tid; i < a.V; i += NT) {
                     const double x = depth(row[i], m, p.inv_t);
                     if (!(x < kRange)) continue;
                     const int bin = bin_of(x);
-                    if (bin >= st.lo && bin <= st.hi) f(place(row[i], i), weight_at(x));
+                    if (bin >= st.lo && bin <= st.hi) f(place(row[i], i), weight_in(x));
                 }
             }
         };
-        last = row_cut(s, p, st.reached, st.before, st.total, each);
+        last = row_cut<NT>(s, p, st.reached, st.before, st.total, n <= (uint32_t)kRank, each);
         __syncthreads();
         each([&](uint64_t pl, uint64_t w) {
             if (pl >= last && w >= p.w_min)
@@ -593,19 +720,19 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick_kernel(const SampleA
         });
     }
     __syncthreads();
-    // the chunk that holds the drawn mass (kMaxChunks <= 1024: one a thread)
+    // the chunk that holds the drawn mass
     const uint64_t mine = tid < a.n_chunks ? s_chunk[tid] : 0;
-    const uint64_t inc_w = wave_scan_u64(mine, lane);
+    const uint64_t inc_w = wave_scan_u64(mine);
     if (lane == 63) s.sum[wave] = inc_w;
     if (tid == 0) s_at = -1;
     __syncthreads();
     uint64_t run = inc_w - mine, total = 0;
 #pragma unroll
-    for (int w = 0; w < kPickWaves; ++w) {
+    for (int w = 0; w < NW; ++w) {
         run += w < wave ? s.sum[w] : 0;
         total += s.sum[w];
     }
-    const uint64_t draw = drawn_mass(u, total);
+    const uint64_t draw = drawn_mass(p.u, total);
     if (mine && run <= draw && run + mine > draw) {
         s_at = tid;
         s_before = run;
@@ -616,96 +743,103 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick_kernel(const SampleA
     const int chunk = s_at;
     if (chunk >= 0) {  // (uniform; a row without a live logit has total 0 and token 0)
         const int i0 = chunk << a.chunk_sh;
+        float l[PER];
         uint64_t w[PER];
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int i = i0 + j * kPickThreads + tid;
-            w[j] = 0;
-            if (i < a.V) {
-                const float l = row[i];
-                w[j] = weight(l, m, p.inv_t);
-                if (w[j] < p.w_min || place(l, i) < last) w[j] = 0;
-            }
+            const int i = i0 + PER * tid + j;
+            l[j] = row[i < a.V ? i : a.V - 1];
         }
-        find_drawn<PER>(s, w, draw - s_before);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int i = i0 + PER * tid + j;
+            w[j] = weight(l[j], m, p.inv_t);
+            if (i >= a.V || w[j] < p.w_min || place(l[j], i) < last) w[j] = 0;
+        }
+        find_drawn<NT, PER>(s, w, draw - s_before);
         token = s.token >= 0 ? i0 + s.token : 0;
         wt = s.wt;
     }
-    write_token(a, b, token, wt, total);
+    write_token<NT>(a, b, token, wt, total);
 }
 
-// A short row (V <= 1024 PER): element 1024 j + tid in register j of thread tid.
-template <int PER>
-__global__ __launch_bounds__(kPickThreads) void sample_row_kernel(const SampleArgs a) {
+// A short row (V <= NT PER): element PER tid + j in register j of thread tid.  Weights are
+// computed where they are used: kept in registers beside the logits they spill.
+template <int NT, int PER>
+__global__ __launch_bounds__(NT) void sample_row_kernel(const SampleArgs a) {
     __shared__ Draw s;
     const int b = blockIdx.x, tid = threadIdx.x;
-    const Row p = row_params(a, b);
-    const float u = a.u[b];
     const float* row = a.logits + (size_t)b * a.V;
     float l[PER];
-    float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-        const int i = j * kPickThreads + tid;
-        l[j] = i < a.V ? row[i] : -INFINITY;
+        const int i = PER * tid + j;
+        l[j] = row[i < a.V ? i : a.V - 1];
     }
+    const SampleRow p = row_params(a, b);
+    float most = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) m = fmaxf(m, l[j]);
-    m = group_max_f<kPickThreads>(m, s.m);
-    uint64_t w[PER];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) w[j] = weight(l[j], m, p.inv_t);
+    for (int j = 0; j < PER; ++j) {
+        if (PER * tid + j >= a.V) l[j] = -INFINITY;
+        most = fmaxf(most, l[j]);
+    }
+    const double m = (double)fminf(group_max_f<NT>(most, s.m), FLT_MAX);
     uint64_t last = 0;
     if (m > -INFINITY && (p.cut_k || p.cut_p)) {
-        for (int i = tid; i < kBins; i += kPickThreads) s.hist[i] = 0;
+        for (int i = tid; i < kBins; i += NT) s.hist[i] = 0;
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (w[j])
-                atomicAdd((unsigned long long*)&s.hist[bin_of(depth(l[j], m, p.inv_t))],
-                          p.cut_k ? 1ull : (unsigned long long)w[j]);
+        for (int j = 0; j < PER; ++j) {
+            const double x = depth(l[j], m, p.inv_t);
+            if (x < kRange)
+                atomicAdd((unsigned long long*)&s.hist[bin_of(x)],
+                          p.cut_k ? 1ull : (unsigned long long)weight_in(x));
+        }
         __syncthreads();
-        const Cut cut = find_cut<kPickThreads>(s.hist, s.cs, [&](uint64_t total) {
+        const Cut cut = find_cut<NT>(s.hist, s.cs, [&](uint64_t total) {
             return p.cut_k ? (uint64_t)p.k : p_target(p.p, total);
         });
         const int hi = min(cut.bin, kBins - 1), lo = p.cut_k ? 0 : hi;
         auto each = [&](auto f) {
 #pragma unroll
-            for (int j = 0; j < PER; ++j)
-                if (w[j]) {
-                    const int bin = bin_of(depth(l[j], m, p.inv_t));
-                    if (bin >= lo && bin <= hi) f(place(l[j], j * kPickThreads + tid), w[j]);
+            for (int j = 0; j < PER; ++j) {
+                const double x = depth(l[j], m, p.inv_t);
+                if (x < kRange) {
+                    const int bin = bin_of(x);
+                    if (bin >= lo && bin <= hi) f(place(l[j], PER * tid + j), weight_in(x));
                 }
+            }
         };
-        last = row_cut(s, p, cut.bin < kBins, cut.before, cut.total, each);
+        last = row_cut<NT>(s, p, cut.bin < kBins, cut.before, cut.total, true, each);
     }
-    uint64_t sum = 0;
+    uint64_t w[PER], sum = 0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-        if (w[j] < p.w_min || place(l[j], j * kPickThreads + tid) < last) w[j] = 0;
+        w[j] = weight(l[j], m, p.inv_t);
+        if (w[j] < p.w_min || place(l[j], PER * tid + j) < last) w[j] = 0;
         sum += w[j];
     }
-    const uint64_t total = group_sum_u64<kPickThreads>(sum, s.sum);
-    find_drawn<PER>(s, w, drawn_mass(u, total));
-    write_token(a, b, max(s.token, 0), s.wt, total);
+    const uint64_t total = group_sum_u64<NT>(sum, s.sum);
+    find_drawn<NT, PER>(s, w, drawn_mass(p.u, total));
+    write_token<NT>(a, b, max(s.token, 0), s.wt, total);
 }
 
 }  // namespace
 
-// log2 of the logits per chunk: enough chunks for the chip, at most kSampleMaxChunks
-// a row.
+// log2 of the logits per chunk: enough chunks for the chip.
+static_assert((MOE_MAX_VOCAB >> 11) <= kSampleMaxChunks, "chunks of a row");
 int sample_chunk_sh(int V, int B) {
-    int sh = 11;
+    int sh = 11;  // .. 14: V <= 2^20 makes at most 512 chunks of 2048
     auto chunks = [&] { return (V + (1 << sh) - 1) >> sh; };
-    while (chunks() > kSampleMaxChunks || (sh < 14 && (int64_t)B * chunks() > 2048)) ++sh;
+    while (sh < 14 && (int64_t)B * chunks() > 1024) ++sh;
     return sh;
 }
 
 hipError_t launch_sample(const SampleArgs& a, hipStream_t s) {
     hipError_t e;
     if (a.V <= kSampleRowMax) {
-        if (a.V <= 4 * kPickThreads) sample_row_kernel<4><<<a.B, kPickThreads, 0, s>>>(a);
-        else sample_row_kernel<16><<<a.B, kPickThreads, 0, s>>>(a);
+        if (a.V <= 4096) sample_row_kernel<512, 8><<<a.B, 512, 0, s>>>(a);
+        else sample_row_kernel<1024, 16><<<a.B, 1024, 0, s>>>(a);
         trace_point(s);
         return hipGetLastError();
     }
@@ -719,10 +853,11 @@ hipError_t launch_sample(const SampleArgs& a, hipStream_t s) {
     sample_gather_kernel<<<grid, kThreads, 0, s>>>(a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     trace_point(s);
-    if (a.chunk_sh == 11) sample_pick_kernel<2><<<a.B, kPickThreads, 0, s>>>(a);
-    else if (a.chunk_sh == 12) sample_pick_kernel<4><<<a.B, kPickThreads, 0, s>>>(a);
-    else if (a.chunk_sh == 13) sample_pick_kernel<8><<<a.B, kPickThreads, 0, s>>>(a);
-    else sample_pick_kernel<16><<<a.B, kPickThreads, 0, s>>>(a);
+    static_assert(kPickThreads == 512, "elements per thread below");
+    if (a.chunk_sh == 11) sample_pick_kernel<4><<<a.B, kPickThreads, 0, s>>>(a);
+    else if (a.chunk_sh == 12) sample_pick_kernel<8><<<a.B, kPickThreads, 0, s>>>(a);
+    else if (a.chunk_sh == 13) sample_pick_kernel<16><<<a.B, kPickThreads, 0, s>>>(a);
+    else sample_pick_kernel<32><<<a.B, kPickThreads, 0, s>>>(a);
     trace_point(s);
     return hipGetLastError();
 }
