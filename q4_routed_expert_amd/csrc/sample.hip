@@ -34,9 +34,8 @@
 namespace q4moe {
 namespace {
 
-constexpr int kThreads = 256;       // of kernels 1 to 3
-constexpr int kPickThreads = 512;   // of kernel 4
-constexpr int kRowThreads = 1024;   // of the short rows' kernel, at most
+constexpr int kThreads = 512;       // of kernels 1 to 3
+constexpr int kRowThreads = 1024;   // of kernel 4 and of the short rows' kernel, at most
 constexpr int kBins = kSampleBins;
 constexpr int kList = kSampleList;
 constexpr int kRank = 256;          // tokens ranked against each other at once
@@ -231,6 +230,20 @@ __device__ __forceinline__ double row_max(const SampleArgs& a, int b) {
 // it, which read as minus infinity, and the piece that would cross the end of the whole
 // array is read element by element).
 constexpr int kPieces = 4;
+__device__ __forceinline__ f32x4 load_piece(const float* p, int64_t g, int64_t n) {
+    if (4 * g + 4 <= n) return *(const f32x4*)(p + 4 * g);
+    f32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = 4 * g + j < n ? p[4 * g + j] : 0.0f;
+    return v;
+}
+// Elements base .. base + 3 of which those outside [i0, i1) become minus infinity.
+__device__ __forceinline__ void mask_piece(f32x4& v, int base, int i0, int i1) {
+    if (base >= i0 && base + 4 <= i1) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (base + j < i0 || base + j >= i1) v[j] = -INFINITY;
+}
 struct Logits {
     const float* p;     // the array
     int64_t o, g1, n;   // the row's first element, the range's last piece + 1, the array's size
@@ -248,14 +261,7 @@ struct Logits {
 #pragma unroll
         for (int u = 0; u < kPieces; ++u) {
             const int64_t at = g + u * kThreads;
-            if (at < g1) {
-                if (4 * at + 4 <= n) {
-                    v[u] = *(const f32x4*)(p + 4 * at);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[u][j] = 4 * at + j < n ? p[4 * at + j] : 0.0f;
-                }
-            }
+            if (at < g1) v[u] = load_piece(p, at, n);
         }
     }
     // f(logit, index) for all of them; the first pieces were loaded by the constructor
@@ -267,11 +273,7 @@ struct Logits {
                 const int64_t at = g + u * kThreads;
                 if (at >= g1) break;
                 const int base = (int)(4 * at - o);
-                if (base < i0 || base + 4 > i1) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if ((uint32_t)(base + j - i0) >= (uint32_t)(i1 - i0)) v[u][j] = -INFINITY;
-                }
+                mask_piece(v[u], base, i0, i1);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) f(v[u][j], base + j);
             }
@@ -665,14 +667,16 @@ __device__ __forceinline__ void write_token(const SampleArgs& a, int b, int toke
     }
 }
 
-// PER: elements of a chunk per thread.
-template <int PER>
-__global__ __launch_bounds__(kPickThreads) void sample_pick_kernel(const SampleArgs a) {
-    constexpr int NT = kPickThreads, NW = NT / 64;
+// R: aligned 16-byte pieces of a chunk per thread, chunk / (4 NT) + 1 (a row that does not
+// start on a piece has one more).
+template <int NT, int R>
+__global__ __launch_bounds__(NT) void sample_pick_kernel(const SampleArgs a) {
+    constexpr int NW = NT / 64;
     constexpr int LPT = kList / NT;  // list entries per thread
     static_assert(kMaxChunks <= NT, "one chunk a thread");
     __shared__ Draw s;
     __shared__ unsigned long long s_chunk[kMaxChunks];
+    __shared__ uint64_t s_seg[R * NW];
     __shared__ int s_at;
     __shared__ uint64_t s_before;
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -724,7 +728,11 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick_kernel(const SampleA
     const uint64_t mine = tid < a.n_chunks ? s_chunk[tid] : 0;
     const uint64_t inc_w = wave_scan_u64(mine);
     if (lane == 63) s.sum[wave] = inc_w;
-    if (tid == 0) s_at = -1;
+    if (tid == 0) {
+        s_at = -1;
+        s.token = 0;
+        s.wt = 0;
+    }
     __syncthreads();
     uint64_t run = inc_w - mine, total = 0;
 #pragma unroll
@@ -743,21 +751,62 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick_kernel(const SampleA
     const int chunk = s_at;
     if (chunk >= 0) {  // (uniform; a row without a live logit has total 0 and token 0)
         const int i0 = chunk << a.chunk_sh;
-        float l[PER];
-        uint64_t w[PER];
+        const int i1 = min(a.V, i0 + (1 << a.chunk_sh));
+        const int64_t o = (int64_t)b * a.V, size = (int64_t)a.B * a.V;
+        const int64_t g0 = (o + i0) >> 2, g1 = (o + i1 + 3) >> 2;
+        f32x4 l[R];
+        uint64_t sum[R];
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int i = i0 + PER * tid + j;
-            l[j] = row[i < a.V ? i : a.V - 1];
+        for (int r = 0; r < R; ++r) {
+            const int64_t g = g0 + r * NT + tid;
+            l[r] = load_piece(a.logits, g < g1 ? g : g0, size);
         }
+        auto kept_weight = [&](float v, int i) {
+            const uint64_t w = weight(v, m, p.inv_t);
+            return w < p.w_min || place(v, i) < last ? 0 : w;
+        };
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int i = i0 + PER * tid + j;
-            w[j] = weight(l[j], m, p.inv_t);
-            if (i >= a.V || w[j] < p.w_min || place(l[j], i) < last) w[j] = 0;
+        for (int r = 0; r < R; ++r) {  // sums of 256 neighbouring elements, in index order
+            const int64_t g = g0 + r * NT + tid;
+            const int base = (int)(4 * g - o);
+            sum[r] = 0;
+            if (g < g1) {
+                mask_piece(l[r], base, i0, i1);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[r] += kept_weight(l[r][j], base + j);
+            }
+            const uint64_t t = wave_sum_u64(sum[r]);
+            if (lane == 0) s_seg[r * NW + wave] = t;
         }
-        find_drawn<NT, PER>(s, w, draw - s_before);
-        token = s.token >= 0 ? i0 + s.token : 0;
+        __syncthreads();
+        const uint64_t want = draw - s_before;
+        uint64_t before = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {  // (uniform over the wave)
+            uint64_t row_before = before;
+            for (int v = 0; v < NW; ++v) {
+                const uint64_t seg = s_seg[r * NW + v];
+                row_before += v < wave ? seg : 0;
+                before += seg;
+            }
+            if (row_before <= want && row_before + s_seg[r * NW + wave] > want) {
+                uint64_t at = row_before + wave_scan_u64(sum[r]) - sum[r];
+                if (at <= want && at + sum[r] > want) {  // one thread of the work group
+                    const int base = (int)(4 * (g0 + r * NT + tid) - o);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint64_t w = kept_weight(l[r][j], base + j);
+                        if (at <= want && at + w > want) {
+                            s.token = base + j;
+                            s.wt = w;
+                        }
+                        at += w;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        token = s.token;
         wt = s.wt;
     }
     write_token<NT>(a, b, token, wt, total);
@@ -853,11 +902,10 @@ hipError_t launch_sample(const SampleArgs& a, hipStream_t s) {
     sample_gather_kernel<<<grid, kThreads, 0, s>>>(a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     trace_point(s);
-    static_assert(kPickThreads == 512, "elements per thread below");
-    if (a.chunk_sh == 11) sample_pick_kernel<4><<<a.B, kPickThreads, 0, s>>>(a);
-    else if (a.chunk_sh == 12) sample_pick_kernel<8><<<a.B, kPickThreads, 0, s>>>(a);
-    else if (a.chunk_sh == 13) sample_pick_kernel<16><<<a.B, kPickThreads, 0, s>>>(a);
-    else sample_pick_kernel<32><<<a.B, kPickThreads, 0, s>>>(a);
+    if (a.chunk_sh == 11) sample_pick_kernel<512, 2><<<a.B, 512, 0, s>>>(a);
+    else if (a.chunk_sh == 12) sample_pick_kernel<512, 3><<<a.B, 512, 0, s>>>(a);
+    else if (a.chunk_sh == 13) sample_pick_kernel<1024, 3><<<a.B, 1024, 0, s>>>(a);
+    else sample_pick_kernel<1024, 5><<<a.B, 1024, 0, s>>>(a);
     trace_point(s);
     return hipGetLastError();
 }
