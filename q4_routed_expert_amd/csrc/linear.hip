@@ -133,6 +133,9 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(const LinearA
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int r = lane & 15, g = lane >> 4;
     const int N = a.N, K = a.K, T = a.T, G = gridDim.x;
+    // neighbouring units go to work groups of one XCD (group i runs on XCD i % 8), whose L2
+    // joins the half lines that two tiles write
+    const int b = (int)blockIdx.x, me = G % 8 == 0 ? (b & 7) * (G / 8) + (b >> 3) : b;
     // piece (token t, columns 8 c .. + 7) of x, 0 past the end; its place in a chunk or x
     auto x_piece = [&](int t, int col) {
         const bool live = t < T && col < K;
@@ -177,19 +180,19 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(const LinearA
 #pragma unroll
         for (int st = 0; st < kSteps; ++st) {
             if (!VEC && kc + st * kStep >= K) break;  // uniform
-            float s9, b;
+            float s9, bi;
             if constexpr (VEC) {  // group 2 st + (g >> 1): one half of word st
                 const int up = g & 2 ? 0 : 16;
                 s9 = __uint_as_float((v.s[st] << up) & 0xFFFF0000u) * 512.0f;
-                b = __uint_as_float((v.b[st] << up) & 0xFFFF0000u);
+                bi = __uint_as_float((v.b[st] << up) & 0xFFFF0000u);
             } else {
                 const bool live = kc + st * kStep + 32 * g < K;
                 s9 = live ? dq_scale(v.s1[st]) : 0.0f;
-                b = live ? bf16_to_f32(v.b1[st]) : 0.0f;
+                bi = live ? bf16_to_f32(v.b1[st]) : 0.0f;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bf16x8 wv = dequant8(v.q[st][j], s9, b);
+                const bf16x8 wv = dequant8(v.q[st][j], s9, bi);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -200,9 +203,9 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(const LinearA
             }
         }
     };
-    int u = RES ? wave * G + (int)blockIdx.x : (int)blockIdx.x, kc = 0, buf = 0;
-    Weights cur, nxt;
-    if (u < units) load(cur, u, 0);
+    int u = RES ? wave * G + me : me, kc = 0, buf = 0;
+    Weights w0, w1;
+    if (u < units) load(w0, u, 0);
     if constexpr (RES) {
         const int per = (K + kStep - 1) / kStep * 16;  // pieces per token
         for (int i = tid; i < NB * per; i += THREADS) {
@@ -217,7 +220,8 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(const LinearA
         }
     }
     __syncthreads();
-    while (u < units) {  // (RES: by wave; else by work group)
+    // one chunk with `cur` while `nxt` is loaded
+    auto chunk = [&](const Weights& cur, Weights& nxt) {
         const bool last = kc + kChunk >= K;
         const int u2 = last ? u + stride : u, kc2 = last ? 0 : kc + kChunk;
         const bool more = u2 < units;
@@ -249,9 +253,13 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(const LinearA
                 __syncthreads();
             }
         }
-        cur = nxt;
         u = u2;
         kc = kc2;
+    };
+    while (u < units) {  // (u: by wave with RES, by work group else)
+        chunk(w0, w1);
+        if (u >= units) break;
+        chunk(w1, w0);
     }
 }
 
