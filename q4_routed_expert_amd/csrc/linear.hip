@@ -176,31 +176,41 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(const LinearA
     f32x4 acc[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // One chunk.  The operands of x for product q + 1 are read before the weights of
+    // product q are dequantised, so that their latency runs under that.
     auto products = [&](const Weights& v, const u32x4* x, int kc) {
+        const u32x4* xl = x + g * TB + (r & (TB - 1));
+        const int steps = VEC ? kSteps : min(kSteps, (K - kc + kStep - 1) / kStep);
+        u32x4 xo[2][NT];
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
-            if (!VEC && kc + st * kStep >= K) break;  // uniform
-            float s9, bi;
-            if constexpr (VEC) {  // group 2 st + (g >> 1): one half of word st
-                const int up = g & 2 ? 0 : 16;
-                s9 = __uint_as_float((v.s[st] << up) & 0xFFFF0000u) * 512.0f;
-                bi = __uint_as_float((v.b[st] << up) & 0xFFFF0000u);
-            } else {
-                const bool live = kc + st * kStep + 32 * g < K;
-                s9 = live ? dq_scale(v.s1[st]) : 0.0f;
-                bi = live ? bf16_to_f32(v.b1[st]) : 0.0f;
-            }
+        for (int n = 0; n < NT; ++n) xo[0][n] = xl[n * 4 * TB];
+        float s9 = 0.0f, bi = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bf16x8 wv = dequant8(v.q[st][j], s9, bi);
+        for (int q = 0; q < 4 * kSteps; ++q) {
+            const int st = q >> 2, j = q & 3;
+            if (!VEC && st >= steps) break;  // uniform
+            if (q + 1 < 4 * kSteps && (VEC || j < 3 || st + 1 < steps)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        wv,
-                        __builtin_bit_cast(bf16x8, x[st * kStepPieces + ((j * NT + n) * 4 + g) * TB +
-                                                     (r & (TB - 1))]),
-                        acc[n], 0, 0, 0);
+                    xo[(q + 1) & 1][n] = xl[((q + 1) >> 2) * kStepPieces + (((q + 1) & 3) * NT + n) * 4 * TB];
             }
+            __builtin_amdgcn_sched_barrier(0);
+            if (j == 0) {
+                if constexpr (VEC) {  // group 2 st + (g >> 1): one half of word st
+                    const int up = g & 2 ? 0 : 16;
+                    s9 = __uint_as_float((v.s[st] << up) & 0xFFFF0000u) * 512.0f;
+                    bi = __uint_as_float((v.b[st] << up) & 0xFFFF0000u);
+                } else {
+                    const bool live = kc + st * kStep + 32 * g < K;
+                    s9 = live ? dq_scale(v.s1[st]) : 0.0f;
+                    bi = live ? bf16_to_f32(v.b1[st]) : 0.0f;
+                }
+            }
+            const bf16x8 wv = dequant8(v.q[st][j], s9, bi);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8, xo[q & 1][n]),
+                                                                 acc[n], 0, 0, 0);
         }
     };
     int u = RES ? wave * G + me : me, kc = 0, buf = 0;
