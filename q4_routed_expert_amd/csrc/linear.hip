@@ -109,184 +109,241 @@ __global__ __launch_bounds__(KW * 64) void linear_split_kernel(const LinearArgs 
     store_tile<NT>(a, acc, row0, lane);
 }
 
-// Many rows.  x lies in LDS in operand order, [step][j][n][g][token] of 16 bytes, so that
-// a wave's read of one operand is contiguous; NB is the number of tokens it has room for
-// (8: lanes of tokens 8 .. 15 read those of 0 .. 7 again, their results are not stored).
-//   RES    all of x (NB K 2 <= 128 KB) is staged once; after that the waves run without
-//          barriers, each over its own tiles (wave w of group b: tiles w G + b, then every
-//          16 G, so that any number of tiles spreads over the CUs)
-//   else   one 512-column chunk of x at a time, double buffered, a barrier per chunk; a
-//          work group's waves take neighbouring tiles
-// The grid is one work group per CU; the next chunk's weights, across tiles too, are
-// loaded before the current chunk's products.
-//   VEC    K is a multiple of 512: a chunk's eight scales of a row are one aligned load
+// Many rows.  x lies in LDS as [step][16 tokens][8 columns][token] of 16 bytes: the eight
+// lanes that the LDS serves at once read (r) and write (neighbouring tokens) 128
+// neighbouring bytes.  NB is the number of tokens it has room for (8: lanes of tokens
+// 8 .. 15 read those of 0 .. 7 again, their results are not stored).
+// K goes in chunks of 512 columns, and a row's sum is two: over the first and over the
+// second half of every chunk, added at the end.  The grid is one work group of 16 waves
+// per CU, and the next chunk's weights, across tiles too, are loaded before the current
+// chunk's products.
+//   kWave     all of x (NB K 2 <= 128 KB) is staged once; after that the waves run without
+//             barriers, each over its own tiles (wave w of group b: tiles w G + b, then
+//             every 16 G, so that any number of tiles spreads over the CUs)
+//   kPair     the same with two waves per tile, one for each half of the chunks: where
+//             the tiles would leave half of the waves idle
+//   kChunked  x is larger: one chunk of it at a time, double buffered, a barrier per
+//             chunk; a work group's pairs of waves take eight neighbouring tiles
+// VEC: K is a multiple of 512, so a chunk's eight scales of a row are one aligned load.
 constexpr int kChunk = 512;
 constexpr int kSteps = kChunk / kStep;
 constexpr int kCus = 256;
+constexpr int kThreads = 1024;
+enum Mode { kWave, kPair, kChunked };
 
-template <int NB, int WAVES, bool RES, bool VEC>
-__global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(const LinearArgs a) {
-    constexpr int NT = (NB + 15) / 16, TB = NB < 16 ? NB : 16, THREADS = WAVES * 64;
+template <int NB, Mode MODE, bool VEC>
+__global__ __launch_bounds__(kThreads) void linear_stream_kernel(const LinearArgs a) {
+    constexpr int NT = (NB + 15) / 16, TB = NB < 16 ? NB : 16;
     constexpr int kStepPieces = NB * 16, kChunkPieces = NB * 64;
-    constexpr int XP = RES ? 1 : kChunkPieces / THREADS;  // pieces of a chunk per thread
-    __shared__ u32x4 s_x[RES ? 8192 : 2 * kChunkPieces];
+    constexpr int XP = MODE == kChunked ? (kChunkPieces + kThreads - 1) / kThreads : 1;  // pieces per thread
+    constexpr int HS = MODE == kWave ? kSteps : kSteps / 2;  // steps of a chunk per wave
+    constexpr int SUMS = MODE == kWave ? 2 : 1;
+    constexpr int SLOTS = MODE == kWave ? 16 : 8;            // tiles of a work group at a time
+    __shared__ u32x4 s_x[MODE == kChunked ? 2 * kChunkPieces : 8192];
+    __shared__ f32x4 s_sum[MODE == kWave ? 1 : SLOTS * NT * 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int slot = wave % SLOTS, half = wave / SLOTS;
     const int r = lane & 15, g = lane >> 4;
     const int N = a.N, K = a.K, T = a.T, G = gridDim.x;
     // neighbouring units go to work groups of one XCD (group i runs on XCD i % 8), whose L2
     // joins the half lines that two tiles write
     const int b = (int)blockIdx.x, me = G % 8 == 0 ? (b & 7) * (G / 8) + (b >> 3) : b;
-    // piece (token t, columns 8 c .. + 7) of x, 0 past the end; its place in a chunk or x
+    // columns col .. + 7 of token t, 0 past the ends; their place in a chunk, or in x
     auto x_piece = [&](int t, int col) {
         const bool live = t < T && col < K;
         const u32x4 v = *(const u32x4*)(a.x + (live ? (size_t)t * K + col : 0));
         return live ? v : u32x4{0u, 0u, 0u, 0u};
     };
-    auto x_place = [&](int t, int c) {  // columns 128 (c >> 4) + 32 gg + 8 j
-        const int gg = (c >> 2) & 3, j = c & 3;
-        return (c >> 4) * kStepPieces + ((j * NT + (t >> 4)) * 4 + gg) * TB + (t & (TB - 1));
+    // piece i of x or of a chunk: eight tokens, then eight neighbouring pieces of a row (128
+    // bytes), then the next tokens; its place
+    auto x_token = [](int i) { return (i & 7) + 8 * ((i >> 6) % (NB / 8)); };
+    auto x_col = [](int i) { return ((i >> 3) & 7) + 8 * ((i >> 6) / (NB / 8)); };
+    auto x_place = [&](int i) {
+        const int t = x_token(i), c = x_col(i);
+        return ((c >> 4) * NT + (t >> 4)) * 16 * TB + (c & 15) * TB + (t & (TB - 1));
     };
     struct Weights {
-        u32x4 q[kSteps];
-        u32x4 s, b;                       // VEC: the chunk's eight scales, biases
-        uint16_t s1[kSteps], b1[kSteps];  // else: this lane's of each step
+        u32x4 q[HS];
+        uint32_t s[HS], b[HS];  // VEC: the step's two scales, biases; else this lane's one
     };
-    const int unit_rows = RES ? 16 : 16 * WAVES;
-    const int units = (N + unit_rows - 1) / unit_rows, stride = RES ? WAVES * G : G;
-    auto row_of = [&](int u) { return RES ? u * 16 : (u * WAVES + wave) * 16; };
+    constexpr int kUnitRows = MODE == kChunked ? 16 * SLOTS : 16;
+    const int units = (N + kUnitRows - 1) / kUnitRows, stride = MODE == kChunked ? G : SLOTS * G;
+    auto row_of = [&](int u) { return MODE == kChunked ? (u * SLOTS + slot) * 16 : u * 16; };
+    const int st0 = half * HS;
     auto load = [&](Weights& v, int u, int kc) {
         const int row0 = row_of(u) + r;
         const size_t row = (size_t)(row0 < N ? row0 : N - 1);  // clamped, valid
         const uint32_t* qp = a.w.q + row * (size_t)(K / 8);
         const size_t so = row * (size_t)(K / kGroup);
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
-            const int k0 = kc + st * kStep + 32 * g, kk = VEC || k0 < K ? k0 : 0;  // clamped, valid
+        for (int st = 0; st < HS; ++st) {
+            const int k0 = kc + (st0 + st) * kStep + 32 * g, kk = VEC || k0 < K ? k0 : 0;  // clamped, valid
             v.q[st] = *(const u32x4*)(qp + kk / 8);
             if constexpr (!VEC) {
-                v.s1[st] = a.w.scale[so + kk / kGroup];
-                v.b1[st] = a.w.bias[so + kk / kGroup];
+                v.s[st] = a.w.scale[so + kk / kGroup];
+                v.b[st] = a.w.bias[so + kk / kGroup];
             }
         }
         if constexpr (VEC) {
-            v.s = *(const u32x4*)(a.w.scale + so + kc / kGroup);
-            v.b = *(const u32x4*)(a.w.bias + so + kc / kGroup);
+            const size_t o = so + kc / kGroup + 2 * st0;
+            if constexpr (HS == 4) {
+                const u32x4 s = *(const u32x4*)(a.w.scale + o), bb = *(const u32x4*)(a.w.bias + o);
+#pragma unroll
+                for (int st = 0; st < HS; ++st) {
+                    v.s[st] = s[st];
+                    v.b[st] = bb[st];
+                }
+            } else {
+                const uint2 s = *(const uint2*)(a.w.scale + o), bb = *(const uint2*)(a.w.bias + o);
+                v.s[0] = s.x, v.s[1] = s.y, v.b[0] = bb.x, v.b[1] = bb.y;
+            }
         }
     };
-    f32x4 acc[NT];
+    f32x4 acc[SUMS][NT];
+    auto clear = [&] {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int h = 0; h < SUMS; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[h][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    };
     // One chunk.  The operands of x for product q + 1 are read before the weights of
     // product q are dequantised, so that their latency runs under that.
     auto products = [&](const Weights& v, const u32x4* x, int kc) {
-        const u32x4* xl = x + g * TB + (r & (TB - 1));
-        const int steps = VEC ? kSteps : min(kSteps, (K - kc + kStep - 1) / kStep);
+        const u32x4* xl = x + st0 * kStepPieces + 4 * g * TB + (r & (TB - 1));
+        const int steps = VEC ? HS : max(0, min(HS, (K - kc + kStep - 1) / kStep - st0));
         u32x4 xo[2][NT];
+        if (VEC || steps > 0) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) xo[0][n] = xl[n * 4 * TB];
+            for (int n = 0; n < NT; ++n) xo[0][n] = xl[n * 16 * TB];
+        }
         float s9 = 0.0f, bi = 0.0f;
 #pragma unroll
-        for (int q = 0; q < 4 * kSteps; ++q) {
-            const int st = q >> 2, j = q & 3;
+        for (int q = 0; q < 4 * HS; ++q) {
+            const int st = q >> 2, j = q & 3, h = SUMS == 2 ? st >> 1 : 0;
             if (!VEC && st >= steps) break;  // uniform
-            if (q + 1 < 4 * kSteps && (VEC || j < 3 || st + 1 < steps)) {
+            if (q + 1 < 4 * HS && (VEC || j < 3 || st + 1 < steps)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    xo[(q + 1) & 1][n] = xl[((q + 1) >> 2) * kStepPieces + (((q + 1) & 3) * NT + n) * 4 * TB];
+                    xo[(q + 1) & 1][n] = xl[((q + 1) >> 2) * kStepPieces + n * 16 * TB + ((q + 1) & 3) * TB];
             }
             __builtin_amdgcn_sched_barrier(0);
             if (j == 0) {
-                if constexpr (VEC) {  // group 2 st + (g >> 1): one half of word st
+                if constexpr (VEC) {  // group 2 st + (g >> 1): one half of the word
                     const int up = g & 2 ? 0 : 16;
                     s9 = __uint_as_float((v.s[st] << up) & 0xFFFF0000u) * 512.0f;
                     bi = __uint_as_float((v.b[st] << up) & 0xFFFF0000u);
                 } else {
-                    const bool live = kc + st * kStep + 32 * g < K;
-                    s9 = live ? dq_scale(v.s1[st]) : 0.0f;
-                    bi = live ? bf16_to_f32(v.b1[st]) : 0.0f;
+                    const bool live = kc + (st0 + st) * kStep + 32 * g < K;
+                    s9 = live ? dq_scale(v.s[st]) : 0.0f;
+                    bi = live ? bf16_to_f32(v.b[st]) : 0.0f;
                 }
             }
             const bf16x8 wv = dequant8(v.q[st][j], s9, bi);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8, xo[q & 1][n]),
-                                                                 acc[n], 0, 0, 0);
+                acc[h][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    wv, __builtin_bit_cast(bf16x8, xo[q & 1][n]), acc[h][n], 0, 0, 0);
         }
     };
-    int u = RES ? wave * G + me : me, kc = 0, buf = 0;
+    int u = MODE == kChunked ? me : slot * G + me, kc = 0, buf = 0;
     Weights w0, w1;
-    if (u < units) load(w0, u, 0);
-    if constexpr (RES) {
-        const int per = (K + kStep - 1) / kStep * 16;  // pieces per token
-        for (int i = tid; i < NB * per; i += THREADS) {
-            const int t = i / per, c = i - t * per;
-            s_x[x_place(t, c)] = x_piece(t, 8 * c);
-        }
-    } else {
+    load(w0, u, 0);
+    clear();
+    if constexpr (MODE == kChunked) {
 #pragma unroll
         for (int p = 0; p < XP; ++p) {
-            const int i = tid + p * THREADS, t = i >> 6, c = i & 63;
-            s_x[x_place(t, c)] = x_piece(t, 8 * c);
+            const int i = tid + p * kThreads;
+            if (i < kChunkPieces) s_x[x_place(i)] = x_piece(x_token(i), 8 * x_col(i));
         }
+    } else {
+        const int pieces = (K + kStep - 1) / kStep * kStepPieces;
+        for (int i = tid; i < pieces; i += kThreads) s_x[x_place(i)] = x_piece(x_token(i), 8 * x_col(i));
     }
     __syncthreads();
     // one chunk with `cur` while `nxt` is loaded
     auto chunk = [&](const Weights& cur, Weights& nxt) {
         const bool last = kc + kChunk >= K;
         const int u2 = last ? u + stride : u, kc2 = last ? 0 : kc + kChunk;
-        const bool more = u2 < units;
+        // (loaded whether they will be used or not, from a valid place: with the loads in a
+        // branch the compiler cannot count those in flight and waits for all of them here)
+        load(nxt, u2, kc2);
         u32x4 xn[XP];
-        if (more) {
-            load(nxt, u2, kc2);
-            if constexpr (!RES) {
+        if constexpr (MODE == kChunked) {
 #pragma unroll
-                for (int p = 0; p < XP; ++p) {
-                    const int i = tid + p * THREADS;
-                    xn[p] = x_piece(i >> 6, kc2 + 8 * (i & 63));
-                }
+            for (int p = 0; p < XP; ++p) {
+                const int i = tid + p * kThreads;
+                xn[p] = x_piece(x_token(i), kc2 + 8 * x_col(i));
             }
         }
-        products(cur, RES ? s_x + kc / kStep * kStepPieces : s_x + buf * kChunkPieces, kc);
-        if (last) {
-            store_tile<NT>(a, acc, row_of(u), lane);
+        products(cur, MODE == kChunked ? s_x + buf * kChunkPieces : s_x + kc / kStep * kStepPieces, kc);
+        if (MODE == kWave && last) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int n = 0; n < NT; ++n) acc[0][n] += acc[SUMS - 1][n];
+            store_tile<NT>(a, acc[0], row_of(u), lane);
+            clear();
         }
-        if constexpr (!RES) {
-            if (more) {
-                buf ^= 1;  // (read last before the previous barrier)
+        if constexpr (MODE == kChunked) {
+            if (last && half == 1) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s_sum[(slot * NT + n) * 64 + lane] = acc[0][n];
+            }
+            buf ^= 1;  // (read last before the previous barrier)
+            {
 #pragma unroll
                 for (int p = 0; p < XP; ++p) {
-                    const int i = tid + p * THREADS;
-                    s_x[buf * kChunkPieces + x_place(i >> 6, i & 63)] = xn[p];
+                    const int i = tid + p * kThreads;
+                    if (i < kChunkPieces) s_x[buf * kChunkPieces + x_place(i)] = xn[p];
                 }
-                __syncthreads();
+            }
+            __syncthreads();
+            if (last) {
+                if (half == 0) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) acc[0][n] += s_sum[(slot * NT + n) * 64 + lane];
+                    store_tile<NT>(a, acc[0], row_of(u), lane);
+                }
+                clear();
+                if (K <= kChunk) __syncthreads();  // s_sum is written again before the next barrier
             }
         }
         u = u2;
         kc = kc2;
     };
-    while (u < units) {  // (u: by wave with RES, by work group else)
+    const int u_first = u;
+    while (u < units) {  // (by wave; kChunked: by work group)
         chunk(w0, w1);
         if (u >= units) break;
         chunk(w1, w0);
     }
+    if constexpr (MODE == kPair) {  // (one tile per pair)
+        if (u_first < units && half == 1) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s_sum[(slot * NT + n) * 64 + lane] = acc[0][n];
+        }
+        __syncthreads();
+        if (u_first < units && half == 0) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[0][n] += s_sum[(slot * NT + n) * 64 + lane];
+            store_tile<NT>(a, acc[0], row_of(u_first), lane);
+        }
+    }
 }
 
-template <int NB, bool RES>
+template <int NB, Mode MODE>
 void launch_stream(const LinearArgs& a, hipStream_t s) {
-    constexpr int WAVES = RES ? 16 : 8;
-    const int tiles = (a.N + 15) / 16, units = RES ? tiles : (tiles + WAVES - 1) / WAVES;
+    const int tiles = (a.N + 15) / 16, units = MODE == kChunked ? (tiles + 7) / 8 : tiles;
     const int grid = units < kCus ? units : kCus;
-    if (a.K % kChunk == 0) linear_stream_kernel<NB, WAVES, RES, true><<<grid, WAVES * 64, 0, s>>>(a);
-    else linear_stream_kernel<NB, WAVES, RES, false><<<grid, WAVES * 64, 0, s>>>(a);
+    if (a.K % kChunk == 0) linear_stream_kernel<NB, MODE, true><<<grid, kThreads, 0, s>>>(a);
+    else linear_stream_kernel<NB, MODE, false><<<grid, kThreads, 0, s>>>(a);
 }
 
 template <int NB>
 void launch(const LinearArgs& a, hipStream_t s) {
+    const bool fits = NB * ((a.K + kStep - 1) / kStep) <= 512;  // x in 128 KB
     if (a.N < 16384) linear_split_kernel<(NB + 15) / 16, 4><<<(a.N + 15) / 16, 256, 0, s>>>(a);
-    else if (NB * ((a.K + kStep - 1) / kStep) <= 512) launch_stream<NB, true>(a, s);
-    else if constexpr (NB > 8) launch_stream<NB, false>(a, s);
+    else if (fits && a.N <= 16 * 8 * kCus) launch_stream<NB, kPair>(a, s);
+    else if (fits) launch_stream<NB, kWave>(a, s);
+    else if constexpr (NB > 8) launch_stream<NB, kChunked>(a, s);
 }
 
 }  // namespace
