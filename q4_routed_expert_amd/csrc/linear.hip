@@ -124,14 +124,20 @@ __global__ __launch_bounds__(KW * 64) void linear_split_kernel(const LinearArgs 
 //             the tiles would leave half of the waves idle
 //   kChunked  x is larger: one chunk of it at a time, double buffered, a barrier per
 //             chunk; a work group's pairs of waves take eight neighbouring tiles
-// VEC: K is a multiple of 512, so a chunk's eight scales of a row are one aligned load.
+// Scales and biases come in blocks of 2048 columns: lane 4 i + c loads those of chunk c of
+// row i (16 bytes, so 64 neighbouring bytes a row), and each product's lanes fetch theirs
+// from that lane.  Loaded per chunk, 16 bytes from each of 16 rows, they cost as much time
+// as the codes: the vector caches serve cache lines, not bytes (measured at N = 30011,
+// K = 8192, one token: 46.5 us, and 35 without any scale loads).
+// FULL: K is a multiple of 2048 (no branches between the loads).  VEC: of 512 (a chunk's
+// eight scales are one aligned load).
 constexpr int kChunk = 512;
 constexpr int kSteps = kChunk / kStep;
 constexpr int kCus = 256;
 constexpr int kThreads = 1024;
 enum Mode { kWave, kPair, kChunked };
 
-template <int NB, Mode MODE, bool VEC>
+template <int NB, Mode MODE, bool FULL, bool VEC>
 __global__ __launch_bounds__(kThreads) void linear_stream_kernel(const LinearArgs a) {
     constexpr int NT = (NB + 15) / 16, TB = NB < 16 ? NB : 16;
     constexpr int kStepPieces = NB * 16, kChunkPieces = NB * 64;
@@ -162,9 +168,11 @@ __global__ __launch_bounds__(kThreads) void linear_stream_kernel(const LinearArg
         const int t = x_token(i), c = x_col(i);
         return ((c >> 4) * NT + (t >> 4)) * 16 * TB + (c & 15) * TB + (t & (TB - 1));
     };
+    struct Scales {
+        u32x4 s, b;  // eight groups each
+    };
     struct Weights {
         u32x4 q[HS];
-        uint32_t s[HS], b[HS];  // VEC: the step's two scales, biases; else this lane's one
     };
     constexpr int kUnitRows = MODE == kChunked ? 16 * SLOTS : 16;
     const int units = (N + kUnitRows - 1) / kUnitRows, stride = MODE == kChunked ? G : SLOTS * G;
@@ -174,28 +182,27 @@ __global__ __launch_bounds__(kThreads) void linear_stream_kernel(const LinearArg
         const int row0 = row_of(u) + r;
         const size_t row = (size_t)(row0 < N ? row0 : N - 1);  // clamped, valid
         const uint32_t* qp = a.w.q + row * (size_t)(K / 8);
-        const size_t so = row * (size_t)(K / kGroup);
 #pragma unroll
         for (int st = 0; st < HS; ++st) {
-            const int k0 = kc + (st0 + st) * kStep + 32 * g, kk = VEC || k0 < K ? k0 : 0;  // clamped, valid
+            const int k0 = kc + (st0 + st) * kStep + 32 * g, kk = VEC && FULL || k0 < K ? k0 : 0;  // clamped, valid
             v.q[st] = *(const u32x4*)(qp + kk / 8);
-            if constexpr (!VEC) {
-                v.s[st] = a.w.scale[so + kk / kGroup];
-                v.b[st] = a.w.bias[so + kk / kGroup];
-            }
         }
+    };
+    // the scales of the 2048 columns from kb on (groups past the row's end: its last)
+    auto load_scales = [&](Scales& v, int u, int kb) {
+        const int row0 = row_of(u) + (lane >> 2);
+        const int groups = K / kGroup, g0 = kb / kGroup + 8 * (lane & 3);
+        const size_t so = (size_t)(row0 < N ? row0 : N - 1) * (size_t)groups;  // clamped, valid
         if constexpr (VEC) {
-            const size_t o = so + kc / kGroup + 2 * st0;
-            if constexpr (HS == 4) {
-                const u32x4 s = *(const u32x4*)(a.w.scale + o), bb = *(const u32x4*)(a.w.bias + o);
+            const size_t o = so + (FULL || g0 < groups ? g0 : 0);
+            v.s = *(const u32x4*)(a.w.scale + o);
+            v.b = *(const u32x4*)(a.w.bias + o);
+        } else {
 #pragma unroll
-                for (int st = 0; st < HS; ++st) {
-                    v.s[st] = s[st];
-                    v.b[st] = bb[st];
-                }
-            } else {
-                const uint2 s = *(const uint2*)(a.w.scale + o), bb = *(const uint2*)(a.w.bias + o);
-                v.s[0] = s.x, v.s[1] = s.y, v.b[0] = bb.x, v.b[1] = bb.y;
+            for (int i = 0; i < 4; ++i) {
+                const size_t o0 = so + min(g0 + 2 * i, groups - 1), o1 = so + min(g0 + 2 * i + 1, groups - 1);
+                v.s[i] = a.w.scale[o0] | (uint32_t)a.w.scale[o1] << 16;
+                v.b[i] = a.w.bias[o0] | (uint32_t)a.w.bias[o1] << 16;
             }
         }
     };
@@ -208,11 +215,23 @@ __global__ __launch_bounds__(kThreads) void linear_stream_kernel(const LinearArg
     };
     // One chunk.  The operands of x for product q + 1 are read before the weights of
     // product q are dequantised, so that their latency runs under that.
-    auto products = [&](const Weights& v, const u32x4* x, int kc) {
+    auto products = [&](const Weights& v, const Scales& sc, int c, const u32x4* x, int kc) {
         const u32x4* xl = x + st0 * kStepPieces + 4 * g * TB + (r & (TB - 1));
         const int steps = VEC ? HS : max(0, min(HS, (K - kc + kStep - 1) / kStep - st0));
-        u32x4 xo[2][NT];
-        if (VEC || steps > 0) {
+        // word st0 + st of the chunk's scales holds the step's two groups
+        uint32_t sw[HS], bw[HS];
+#pragma unroll
+        for (int st = 0; st < HS; ++st) {
+            const uint32_t s = HS == 4 ? sc.s[st] : half ? sc.s[2 + st] : sc.s[st];
+            const uint32_t b = HS == 4 ? sc.b[st] : half ? sc.b[2 + st] : sc.b[st];
+            sw[st] = (uint32_t)__builtin_amdgcn_ds_bpermute(16 * r + 4 * c, (int)s);
+            bw[st] = (uint32_t)__builtin_amdgcn_ds_bpermute(16 * r + 4 * c, (int)b);
+        }
+        // (four operands of two products do not fit the registers of 16 waves: read for the
+        // same product then, ahead of its dequantisation)
+        constexpr int AHEAD = NT == 4 ? 0 : 1;
+        u32x4 xo[1 + AHEAD][NT];
+        if (AHEAD && (VEC || steps > 0)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) xo[0][n] = xl[n * 16 * TB];
         }
@@ -221,32 +240,31 @@ __global__ __launch_bounds__(kThreads) void linear_stream_kernel(const LinearArg
         for (int q = 0; q < 4 * HS; ++q) {
             const int st = q >> 2, j = q & 3, h = SUMS == 2 ? st >> 1 : 0;
             if (!VEC && st >= steps) break;  // uniform
-            if (q + 1 < 4 * HS && (VEC || j < 3 || st + 1 < steps)) {
+            if (q + AHEAD < 4 * HS && (!AHEAD || VEC || j < 3 || st + 1 < steps)) {
+                const int qa = q + AHEAD;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    xo[(q + 1) & 1][n] = xl[((q + 1) >> 2) * kStepPieces + n * 16 * TB + ((q + 1) & 3) * TB];
+                    xo[qa & AHEAD][n] = xl[(qa >> 2) * kStepPieces + n * 16 * TB + (qa & 3) * TB];
             }
             __builtin_amdgcn_sched_barrier(0);
-            if (j == 0) {
-                if constexpr (VEC) {  // group 2 st + (g >> 1): one half of the word
-                    const int up = g & 2 ? 0 : 16;
-                    s9 = __uint_as_float((v.s[st] << up) & 0xFFFF0000u) * 512.0f;
-                    bi = __uint_as_float((v.b[st] << up) & 0xFFFF0000u);
-                } else {
-                    const bool live = kc + (st0 + st) * kStep + 32 * g < K;
-                    s9 = live ? dq_scale(v.s[st]) : 0.0f;
-                    bi = live ? bf16_to_f32(v.b[st]) : 0.0f;
-                }
+            if (j == 0) {  // group 2 st + (g >> 1): one half of the word
+                const int up = g & 2 ? 0 : 16;
+                s9 = __uint_as_float((sw[st] << up) & 0xFFFF0000u) * 512.0f;
+                bi = __uint_as_float((bw[st] << up) & 0xFFFF0000u);
+                if (!VEC && kc + (st0 + st) * kStep + 32 * g >= K) s9 = bi = 0.0f;  // half a step
             }
             const bf16x8 wv = dequant8(v.q[st][j], s9, bi);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 acc[h][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    wv, __builtin_bit_cast(bf16x8, xo[q & 1][n]), acc[h][n], 0, 0, 0);
+                    wv, __builtin_bit_cast(bf16x8, xo[q & AHEAD][n]), acc[h][n], 0, 0, 0);
         }
     };
-    int u = MODE == kChunked ? me : slot * G + me, kc = 0, buf = 0;
+    int u = MODE == kChunked ? me : slot * G + me, buf = 0;
+    const int u_first = u;
     Weights w0, w1;
+    Scales sc, sc_next;
+    load_scales(sc, u, 0);
     load(w0, u, 0);
     clear();
     if constexpr (MODE == kChunked) {
@@ -260,60 +278,71 @@ __global__ __launch_bounds__(kThreads) void linear_stream_kernel(const LinearArg
         for (int i = tid; i < pieces; i += kThreads) s_x[x_place(i)] = x_piece(x_token(i), 8 * x_col(i));
     }
     __syncthreads();
-    // one chunk with `cur` while `nxt` is loaded
-    auto chunk = [&](const Weights& cur, Weights& nxt) {
+    // Chunk c of the block at kb with `cur`, while the next chunk is loaded to `nxt`.  (Loads
+    // are made whether they will be used or not, from a valid place: with the loads in a
+    // branch the compiler cannot count those in flight and waits for all of them.)
+    auto chunk = [&](int c, int kb, int u2, const Weights& cur, Weights& nxt) {
+        const int kc = kb + c * kChunk;
         const bool last = kc + kChunk >= K;
-        const int u2 = last ? u + stride : u, kc2 = last ? 0 : kc + kChunk;
-        // (loaded whether they will be used or not, from a valid place: with the loads in a
-        // branch the compiler cannot count those in flight and waits for all of them here)
-        load(nxt, u2, kc2);
+        const bool dummy = !FULL && kc >= K;  // uniform; evens the number of chunks
+        const bool block_end = c == 3 || (!FULL && c == 1 && kc + kChunk >= K);
+        const int un = block_end ? u2 : u, kn = block_end ? (kb + 2048 < K ? kb + 2048 : 0) : kc + kChunk;
+        load(nxt, un, kn);
         u32x4 xn[XP];
         if constexpr (MODE == kChunked) {
 #pragma unroll
             for (int p = 0; p < XP; ++p) {
                 const int i = tid + p * kThreads;
-                xn[p] = x_piece(x_token(i), kc2 + 8 * x_col(i));
+                xn[p] = x_piece(x_token(i), kn + 8 * x_col(i));
             }
         }
-        products(cur, MODE == kChunked ? s_x + buf * kChunkPieces : s_x + kc / kStep * kStepPieces, kc);
-        if (MODE == kWave && last) {
+        if (!dummy)
+            products(cur, sc, c, MODE == kChunked ? s_x + buf * kChunkPieces : s_x + kc / kStep * kStepPieces,
+                     kc);
+        if (MODE == kWave && last && !dummy) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) acc[0][n] += acc[SUMS - 1][n];
             store_tile<NT>(a, acc[0], row_of(u), lane);
             clear();
         }
         if constexpr (MODE == kChunked) {
-            if (last && half == 1) {
+            if (last && !dummy && half == 1) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) s_sum[(slot * NT + n) * 64 + lane] = acc[0][n];
             }
             buf ^= 1;  // (read last before the previous barrier)
-            {
 #pragma unroll
-                for (int p = 0; p < XP; ++p) {
-                    const int i = tid + p * kThreads;
-                    if (i < kChunkPieces) s_x[buf * kChunkPieces + x_place(i)] = xn[p];
-                }
+            for (int p = 0; p < XP; ++p) {
+                const int i = tid + p * kThreads;
+                if (i < kChunkPieces) s_x[buf * kChunkPieces + x_place(i)] = xn[p];
             }
             __syncthreads();
-            if (last) {
+            if (last && !dummy) {
                 if (half == 0) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n) acc[0][n] += s_sum[(slot * NT + n) * 64 + lane];
                     store_tile<NT>(a, acc[0], row_of(u), lane);
                 }
                 clear();
-                if (K <= kChunk) __syncthreads();  // s_sum is written again before the next barrier
+                // (s_sum is written again after another barrier at least: a tile has an even
+                // number of chunks, dummies included)
             }
         }
-        u = u2;
-        kc = kc2;
     };
-    const int u_first = u;
+    int kb = 0;
     while (u < units) {  // (by wave; kChunked: by work group)
-        chunk(w0, w1);
-        if (u >= units) break;
-        chunk(w1, w0);
+        const bool row_end = kb + 2048 >= K;
+        const int u2 = row_end ? u + stride : u, kb2 = row_end ? 0 : kb + 2048;
+        load_scales(sc_next, u2, kb2);
+        chunk(0, kb, u2, w0, w1);
+        chunk(1, kb, u2, w1, w0);
+        if (FULL || kb + 2 * kChunk < K) {
+            chunk(2, kb, u2, w0, w1);
+            chunk(3, kb, u2, w1, w0);
+        }
+        sc = sc_next;
+        u = u2;
+        kb = kb2;
     }
     if constexpr (MODE == kPair) {  // (one tile per pair)
         if (u_first < units && half == 1) {
@@ -333,8 +362,9 @@ template <int NB, Mode MODE>
 void launch_stream(const LinearArgs& a, hipStream_t s) {
     const int tiles = (a.N + 15) / 16, units = MODE == kChunked ? (tiles + 7) / 8 : tiles;
     const int grid = units < kCus ? units : kCus;
-    if (a.K % kChunk == 0) linear_stream_kernel<NB, MODE, true><<<grid, kThreads, 0, s>>>(a);
-    else linear_stream_kernel<NB, MODE, false><<<grid, kThreads, 0, s>>>(a);
+    if (a.K % 2048 == 0) linear_stream_kernel<NB, MODE, true, true><<<grid, kThreads, 0, s>>>(a);
+    else if (a.K % kChunk == 0) linear_stream_kernel<NB, MODE, false, true><<<grid, kThreads, 0, s>>>(a);
+    else linear_stream_kernel<NB, MODE, false, false><<<grid, kThreads, 0, s>>>(a);
 }
 
 template <int NB>
