@@ -27,15 +27,15 @@ namespace {
 
 constexpr int kStep = 128;  // columns per wave and step
 
-// D of the 16x16 product: lane (c = lane & 15, g) holds token 16 n + c, rows
+// D of the 16x16 products: lane (c = lane & 15, g) holds token t0 + 16 n + c, rows
 // row0 + 4 g .. + 3.
 template <int NT>
-__device__ __forceinline__ void store_tile(const LinearArgs& a, const f32x4 (&acc)[NT], int row0, int lane) {
+__device__ __forceinline__ void store_tile(const LinearArgs& a, const f32x4 (&acc)[NT], int row0, int t0, int lane) {
     const int c = lane & 15, o = row0 + 4 * (lane >> 4);
     const int N = a.N;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int t = 16 * n + c;
+        const int t = t0 + 16 * n + c;
         if (t >= a.T) continue;
         const size_t at = (size_t)t * N + o;
         if (o + 4 <= N && (N & 3) == 0) {  // four neighbours, aligned
@@ -54,59 +54,75 @@ __device__ __forceinline__ void store_tile(const LinearArgs& a, const f32x4 (&ac
     }
 }
 
-// One 16-row tile per work group; its KW waves take the 128-column steps in
-// turn and their sums meet in LDS in wave order.
-template <int NT, int KW>
-__global__ __launch_bounds__(KW * 64) void linear_split_kernel(const LinearArgs a) {
-    __shared__ f32x4 red[KW - 1][NT][64];
+// RT tiles of 16 rows and one of 16 tokens per work group; its 16 waves take the 128-column
+// steps in turn and their sums meet in LDS in wave order.  (More tokens are more work
+// groups: each dequantises its weights again, but with few rows the CUs are there, and
+// what costs time is reading x, which every work group reads whole.)
+constexpr int kSplitWaves = 16;
+
+template <int RT>
+__global__ __launch_bounds__(kSplitWaves * 64) void linear_split_kernel(const LinearArgs a) {
+    __shared__ f32x4 red[kSplitWaves][RT][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int r = lane & 15, g = lane >> 4;
-    const int N = a.N, K = a.K, T = a.T;
-    const int row0 = blockIdx.x * 16;
-    const size_t row = (size_t)(row0 + r < N ? row0 + r : N - 1);  // clamped, valid
-    const uint32_t* qp = a.w.q + row * (size_t)(K / 8);
-    const uint16_t* sp = a.w.scale + row * (size_t)(K / kGroup);
-    const uint16_t* bp = a.w.bias + row * (size_t)(K / kGroup);
-    f32x4 acc[NT];
+    const int N = a.N, K = a.K, t0 = 16 * blockIdx.y;
+    const int row0 = blockIdx.x * 16 * RT;
+    const int t = t0 + r < a.T ? t0 + r : a.T - 1;  // clamped, valid
+    const uint16_t* xr = a.x + (size_t)t * K;
+    f32x4 acc[RT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int kb = wave * kStep; kb < K; kb += KW * kStep) {
+    for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int kb = wave * kStep; kb < K; kb += kSplitWaves * kStep) {
         const int k0 = kb + 32 * g;
         const bool live = k0 < K;       // K is a multiple of 64: the last step may be half
         const int kk = live ? k0 : 0;   // clamped, valid
-        const u32x4 w = *(const u32x4*)(qp + kk / 8);
-        const float s9 = live ? dq_scale(sp[kk / kGroup]) : 0.0f;
-        const float b = live ? bf16_to_f32(bp[kk / kGroup]) : 0.0f;
-        u32x4 x[NT][4];
+        u32x4 w[RT], x[4];
+        float s9[RT], b[RT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int t = 16 * n + r;
-            const u32x4* xp = (const u32x4*)(a.x + (size_t)(t < T ? t : T - 1) * K + kk);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[n][j] = xp[j];
-                if (!live) x[n][j] = u32x4{0u, 0u, 0u, 0u};
-            }
+        for (int i = 0; i < RT; ++i) {
+            const int at = row0 + 16 * i + r;
+            const size_t row = (size_t)(at < N ? at : N - 1);  // clamped, valid
+            w[i] = *(const u32x4*)(a.w.q + row * (size_t)(K / 8) + kk / 8);
+            s9[i] = live ? dq_scale(a.w.scale[row * (size_t)(K / kGroup) + kk / kGroup]) : 0.0f;
+            b[i] = live ? bf16_to_f32(a.w.bias[row * (size_t)(K / kGroup) + kk / kGroup]) : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const bf16x8 wv = dequant8(w[j], s9, b);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    wv, __builtin_bit_cast(bf16x8, x[n][j]), acc[n], 0, 0, 0);
+            x[j] = ((const u32x4*)(xr + kk))[j];
+            if (!live) x[j] = u32x4{0u, 0u, 0u, 0u};
         }
-    }
-    if (wave > 0) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) red[wave - 1][n][lane] = acc[n];
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    dequant8(w[i][j], s9[i], b[i]), __builtin_bit_cast(bf16x8, x[j]), acc[i], 0, 0, 0);
     }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) red[wave][i][lane] = acc[i];
     __syncthreads();
-    if (wave > 0) return;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-        for (int w = 0; w < KW - 1; ++w) acc[n] += red[w][n][lane];
-    store_tile<NT>(a, acc, row0, lane);
+    if (wave >= RT) return;
+    f32x4 sum[1] = {red[0][wave][lane]};
+    for (int w = 1; w < kSplitWaves; ++w) sum[0] += red[w][wave][lane];
+    store_tile<1>(a, sum, row0 + 16 * wave, t0, lane);
+}
+
+// Sixteen bytes at a 2-byte address (one load: the hardware takes any alignment).
+struct __attribute__((packed, aligned(2))) Unaligned {
+    uint32_t w[4];
+};
+
+// The 16-bit groups of v without the first n (0 <= n < 8), zeros at the end.
+__device__ __forceinline__ u32x4 shift_groups(const Unaligned& v, int n) {
+    uint64_t lo = v.w[0] | (uint64_t)v.w[1] << 32, hi = v.w[2] | (uint64_t)v.w[3] << 32;
+    if (n & 4) {
+        lo = hi;
+        hi = 0;
+    }
+    const int s = 16 * (n & 3);
+    lo = lo >> s | (hi << 1) << (63 - s);
+    hi >>= s;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
 // Many rows.  x lies in LDS as [step][16 tokens][8 columns][token] of 16 bytes: the eight
@@ -129,8 +145,8 @@ __global__ __launch_bounds__(KW * 64) void linear_split_kernel(const LinearArgs 
 // from that lane.  Loaded per chunk, 16 bytes from each of 16 rows, they cost as much time
 // as the codes: the vector caches serve cache lines, not bytes (measured at N = 30011,
 // K = 8192, one token: 46.5 us, and 35 without any scale loads).
-// FULL: K is a multiple of 2048 (no branches between the loads).  VEC: of 512 (a chunk's
-// eight scales are one aligned load).
+// FULL: K is a multiple of 2048 (no branches between the loads).  VEC: of 512 (no chunk is
+// cut short, a row's scales start on 16 bytes).
 constexpr int kChunk = 512;
 constexpr int kSteps = kChunk / kStep;
 constexpr int kCus = 256;
@@ -198,12 +214,11 @@ __global__ __launch_bounds__(kThreads) void linear_stream_kernel(const LinearArg
             v.s = *(const u32x4*)(a.w.scale + o);
             v.b = *(const u32x4*)(a.w.bias + o);
         } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const size_t o0 = so + min(g0 + 2 * i, groups - 1), o1 = so + min(g0 + 2 * i + 1, groups - 1);
-                v.s[i] = a.w.scale[o0] | (uint32_t)a.w.scale[o1] << 16;
-                v.b[i] = a.w.bias[o0] | (uint32_t)a.w.bias[o1] << 16;
-            }
+            // eight groups from any 2-byte address, inside the array (it has eight at least);
+            // where that starts before g0, the first ones are shifted out
+            const size_t o = so + min(g0, groups - 1), end = (size_t)N * groups - 8, at = o < end ? o : end;
+            v.s = shift_groups(*(const Unaligned*)(a.w.scale + at), (int)(o - at));
+            v.b = shift_groups(*(const Unaligned*)(a.w.bias + at), (int)(o - at));
         }
     };
     f32x4 acc[SUMS][NT];
@@ -302,7 +317,7 @@ __global__ __launch_bounds__(kThreads) void linear_stream_kernel(const LinearArg
         if (MODE == kWave && last && !dummy) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) acc[0][n] += acc[SUMS - 1][n];
-            store_tile<NT>(a, acc[0], row_of(u), lane);
+            store_tile<NT>(a, acc[0], row_of(u), 0, lane);
             clear();
         }
         if constexpr (MODE == kChunked) {
@@ -321,7 +336,7 @@ __global__ __launch_bounds__(kThreads) void linear_stream_kernel(const LinearArg
                 if (half == 0) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n) acc[0][n] += s_sum[(slot * NT + n) * 64 + lane];
-                    store_tile<NT>(a, acc[0], row_of(u), lane);
+                    store_tile<NT>(a, acc[0], row_of(u), 0, lane);
                 }
                 clear();
                 // (s_sum is written again after another barrier at least: a tile has an even
@@ -353,7 +368,7 @@ __global__ __launch_bounds__(kThreads) void linear_stream_kernel(const LinearArg
         if (u_first < units && half == 0) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) acc[0][n] += s_sum[(slot * NT + n) * 64 + lane];
-            store_tile<NT>(a, acc[0], row_of(u_first), lane);
+            store_tile<NT>(a, acc[0], row_of(u_first), 0, lane);
         }
     }
 }
@@ -370,7 +385,9 @@ void launch_stream(const LinearArgs& a, hipStream_t s) {
 template <int NB>
 void launch(const LinearArgs& a, hipStream_t s) {
     const bool fits = NB * ((a.K + kStep - 1) / kStep) <= 512;  // x in 128 KB
-    if (a.N < 16384) linear_split_kernel<(NB + 15) / 16, 4><<<(a.N + 15) / 16, 256, 0, s>>>(a);
+    const int groups = (a.T + 15) / 16, tiles = (a.N + 15) / 16;
+    if (a.N <= 4096) linear_split_kernel<1><<<dim3(tiles, groups), kSplitWaves * 64, 0, s>>>(a);
+    else if (a.N < 8192) linear_split_kernel<2><<<dim3((tiles + 1) / 2, groups), kSplitWaves * 64, 0, s>>>(a);
     else if (fits && a.N <= 16 * 8 * kCus) launch_stream<NB, kPair>(a, s);
     else if (fits) launch_stream<NB, kWave>(a, s);
     else if constexpr (NB > 8) launch_stream<NB, kChunked>(a, s);

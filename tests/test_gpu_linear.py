@@ -56,7 +56,9 @@ def check(y, q, s, b, x, rows=None):
     (1, 64, 1), (16, 64, 1), (17, 128, 3), (5, 192, 64), (100, 448, 16), (513, 512, 17),
     (2048, 2048, 1), (2049, 2048, 8), (1000, 4160, 5), (64, 8192, 33), (333, 8192, 64),
     (4097, 576, 32), (7000, 1024, 48), (30000, 256, 2), (9001, 2112, 9), (6000, 2048, 64),
-    (16500, 640, 31), (300, 8128, 2)])
+    (16500, 640, 31), (300, 8128, 2),
+    (20011, 64, 5), (17001, 192, 40), (16400, 4160, 20), (33000, 1088, 64), (40000, 448, 12),
+    (16384, 8192, 8), (35000, 2112, 33)])
 def test_products(dev, N, K, T, out):
     q, s, b, x = make(N, K, T, seed=N + K + T)
     y = q4.linear(*put(dev, q, s, b, x), out_dtype=out)
