@@ -350,27 +350,32 @@ def lm_argmax(lm: DeviceLmHead, x: torch.Tensor | None, ws: torch.Tensor,
     return logits, token, x_next
 
 
-def _launch_on(where: str, stream, **tensors):
+# The current stream's handle without building a stream object (2.5 us of a call).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _launch_on(where: str, stream, **tensors) -> int:
     """Stream handle for a call whose tensors are `tensors` (None: absent).  All of
-    them have to be on one GPU; that GPU has to be the current one, because the
+    them have to be on one GPU, and that GPU has to be the current one, because the
     library launches on the current device."""
-    dev = None
+    dev = -1
     for name, t in tensors.items():
         if t is None:
             continue
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0:
             raise ValueError(f"{name} must be on the GPU")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{where}: {name} is on {t.device}, other arguments on {dev}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{where}: the tensors are on {dev}, the current device is "
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{where}: {name} is on cuda:{d}, other arguments on cuda:{dev}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{where}: the tensors are on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
-    if stream.device != dev:
-        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {dev}")
+        return _raw_stream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on cuda:{dev}")
     return stream.cuda_stream
 
 
