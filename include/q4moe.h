@@ -281,8 +281,8 @@ int moe_dequant(const moe_q4mat* m, int32_t n_rows, int32_t K, uint16_t* w_out, 
    MOE_ROUTING_IN.  Per token with logits l:
      s_e = softmax(l)_e or 1 / (1 + exp(-l_e))
      v_e = s_e + balance_e            (the selection value; balance NULL: s_e)
-   An expert is out when its logit is NaN or -inf or its balance is not finite:
-   s_e = 0 and v_e = -inf.  With n_groups > 1 the experts fall into n_groups
+   (a score below exp(-700) is 0).  An expert is out when its logit is NaN or -inf
+   or its balance is not finite: s_e = 0 and v_e = -inf.  With n_groups > 1 the experts fall into n_groups
    runs of E / n_groups; a group's value is the sum of its group_top (1 or 2)
    largest v_e that are not out (-inf without any), and only the top_groups
    groups with the largest values take part.  idx = the top_k experts with the
@@ -403,7 +403,8 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
    before its first kernel and events[i] right after its i-th kernel, for
    i < n (moe_route: router logits (with MOE_LOGITS_IN: the clearing of
    the histogram), top-k + histogram, scan + scatter + maps; moe_route_scored
-   the same with its selection in the place of the top-k;
+   the same with its selection in the place of the top-k, for up to 64 tokens
+   (router logits, unless given,) selection with the sort;
    moe_prefill: gate/up, routed down,
    shared down + combine; moe_decode and moe_decode_tokens: router
    partial sums + shared gate/up, logits + top-k + routed gate/up, down +

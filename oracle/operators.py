@@ -40,11 +40,11 @@ def route_scored(logits, k: int, score="softmax", balance=None, n_groups=1, top_
         live = l > -np.inf  # (NaN compares false)
         s = np.zeros(E)
         if score == "sigmoid":
-            with np.errstate(over="ignore"):
-                s[live] = 1.0 / (1.0 + np.exp(-l[live]))
+            e = np.exp(-np.minimum(np.abs(l[live]), 800.0)) * (np.abs(l[live]) <= 700.0)
+            s[live] = np.where(l[live] >= 0, 1.0, e) / (1.0 + e)
         elif live.any():
             m = l[live].max()
-            z = np.array([0.0 if not ok else 1.0 if v == m else np.exp(v - m)
+            z = np.array([0.0 if not ok else 1.0 if v == m else np.exp(v - m) if m - v <= 700.0 else 0.0
                           for v, ok in zip(l, live)])
             s = z / z.sum()
         live &= np.isfinite(bal)

@@ -278,8 +278,11 @@ int moe_route_scored(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t 
         return fail(MOE_EUNSUPPORTED, "%d groups of %d experts hold fewer than top_k=%d",
                     spec->top_groups, L->n_experts / G, L->top_k);
     hipStream_t s = (hipStream_t)stream;
+    const bool small = q4moe::route_is_small(T);
     trace_begin(s);
-    if ((rc = hip_status(q4moe::launch_router_logits(logits_in ? nullptr : x, T, L->d, L->w_router,
+    // (with given logits this call only clears the histogram, which few tokens do not use)
+    if (!(small && logits_in) &&
+        (rc = hip_status(q4moe::launch_router_logits(logits_in ? nullptr : x, T, L->d, L->w_router,
                                                      L->router_bias, L->n_experts, r->logits,
                                                      r->blk_counts, s),
                          "router logits")))
@@ -299,6 +302,7 @@ int moe_route_scored(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t 
     a.idx = r->topk_idx;
     a.w = r->topk_w;
     a.blk_counts = r->blk_counts;
+    if (small) return hip_status(q4moe::launch_route_small(a, r, s), "route small");
     if ((rc = hip_status(q4moe::launch_select(a, s), "select"))) return rc;
     return hip_status(q4moe::launch_route_sort(r->topk_idx, T, L->top_k, L->n_experts, r, s),
                       "route sort");

@@ -34,6 +34,9 @@ struct ScoreArgs {
     int32_t* blk_counts;      // [ceil(T/MOE_ROUTE_BLOCK)][E], cleared; counts are added
 };
 hipError_t launch_select(const ScoreArgs& a, hipStream_t s);
+// Selection and sort of a few tokens in one launch (blk_counts is not used).
+bool route_is_small(int T);
+hipError_t launch_route_small(const ScoreArgs& a, const moe_routing* r, hipStream_t s);
 
 // y = W x for a few token rows (moe_linear).
 struct LinearArgs {
