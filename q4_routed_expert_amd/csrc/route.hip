@@ -340,7 +340,7 @@ hipError_t launch_topk(const float* logits, int T, int E, int k, int32_t* idx, f
 //        (a fixed-order sum over the count table);
 //     2. one wave scans the totals, ceil(totals/32) and ceil(totals/128) over
 //        the experts: offsets and the first entry of each expert's tiles in
-//        both maps (block 0 writes counts, offsets and both maps);
+//        both maps (the blocks share the writing of counts, offsets and both maps);
 //     3. stable scatter: each wave owns 64 consecutive tokens; each lane ORs
 //        its bit into a 64-bit mask per expert, and the sorted row of
 //        (token, slot) is offsets[e] + rows of e in earlier blocks + rows of e
@@ -350,9 +350,10 @@ hipError_t launch_topk(const float* logits, int T, int E, int k, int32_t* idx, f
 // ---------------------------------------------------------------------------
 constexpr int kRouteBlock = MOE_ROUTE_BLOCK;
 constexpr int kRouteWaves = kRouteBlock / 64;
+constexpr int kScatterThreads = 4 * kRouteBlock;  // four groups share the count table's rows
 static_assert(kRouteBlock % 64 == 0 && kRouteBlock >= kMaxExperts, "route block");
 
-__global__ __launch_bounds__(kRouteBlock) void route_scatter_kernel(
+__global__ __launch_bounds__(kScatterThreads) void route_scatter_kernel(
     const int32_t* __restrict__ idx, int T, int k, int E, const int32_t* __restrict__ blk_counts,
     int n_blk, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
     int32_t* __restrict__ perm, int32_t* __restrict__ inv_perm, int32_t* __restrict__ block_map,
@@ -360,27 +361,32 @@ __global__ __launch_bounds__(kRouteBlock) void route_scatter_kernel(
     __shared__ unsigned long long mask[kRouteWaves][kMaxExperts];
     __shared__ int run[kRouteWaves][kMaxExperts];
     __shared__ int s_cnt[kMaxExperts], s_before[kMaxExperts];
+    __shared__ int s_tot4[4][kMaxExperts], s_bef4[4][kMaxExperts];
     __shared__ int s_off[kMaxExperts + 1], s_b32[kMaxExperts + 1], s_b128[kMaxExperts + 1];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, g = blockIdx.x;
+    const bool token = tid < kRouteBlock;            // the block's tokens: one per thread
+    const int wave = token ? tid >> 6 : 0;
     // this block's selections, loaded first so that their round trip overlaps
     // the count-table reads below
     const int t = g * kRouteBlock + tid;
-    const bool valid = t < T;
+    const bool valid = token && t < T;
     int ex[kMaxTopK];
 #pragma unroll
     for (int s = 0; s < kMaxTopK; ++s) ex[s] = (valid && s < k) ? idx[(size_t)t * k + s] : 0;
 
-    // 1. totals and earlier-block counts
-    if (tid < E) {
+    // 1. totals and earlier-block counts: group q of threads takes every fourth run of
+    // sixteen blocks (integer sums: the same in any order)
+    const int q = tid / kRouteBlock, ec = tid % kRouteBlock;
+    if (ec < E) {
         // sixteen blocks' counts in flight at a time (one load after another,
         // each waited for, would cost one memory round trip per block)
         int tot = 0, before = 0;
-        for (int b0 = 0; b0 < n_blk; b0 += 16) {
+        for (int b0 = 16 * q; b0 < n_blk; b0 += 64) {
             int c[16];
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
                 const int b = b0 + u < n_blk ? b0 + u : 0;  // clamped, always valid
-                c[u] = blk_counts[(size_t)b * E + tid];
+                c[u] = blk_counts[(size_t)b * E + ec];
             }
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
@@ -390,13 +396,18 @@ __global__ __launch_bounds__(kRouteBlock) void route_scatter_kernel(
                 tot += v;
             }
         }
-        s_cnt[tid] = tot;
-        s_before[tid] = before;
+        s_tot4[q][ec] = tot;
+        s_bef4[q][ec] = before;
     }
-    for (int i = tid; i < kRouteWaves * kMaxExperts; i += kRouteBlock) (&mask[0][0])[i] = 0ull;
+    for (int i = tid; i < kRouteWaves * kMaxExperts; i += kScatterThreads) (&mask[0][0])[i] = 0ull;
+    __syncthreads();
+    if (tid < E) {
+        s_cnt[tid] = s_tot4[0][tid] + s_tot4[1][tid] + s_tot4[2][tid] + s_tot4[3][tid];
+        s_before[tid] = s_bef4[0][tid] + s_bef4[1][tid] + s_bef4[2][tid] + s_bef4[3][tid];
+    }
     __syncthreads();
     // 2. scan over the experts (wave 0, four experts per lane)
-    if (wave == 0) {
+    if (tid < 64) {
         int c[4], b32[4], b128[4], sc = 0, s32 = 0, s128 = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -444,7 +455,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_scatter_kernel(
     for (int s = 0; s < kMaxTopK; ++s)
         if (valid && s < k) atomicOr(&mask[wave][ex[s]], 1ull << lane);
     __syncthreads();
-    if (g == 0 && tid < E) {  // 2b. counts, offsets and both maps
+    if (tid < E && tid % n_blk == g) {  // 2b. counts, offsets and both maps, shared out over the blocks
         const int c = s_cnt[tid], o = s_off[tid];
         counts[tid] = c;
         offsets[tid] = o;
@@ -458,7 +469,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_scatter_kernel(
             tile_map[2 * b] = tid;
             tile_map[2 * b + 1] = o + kTileRows * j;
         }
-        if (tid == 0) {
+        if (tid == 0) {  // (expert 0: block 0)
             offsets[E] = s_off[E];
             *n_blocks = s_b32[E];
             *n_tiles = s_b128[E];
@@ -489,7 +500,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_scatter_kernel(
 hipError_t launch_route_sort(const int32_t* idx, int T, int k, int E, const moe_routing* r,
                              hipStream_t s) {
     const int n_blk = (T + kRouteBlock - 1) / kRouteBlock;
-    hipLaunchKernelGGL(route_scatter_kernel, dim3(n_blk), dim3(kRouteBlock), 0, s, idx, T, k, E,
+    hipLaunchKernelGGL(route_scatter_kernel, dim3(n_blk), dim3(kScatterThreads), 0, s, idx, T, k, E,
                        r->blk_counts, n_blk, r->counts, r->offsets, r->perm, r->inv_perm,
                        r->block_map, r->n_blocks, r->tile_map, r->n_tiles);
     trace_point(s);
