@@ -410,6 +410,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
             rows[name] = v
             setattr(p, name, v.data_ptr())
         else:
+            if dt == torch.int32 and not -2**31 <= v < 2**31:
+                raise ValueError(f"{name}: {v} is not an int32")
             setattr(p, name + "_all", v)
     if token is None:
         token = torch.empty(B, dtype=torch.int32, device=logits.device)

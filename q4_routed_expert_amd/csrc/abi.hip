@@ -653,6 +653,10 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
         return fail(MOE_EINVAL, "residual_out without a residual");
     if (!y && !y8) return fail(MOE_EINVAL, "neither y nor y8 is given");
     if (!y8 != !y8_scale) return fail(MOE_EINVAL, "y8 and y8_scale come together");
+    const void* const out[] = {residual_out, y, y8, y8_scale};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (out[i] && out[i] == out[j]) return fail(MOE_EINVAL, "two outputs share a buffer");
     q4moe::NormArgs a;
     a.x = x;
     a.residual = residual;

@@ -31,6 +31,8 @@ def _norm(**kw):
     (dict(residual_out=FAKE), _abi.MOE_EINVAL),        # nothing to add
     (dict(y=None), _abi.MOE_EINVAL),                   # no output at all
     (dict(y8=FAKE), _abi.MOE_EINVAL), (dict(scale=FAKE), _abi.MOE_EINVAL),
+    (dict(residual=FAKE, residual_out=FAKE + 64, y=FAKE + 64), _abi.MOE_EINVAL),  # shared outputs
+    (dict(y8=FAKE + 64, scale=FAKE, y=FAKE + 64), _abi.MOE_EINVAL),
     (dict(eps=-1.0), _abi.MOE_EINVAL), (dict(eps=float("nan")), _abi.MOE_EINVAL),
     (dict(eps=float("inf")), _abi.MOE_EINVAL), (dict(flags=4), _abi.MOE_EINVAL),
 ])
@@ -229,7 +231,7 @@ def test_sample_binding_refuses():
                      (dict(token=u), "token"), (dict(prob=u.double()), "prob"),
                      (dict(x_next=torch.zeros(3, 128, dtype=bf16)), "x_next"),
                      (dict(x_next=torch.zeros(2, 128, dtype=bf16), lm=lm), "x_next"),
-                     (dict(ws=u), "ws"),
+                     (dict(top_k=2**32 + 1), "top_k"), (dict(ws=u), "ws"),
                      (dict(ws=torch.empty(10, dtype=torch.uint8)), "GPU")):
         a = dict(logits=l, u=u)
         a.update(kw)
