@@ -10,6 +10,14 @@ stream.  There is no fallback: if the library is missing, loading raises.
     y1 = decode(layer, x1, ws)                 # one token
     lm = DeviceLmHead.from_host(head, embed)     # V x d output head, embedding
     logits, tok, _ = lm_argmax(lm, h, lm_workspace(lm), x_next=x_in)  # greedy token
+
+The operators around the layer:
+
+    y, _, _ = add_norm(x, w, residual, residual_out=residual)  # bf16 [T, d]
+    r = route_scored(layer, y, RouterSpec(score="sigmoid", balance=b))
+    y = decode_tokens(layer, y, ws, routing=r, routing_in=True)  # or prefill(layer, y, r)
+    logits = linear(q, scale, bias, h)                         # fp32 [T, N], T <= 64
+    token, prob, _ = sample(logits, u, temperature=0.8, top_k=50, top_p=0.95)
 """
 from __future__ import annotations
 
