@@ -403,7 +403,7 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
    before its first kernel and events[i] right after its i-th kernel, for
    i < n (moe_route: router logits (with MOE_LOGITS_IN: the clearing of
    the histogram), top-k + histogram, scan + scatter + maps; moe_route_scored
-   the same with its selection in the place of the top-k, for up to 64 tokens
+   the same with its selection in the place of the top-k, for up to 16 tokens
    (router logits, unless given,) selection with the sort;
    moe_prefill: gate/up, routed down,
    shared down + combine; moe_decode and moe_decode_tokens: router

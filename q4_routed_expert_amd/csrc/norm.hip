@@ -139,6 +139,10 @@ void launch(const NormArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// One wave a row up to 512 columns (32768 rows of 512: 11.9 us, and 21.8 with four waves, of
+// which three would idle), else four (2048 columns: 39.9 us against 39.6 with one wave and
+// four pieces a lane; one row: 3.0 against 3.1).  32768 rows of 2048 with an fp32 residual
+// move 805 MB in 138 us, 5.8 TB/s.
 hipError_t launch_add_norm(const NormArgs& a, hipStream_t s) {
     if (a.d <= 512) launch<1, 1>(a, s);
     else if (a.d <= 2048) launch<4, 1>(a, s);

@@ -52,7 +52,7 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 constexpr int kSampleBins = 2048;       // histogram bins of a row
 constexpr int kSampleList = 4096;       // tokens a row's list holds
 constexpr int kSampleMaxChunks = 512;   // chunks of a row
-constexpr int kSampleRowMax = 16384;    // rows up to here take the one-kernel form
+constexpr int kSampleRowMax = 8192;     // rows up to here take the one-kernel form
 struct SampleState {     // what a row's histogram says about its cut
     uint64_t total;      // sum of the histogram (its mass, or with top-k its count)
     uint64_t before;     // mass before the listed bins

@@ -69,6 +69,11 @@ CASES = [
     (129, 252, 8, dict(score="sigmoid", n_groups=2, top_groups=1, group_top=2)),
     (1025, 32, 4, dict(score="softmax", n_groups=8, top_groups=1, group_top=2)),
     (17, 256, 8, dict(score="sigmoid", n_groups=1, scale=-0.5)),
+    (16, 256, 8, dict(score="sigmoid", n_groups=16, top_groups=5, group_top=2)),
+    (15, 200, 3, dict(score="softmax", n_groups=50, top_groups=2, group_top=2)),
+    (2, 128, 8, dict(score="sigmoid", n_groups=1)),
+    (9, 256, 8, dict(score="softmax", n_groups=2, top_groups=1, group_top=2, renorm=False)),
+    (600, 64, 8, dict(score="softmax", n_groups=16, top_groups=4, group_top=2)),
 ]
 
 
@@ -123,7 +128,7 @@ def test_longest_chunk(dev):
         assert np.array_equal(getattr(r, name).cpu().numpy(), want[name]), name
 
 
-@pytest.mark.parametrize("T", [1, 3, 8, 70])
+@pytest.mark.parametrize("T", [1, 3, 8, 16, 70])
 def test_the_experts_products_follow_the_selection(dev, T):
     # x -> scored routing -> prefill, and the same selection through decode: both
     # against the oracle's layer with that selection (the bar of the layer's own
@@ -186,8 +191,9 @@ def test_decode_from_a_selection_equals_decode(dev):
         assert torch.equal(got.view(torch.int16), want.view(torch.int16))
 
 
-def test_graph_replays(dev):
-    T, E, k = 70, 256, 8
+@pytest.mark.parametrize("T", [7, 70])
+def test_graph_replays(dev, T):
+    E, k = 256, 8
     rng = np.random.default_rng(6)
     layer = small_layer(E, k, dev)
     kw = dict(score="sigmoid", n_groups=8, top_groups=4, group_top=2)

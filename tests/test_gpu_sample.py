@@ -57,7 +57,7 @@ def check(dev, l, u, temperature, top_k, top_p, min_p, arrays=True, stream=None,
 
 
 SIZES = [(1, 1), (3, 2), (2, 63), (5, 1000), (4, 2047), (4, 2048), (4, 2049), (37, 3001),
-         (2, 16385), (7, 30011), (1, 248320), (3, 100003)]
+         (2, 4097), (3, 8191), (2, 8192), (2, 8193), (2, 16385), (7, 30011), (1, 248320), (3, 100003)]
 FILTERS = [(1.0, 0, 1.0, 0.0), (0.7, 50, 1.0, 0.0), (1.0, 0, 0.9, 0.0), (1.3, 0, 1.0, 0.05),
            (0.8, 40, 0.95, 0.02), (0.0, 0, 1.0, 0.0), (1.0, 1, 0.5, 0.0), (2.5, 1000, 0.3, 0.0),
            (5.0, 0, 0.999, 0.0), (1.0, 0, 0.0, 0.0), (0.6, 0, 0.5, 1.0), (50.0, 700, 0.99, 0.5)]
