@@ -6,6 +6,19 @@
 
 namespace q4moe {
 
+// a * b + c with c in scalar registers (the compiler keeps such constants in vector
+// registers and copies them for its two-operand form, one more instruction a step).
+__device__ __forceinline__ double fma_const(double a, double b, double c) {
+    double d;
+    #if defined(__HIP_DEVICE_COMPILE__)
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+#else
+    d = __builtin_fma(a, b, c);
+#endif
+    return d;
+}
+
+
 // y = norm(x + residual) (moe_add_norm).
 struct NormArgs {
     const uint16_t* x;        // bf16 [T][d]

@@ -350,10 +350,10 @@ hipError_t launch_topk(const float* logits, int T, int E, int k, int32_t* idx, f
 // ---------------------------------------------------------------------------
 constexpr int kRouteBlock = MOE_ROUTE_BLOCK;
 constexpr int kRouteWaves = kRouteBlock / 64;
-constexpr int kScatterThreads = 4 * kRouteBlock;  // four groups share the count table's rows
+constexpr int kScatterGroups = 4;  // of kRouteBlock threads share the count table's rows, at most
 static_assert(kRouteBlock % 64 == 0 && kRouteBlock >= kMaxExperts, "route block");
 
-__global__ __launch_bounds__(kScatterThreads) void route_scatter_kernel(
+__global__ __launch_bounds__(kScatterGroups * kRouteBlock) void route_scatter_kernel(
     const int32_t* __restrict__ idx, int T, int k, int E, const int32_t* __restrict__ blk_counts,
     int n_blk, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
     int32_t* __restrict__ perm, int32_t* __restrict__ inv_perm, int32_t* __restrict__ block_map,
@@ -361,7 +361,7 @@ __global__ __launch_bounds__(kScatterThreads) void route_scatter_kernel(
     __shared__ unsigned long long mask[kRouteWaves][kMaxExperts];
     __shared__ int run[kRouteWaves][kMaxExperts];
     __shared__ int s_cnt[kMaxExperts], s_before[kMaxExperts];
-    __shared__ int s_tot4[4][kMaxExperts], s_bef4[4][kMaxExperts];
+    __shared__ int s_tot4[kScatterGroups][kMaxExperts], s_bef4[kScatterGroups][kMaxExperts];
     __shared__ int s_off[kMaxExperts + 1], s_b32[kMaxExperts + 1], s_b128[kMaxExperts + 1];
     const int tid = threadIdx.x, lane = tid & 63, g = blockIdx.x;
     const bool token = tid < kRouteBlock;            // the block's tokens: one per thread
@@ -374,14 +374,15 @@ __global__ __launch_bounds__(kScatterThreads) void route_scatter_kernel(
 #pragma unroll
     for (int s = 0; s < kMaxTopK; ++s) ex[s] = (valid && s < k) ? idx[(size_t)t * k + s] : 0;
 
-    // 1. totals and earlier-block counts: group q of threads takes every fourth run of
-    // sixteen blocks (integer sums: the same in any order)
-    const int q = tid / kRouteBlock, ec = tid % kRouteBlock;
+    // 1. totals and earlier-block counts: the groups of threads take runs of sixteen blocks
+    // in turn (integer sums: the same in any order)
+    const int q = tid / kRouteBlock, ec = tid % kRouteBlock, n_threads = blockDim.x;
+    const int n_grp = n_threads / kRouteBlock;
     if (ec < E) {
         // sixteen blocks' counts in flight at a time (one load after another,
         // each waited for, would cost one memory round trip per block)
         int tot = 0, before = 0;
-        for (int b0 = 16 * q; b0 < n_blk; b0 += 64) {
+        for (int b0 = 16 * q; b0 < n_blk; b0 += 16 * n_grp) {
             int c[16];
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
@@ -399,11 +400,16 @@ __global__ __launch_bounds__(kScatterThreads) void route_scatter_kernel(
         s_tot4[q][ec] = tot;
         s_bef4[q][ec] = before;
     }
-    for (int i = tid; i < kRouteWaves * kMaxExperts; i += kScatterThreads) (&mask[0][0])[i] = 0ull;
+    for (int i = tid; i < kRouteWaves * kMaxExperts; i += n_threads) (&mask[0][0])[i] = 0ull;
     __syncthreads();
     if (tid < E) {
-        s_cnt[tid] = s_tot4[0][tid] + s_tot4[1][tid] + s_tot4[2][tid] + s_tot4[3][tid];
-        s_before[tid] = s_bef4[0][tid] + s_bef4[1][tid] + s_bef4[2][tid] + s_bef4[3][tid];
+        int tot = 0, before = 0;
+        for (int p = 0; p < n_grp; ++p) {
+            tot += s_tot4[p][tid];
+            before += s_bef4[p][tid];
+        }
+        s_cnt[tid] = tot;
+        s_before[tid] = before;
     }
     __syncthreads();
     // 2. scan over the experts (wave 0, four experts per lane)
@@ -500,7 +506,10 @@ __global__ __launch_bounds__(kScatterThreads) void route_scatter_kernel(
 hipError_t launch_route_sort(const int32_t* idx, int T, int k, int E, const moe_routing* r,
                              hipStream_t s) {
     const int n_blk = (T + kRouteBlock - 1) / kRouteBlock;
-    hipLaunchKernelGGL(route_scatter_kernel, dim3(n_blk), dim3(kScatterThreads), 0, s, idx, T, k, E,
+    // one group where sixteen blocks are all there are, else four (128 blocks: 24.7 us with
+    // one and 19.2 with four)
+    const int threads = n_blk > 16 ? kScatterGroups * kRouteBlock : kRouteBlock;
+    hipLaunchKernelGGL(route_scatter_kernel, dim3(n_blk), dim3(threads), 0, s, idx, T, k, E,
                        r->blk_counts, n_blk, r->counts, r->offsets, r->perm, r->inv_perm,
                        r->block_map, r->n_blocks, r->tile_map, r->n_tiles);
     trace_point(s);

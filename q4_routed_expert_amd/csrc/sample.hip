@@ -89,18 +89,6 @@ __device__ __forceinline__ int bin_of(double x) {
     return min(kBins - 1, magic_int(__builtin_fma(x, kBins / kRange, kMagic - 0.5)));
 }
 
-// a * b + c with c in scalar registers (the compiler keeps such constants in vector
-// registers and copies them for its two-operand form, one more instruction a step).
-__device__ __forceinline__ double fma_const(double a, double b, double c) {
-    double d;
-    #if defined(__HIP_DEVICE_COMPILE__)
-    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
-#else
-    d = __builtin_fma(a, b, c);
-#endif
-    return d;
-}
-
 // round(2^43 exp(-x)) for 0 <= x < kRange.  x = n ln 2 - r with |r| <= ln 2 / 2; exp(r) =
 // 1 + r g(r), g the polynomial of degree 8 through (exp(r) - 1) / r at the nine Chebyshev
 // nodes of the interval (relative error below 2^-44 = half a unit of the largest

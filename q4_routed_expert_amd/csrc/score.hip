@@ -22,8 +22,10 @@ constexpr int kWaves = 4;  // tokens per work group
 // Order-preserving 64-bit key: a larger value has a larger key, -0.0 = +0.0.
 // Key 0 is below the key of every value, minus infinity included.
 __device__ __forceinline__ uint64_t order_key(double v) {
-    const uint64_t u = (uint64_t)__double_as_longlong(v == 0.0 ? 0.0 : v);
-    return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+    const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);  // (-0.0 + 0.0 = +0.0)
+    const uint32_t sign = (uint32_t)((int32_t)(uint32_t)(u >> 32) >> 31);  // all ones: negative
+    const uint32_t hi = (uint32_t)(u >> 32) ^ (sign | 0x80000000u), lo = (uint32_t)u ^ sign;
+    return ((uint64_t)hi << 32) | lo;
 }
 
 __device__ __forceinline__ double readlane_f64(double v, int lane) {
@@ -67,20 +69,20 @@ __device__ __forceinline__ float wave_max_f32(float v) {
 // and 2^-n by the exponent field.
 __device__ __forceinline__ double exp_neg(double x) {
     constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: the sum's low bits are the integer
-    const double t = __builtin_fma(x, 1.4426950408889634, kMagic);
+    const double t = fma_const(x, 1.4426950408889634, kMagic);
     const double n = t - kMagic;
     double r = __builtin_fma(n, 0.69314718055994529, -x);  // ln 2 in two parts
     r = __builtin_fma(n, 2.3190468138462996e-17, r);
     double e = 2.5105252864022e-08;
-    e = __builtin_fma(e, r, 2.7626348719601085e-07);
-    e = __builtin_fma(e, r, 2.7557254891675844e-06);
-    e = __builtin_fma(e, r, 2.48015043661086e-05);
-    e = __builtin_fma(e, r, 0.00019841269875881047);
-    e = __builtin_fma(e, r, 0.0013888888932477204);
-    e = __builtin_fma(e, r, 0.008333333333325376);
-    e = __builtin_fma(e, r, 0.04166666666657314);
-    e = __builtin_fma(e, r, 0.16666666666666674);
-    e = __builtin_fma(e, r, 0.5000000000000006);
+    e = fma_const(e, r, 2.7626348719601085e-07);
+    e = fma_const(e, r, 2.7557254891675844e-06);
+    e = fma_const(e, r, 2.48015043661086e-05);
+    e = fma_const(e, r, 0.00019841269875881047);
+    e = fma_const(e, r, 0.0013888888932477204);
+    e = fma_const(e, r, 0.008333333333325376);
+    e = fma_const(e, r, 0.04166666666657314);
+    e = fma_const(e, r, 0.16666666666666674);
+    e = fma_const(e, r, 0.5000000000000006);
     e = __builtin_fma(e, r, 1.0);
     e = __builtin_fma(e, r, 1.0);
     const uint64_t u = (uint64_t)__double_as_longlong(e) - ((uint64_t)__double_as_longlong(t) << 52);
@@ -186,23 +188,24 @@ __device__ __forceinline__ void wave_select(const float* __restrict__ lrow, cons
     for (int i = 0; i < 4; ++i) s_v[e0 + i] = v[i] > -INFINITY ? score[i] : 0.0;
     wave_lds_fence();
     // each lane's experts in order, equal ones by index (neighbours are exchanged only
-    // where the later one is larger); their numbers 0 .. 3 in the bytes of `at`
-    uint32_t at = 0x03020100u;
-    auto exchange = [&](uint64_t& x, uint64_t& y, int i) {
-        const bool swap = y > x;
-        const uint64_t h = swap ? y : x;
-        y = swap ? x : y;
-        x = h;
-        const uint32_t two = (at >> (8 * i)) & 0xFFFFu;
-        const uint32_t turned = (two >> 8) | ((two & 0xFFu) << 8);
-        at = swap ? (at & ~(0xFFFFu << (8 * i))) | (turned << (8 * i)) : at;
+    // where the later one is larger); their numbers 0 .. 3 then go into the bytes of `at`
+    uint32_t num[4] = {0, 1, 2, 3};
+    auto exchange = [&](int i) {
+        const bool swap = key[i + 1] > key[i];
+        const uint64_t h = swap ? key[i + 1] : key[i];
+        key[i + 1] = swap ? key[i] : key[i + 1];
+        key[i] = h;
+        const uint32_t m = swap ? num[i + 1] : num[i];
+        num[i + 1] = swap ? num[i] : num[i + 1];
+        num[i] = m;
     };
-    exchange(key[0], key[1], 0);
-    exchange(key[1], key[2], 1);
-    exchange(key[0], key[1], 0);
-    exchange(key[2], key[3], 2);
-    exchange(key[1], key[2], 1);
-    exchange(key[0], key[1], 0);
+    exchange(0);
+    exchange(1);
+    exchange(0);
+    exchange(2);
+    exchange(1);
+    exchange(0);
+    uint32_t at = num[0] | num[1] << 8 | num[2] << 16 | num[3] << 24;
     auto umax = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
     int my_e = 0;
 #pragma unroll
