@@ -339,7 +339,7 @@ int moe_route_scored(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t 
    Of lm only V, and with x_next also d and embed, are used.  logits and x_next
    are 16-byte aligned, the other arrays 4-byte.  1 <= B <= MOE_MAX_SAMPLE_ROWS.
    ws must hold moe_sample_workspace_bytes(V, B) bytes (no initialisation, not
-   preserved). */
+   preserved); a workspace for more rows of the same V serves fewer. */
 #define MOE_MAX_SAMPLE_ROWS 1024
 typedef struct {
     const float* u;             /* [B] uniform numbers */
@@ -409,8 +409,9 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
    shared down + combine; moe_decode and moe_decode_tokens: router
    partial sums + shared gate/up, logits + top-k + routed gate/up, down +
    combine; moe_lm_argmax: output head (with MOE_LOGITS_IN: the scan of the
-   given logits), pick + embedding row).  The one-kernel calls record events[0]
-   and events[1]: moe_linear, moe_add_norm.  The
+   given logits), pick + embedding row).  moe_sample: its one kernel (V <= 8192), or
+   chunk maxima, histogram, gathering, pick; the one-kernel calls moe_linear and
+   moe_add_norm record events[0] and events[1].  The
    elapsed time between consecutive events is one kernel's duration.  events
    are hipEvent_t handles created and owned by the caller; pass NULL to stop. */
 void moe_trace_events(void* const* events, int32_t n);

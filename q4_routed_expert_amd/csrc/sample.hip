@@ -23,8 +23,9 @@
 //   4. sample_pick_kernel    one work group per row: the exact cut, the chunk that holds
 //                            the drawn mass, the token in it, its embedding row
 // A row without top-k and top-p needs no cut: kernel 2 writes the chunks' masses
-// itself.  If the list overflows (thousands of equal logits at the cut), kernel 4
-// narrows over the whole row instead.
+// itself.  If the list overflows (more than 4096 tokens, or 2048 of one chunk:
+// thousands of equal logits at the cut, or such a top-k), kernel 4 narrows over the whole
+// row instead.
 // Short rows (sample_row_kernel): one work group does all of it with the row in its
 // registers.
 #include <float.h>
@@ -371,7 +372,7 @@ __device__ __forceinline__ Cut find_cut(const uint64_t* h, CutScratch& s, Of of)
 }
 
 __global__ __launch_bounds__(kThreads) void sample_gather_kernel(const SampleArgs a) {
-    constexpr uint32_t kLocal = 1024;  // entries collected in LDS; more go out one by one
+    constexpr uint32_t kLocal = 2048;  // entries of the list that one chunk may give
     __shared__ unsigned long long s_list[kLocal];
     __shared__ uint32_t s_n, s_base;
     __shared__ uint64_t s_sum[kThreads / 64];
@@ -403,23 +404,19 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(const SampleArg
             const uint64_t w = weight_in(x);
             sum += w >= p.w_min ? w : 0;
         } else if (bin <= hi) {
-            uint32_t at = atomicAdd(&s_n, 1u);
-            if (at < kLocal) {
-                s_list[at] = place(l, i);
-            } else {
-                at = atomicAdd(&a.list_n[b], 1u);
-                if (at < (uint32_t)kList) a.list[(size_t)b * kList + at] = place(l, i);
-            }
+            const uint32_t at = atomicAdd(&s_n, 1u);
+            if (at < kLocal) s_list[at] = place(l, i);
         }
     });
     sum = group_sum_u64<kThreads>(sum, s_sum);  // (its barriers also complete the list)
-    const uint32_t n = min(s_n, kLocal);
+    // a list that overflows, in a chunk or in all, is not used: list_n says so
+    const uint32_t n = s_n <= kLocal ? s_n : (uint32_t)kList + 1;
     if (tid == 0) {
         a.chunk_w[(size_t)b * a.n_chunks + c] = sum;
         s_base = n ? atomicAdd(&a.list_n[b], n) : 0;
     }
     __syncthreads();
-    // a list that overflows is not used: list_n says so
+    if (n > kLocal) return;
     for (uint32_t i = tid; i < n; i += kThreads)
         if (s_base + i < (uint32_t)kList) a.list[(size_t)b * kList + s_base + i] = s_list[i];
 }
@@ -441,10 +438,10 @@ struct Draw {
 // more than kRank.  s.n has to be 0 before; a barrier completes it here.
 template <typename Each>
 __device__ __forceinline__ bool collect(Draw& s, uint64_t lo, uint64_t hi, Each each) {
-    each([&](uint64_t p, uint64_t q) {
+    each([&](uint64_t p, auto q) {
         if (p >= lo && p <= hi && s.n <= (uint32_t)kRank) {
             const uint32_t at = atomicAdd(&s.n, 1u);
-            if (at < (uint32_t)kRank) s.rank[at] = ulonglong2{p, q};
+            if (at < (uint32_t)kRank) s.rank[at] = ulonglong2{p, q()};
         }
     });
     __syncthreads();
@@ -484,8 +481,9 @@ __device__ __forceinline__ bool rank_tokens(const Draw& s, int n, ulonglong2* me
 }
 
 // The last kept token of a region: the first, in the row's order, at which the running
-// sum of a quantity reaches the target (some token does).  each(f) calls f(place,
-// quantity) for this thread's tokens of the region.  Tokens are narrowed down by their
+// sum of a quantity reaches the target (some token does).  each(f) calls f(place, q) for
+// this thread's tokens of the region; q() is the quantity, computed only where it is
+// asked for.  Tokens are narrowed down by their
 // place, a factor of 2048 a time, until kRank of them are left, which are ranked.
 // Returns the token's place.
 template <int NT, typename Each>
@@ -499,7 +497,7 @@ __device__ __forceinline__ uint64_t narrow_cut(Draw& s, uint64_t target, Each ea
     }
     __syncthreads();
     uint64_t l = 0, h = 0;  // ~smallest and largest place (0: no token)
-    each([&](uint64_t p, uint64_t) {
+    each([&](uint64_t p, auto) {
         l = ~p > l ? ~p : l;
         h = p > h ? p : h;
     });
@@ -518,9 +516,9 @@ __device__ __forceinline__ uint64_t narrow_cut(Draw& s, uint64_t target, Each ea
         for (int i = tid; i < kBins; i += NT) s.hist[i] = 0;
         if (tid == 0) s.n = 0;
         __syncthreads();
-        each([&](uint64_t p, uint64_t q) {
+        each([&](uint64_t p, auto q) {
             if (p >= lo && p <= hi)
-                atomicAdd((unsigned long long*)&s.hist[(int)((hi - p) >> shift)], (unsigned long long)q);
+                atomicAdd((unsigned long long*)&s.hist[(int)((hi - p) >> shift)], (unsigned long long)q());
         });
         __syncthreads();
         const Cut c = find_cut<NT>(s.hist, s.cs, [&](uint64_t) { return target; });
@@ -543,7 +541,7 @@ __device__ __forceinline__ uint64_t narrow_cut(Draw& s, uint64_t target, Each ea
     }
 }
 
-// The cut of a row whose region's tokens each(f) visits as f(place, weight): top-k (if
+// The cut of a row whose region's tokens each(f) visits as f(place, weight()): top-k (if
 // its target lies in the region), then top-p.  base: mass before the region, total: the
 // mass top-p refers to without top-k.  few: the region may hold kRank tokens or fewer.
 template <int NT, typename Each>
@@ -583,10 +581,10 @@ __device__ __forceinline__ uint64_t row_cut(Draw& s, const SampleRow& p, bool k_
     uint64_t last = 0;
     if (p.cut_k) {
         if (k_reached)
-            last = narrow_cut<NT>(s, p.k, [&](auto f) { each([&](uint64_t pl, uint64_t) { f(pl, 1ull); }); });
+            last = narrow_cut<NT>(s, p.k, [&](auto f) { each([&](uint64_t pl, auto) { f(pl, [] { return 1ull; }); }); });
         if (!p.cut_p) return last;
         uint64_t mass = 0;
-        each([&](uint64_t pl, uint64_t w) { mass += pl >= last ? w : 0; });
+        each([&](uint64_t pl, auto w) { if (pl >= last) mass += w(); });
         total = group_sum_u64<NT>(mass, s.sum);
         base = 0;
     }
@@ -694,21 +692,31 @@ __global__ __launch_bounds__(NT) void sample_pick_kernel(const SampleArgs a) {
             if (listed) {
 #pragma unroll
                 for (int j = 0; j < LPT; ++j)
-                    if (lw[j]) f(lp[j], lw[j]);
+                    if (lw[j]) f(lp[j], [&] { return lw[j]; });
             } else {
-                for (int i = tid; i < a.V; i += NT) {
-                    const double x = depth(row[i], m, p.inv_t);
-                    if (!(x < kRange)) continue;
-                    const int bin = bin_of(x);
-                    if (bin >= st.lo && bin <= st.hi) f(place(row[i], i), weight_in(x));
+                // the whole row, eight logits of a thread in flight
+                for (int i0 = tid; i0 < a.V; i0 += 8 * NT) {
+                    float l[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) l[q] = row[min(i0 + q * NT, a.V - 1)];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int i = i0 + q * NT;
+                        const double x = depth(l[q], m, p.inv_t);
+                        if (i < a.V && x < kRange) {
+                            const int bin = bin_of(x);
+                            if (bin >= st.lo && bin <= st.hi) f(place(l[q], i), [&] { return weight_in(x); });
+                        }
+                    }
                 }
             }
         };
         last = row_cut<NT>(s, p, st.reached, st.before, st.total, n <= (uint32_t)kRank, each);
         __syncthreads();
-        each([&](uint64_t pl, uint64_t w) {
-            if (pl >= last && w >= p.w_min)
-                atomicAdd(&s_chunk[place_index(pl) >> a.chunk_sh], (unsigned long long)w);
+        each([&](uint64_t pl, auto weight_of) {
+            if (pl < last) return;
+            const uint64_t w = weight_of();
+            if (w >= p.w_min) atomicAdd(&s_chunk[place_index(pl) >> a.chunk_sh], (unsigned long long)w);
         });
     }
     __syncthreads();
@@ -843,7 +851,7 @@ __global__ __launch_bounds__(NT) void sample_row_kernel(const SampleArgs a) {
                 const double x = depth(l[j], m, p.inv_t);
                 if (x < kRange) {
                     const int bin = bin_of(x);
-                    if (bin >= lo && bin <= hi) f(place(l[j], PER * tid + j), weight_in(x));
+                    if (bin >= lo && bin <= hi) f(place(l[j], PER * tid + j), [&] { return weight_in(x); });
                 }
             }
         };

@@ -218,6 +218,9 @@ def test_sample_workspace_bytes():
         assert lib.moe_sample_workspace_bytes(V, B) > 0
     for V, B in ((0, 1), (1, 0), (_abi.MOE_MAX_VOCAB + 1, 1), (10, _abi.MOE_MAX_SAMPLE_ROWS + 1)):
         assert lib.moe_sample_workspace_bytes(V, B) == 0
+    for V in (1, 8192, 8193, 20000, 100003, 248320, _abi.MOE_MAX_VOCAB):  # more rows, more bytes
+        sizes = [lib.moe_sample_workspace_bytes(V, B) for B in range(1, 200)]
+        assert all(a < b for a, b in zip(sizes, sizes[1:])), V
 
 
 def test_sample_binding_refuses():
