@@ -422,9 +422,9 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
                 raise ValueError(f"{name}: {v} is not an int32")
             setattr(p, name + "_all", v)
     if token is None:
-        token = torch.empty(B, dtype=torch.int32, device=logits.device)
+        token = logits.new_empty(B, dtype=torch.int32)
     if prob is None:
-        prob = torch.empty(B, dtype=torch.float32, device=logits.device)
+        prob = logits.new_empty(B)
     _need(token, "token", torch.int32, B)
     _need(prob, "prob", torch.float32, B)
     if x_next is not None:
@@ -459,7 +459,7 @@ def linear(q: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor, x: torch.Te
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, not {out_dtype}")
     if y is None:
-        y = torch.empty((T, N), dtype=out_dtype, device=x.device)
+        y = x.new_empty((T, N), dtype=out_dtype)
     _need(x, "x", torch.bfloat16, T * K)
     _need(q, "q", torch.int32, N * K // 8)
     for name, t in (("scale", scale), ("bias", bias)):
@@ -500,13 +500,13 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     e4m3 = e4m3 or y8 is not None or y8_scale is not None
     if e4m3:
         if y8 is None:
-            y8 = torch.empty((T, d), dtype=torch.float8_e4m3fn, device=x.device)
+            y8 = torch.empty_like(x, dtype=torch.float8_e4m3fn)
         if y8_scale is None:
-            y8_scale = torch.empty((T, d // 64), dtype=torch.float32, device=x.device)
+            y8_scale = x.new_empty((T, d // 64), dtype=torch.float32)
         _need(y8, "y8", torch.float8_e4m3fn, T * d)
         _need(y8_scale, "y8_scale", torch.float32, T * (d // 64))
     elif y is None:
-        y = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
+        y = torch.empty_like(x)
     if y is not None:
         _need(y, "y", torch.bfloat16, T * d)
     s = _launch_on("add_norm", stream, x=x, weight=weight, residual=residual,
