@@ -387,8 +387,11 @@ int moe_linear(const moe_q4mat* m, int32_t N, int32_t K, const uint16_t* x, int3
      y: bf16 [T][d] (one rounding), or NULL
      y8, y8_scale: the row in 8 bits, or both NULL: y8 e4m3 (OCP) [T][d] and one
        fp32 scale per 64 columns, [T][d/64]: scale = max|y| / 448 over the group,
-       y8 = e4m3(y / scale), to nearest even, from the unrounded y.  A group of
-       zeros has scale 0; a NaN makes its whole group's codes and scale NaN.
+       y8 = e4m3(y / scale), to nearest even, from the unrounded y and the stored
+       scale, at most 448.  Where the scale is 0 (a group of zeros, or of values
+       up to 448 * 2^-150) the codes are 0; an infinite y makes its group's scale
+       infinite, the finite values' codes 0 and its own NaN; a NaN makes its whole
+       group's codes and scale NaN.
    At least one of y and y8.  y may be x or a bf16 residual; other overlaps of
    outputs with inputs are not allowed.  1 <= T <= MOE_MAX_TOKENS, d a multiple
    of 64, <= MOE_MAX_D; eps finite, >= 0.  One kernel, no workspace. */

@@ -4,8 +4,10 @@
 //   y = r / sqrt(mean(r^2) + eps) * w
 //
 // in fp32 from the stored r, rounded once to bf16; or, per 64 columns, to e4m3
-// codes with the fp32 scale max|y| / 448 (448 = the largest e4m3 value), from
-// the unrounded y.
+// codes of y / scale with the fp32 scale max|y| / 448 (448 = the largest e4m3
+// value), from the unrounded y.  The quotient is by the scale that is stored: a
+// factor 448 / max|y| rounds otherwise (one code in 10^5 lands on the other side of a
+// border) and leaves fp32's range for a small max|y|.
 //
 // Every input is read once and every output written once: a row stays in the
 // registers between its sum of squares and its scaling.  The kernel is bound by
@@ -108,23 +110,36 @@ __global__ __launch_bounds__(W * 64) void add_norm_kernel(const NormArgs a) {
             m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));
             m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, false));
             const float amax = __uint_as_float(m);
-            float q = 448.0f / amax;          // all zeros: infinite, replaced below
-            q = q > 3.4e38f ? 3.4e38f : q;    // (a NaN stays one)
+            float scale, z[8];
+            if (amax > 0x1p-70f && amax < 0x1p80f) {
+                // Both quotients as products by a reciprocal and their exact remainder: the
+                // scale is amax / 448 correctly rounded (checked for every mantissa), and
+                // y / scale unless it lies within 2^-22 of a step from the middle of two fp32
+                // numbers.  (2048 x 2048 with eight IEEE divisions: 8.6 us instead of 7.7.)
+                scale = amax * (1.0f / 448.0f);
+                scale = __builtin_fmaf(__builtin_fmaf(-scale, 448.0f, amax), 1.0f / 448.0f, scale);
+                const float inv_s = __builtin_amdgcn_rcpf(scale);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float t = y[i] * inv_s;
+                    z[i] = __builtin_fmaf(__builtin_fmaf(-t, scale, y[i]), inv_s, t);
+                }
+            } else {  // where a remainder could leave fp32's range
+                scale = amax / 448.0f;  // (0 for the smallest subnormals too)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[i] = scale == 0.0f ? 0.0f : y[i] / scale;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = z[i] > 448.0f ? 448.0f : z[i] < -448.0f ? -448.0f : z[i];  // (a NaN stays one)
             uint32_t w8[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float z[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float t = y[4 * h + i] * q;
-                    z[i] = t > 448.0f ? 448.0f : t < -448.0f ? -448.0f : t;
-                }
-                int w = __builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], 0, false);
-                w8[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], w, true);
+                const int w = __builtin_amdgcn_cvt_pk_fp8_f32(z[4 * h], z[4 * h + 1], 0, false);
+                w8[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(z[4 * h + 2], z[4 * h + 3], w, true);
             }
             if (live) {
                 *(uint2*)(a.y8 + row + c) = uint2{w8[0], w8[1]};
-                if ((tid & 7) == 0) a.y8_scale[(row + c) / kGroup] = amax / 448.0f;
+                if ((tid & 7) == 0) a.y8_scale[(row + c) / kGroup] = scale;
             }
         }
     }
