@@ -4,6 +4,11 @@ Argument marshalling only: every step of the layer runs in the HIP kernels
 behind the C ABI of include/q4moe.h.  PyTorch supplies device memory and the
 stream.  There is no fallback: if the library is missing, loading raises.
 
+Calls launch on the current stream or on `stream`.  What a call allocates itself
+(outputs, routings, workspaces) is allocated on the stream it launches on; tensors
+that are given to it have to be ready on that stream, and the weights of a layer or
+head to be kept until the work is done, as everywhere in torch.
+
     layer = DeviceLayer.from_host(L)           # L: dict of numpy arrays
     r = route(layer, x)                        # x: bf16 [T, d] on the GPU
     y = prefill(layer, x, r)                   # bf16 [T, d]
@@ -80,6 +85,32 @@ def _on_gpu(**tensors):
             raise ValueError(f"{name} must be on the GPU")
 
 
+def _made(stream, make, *args, **kw):
+    """make(*args, **kw), a tensor or a DeviceRouting of the call's own, on the stream
+    that the call launches on.  Memory taken from another stream's pool may still be in
+    use by that stream's queued work, its fills are not ordered before the call's
+    kernels, and once dropped it goes to that stream's next tensor, which does not
+    wait for them either."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        out = make(*args, **kw)
+    _used_on(torch.cuda.current_stream(stream.device), out)  # by the caller, after a wait
+    return out
+
+
+def _used_on(stream, *tensors):
+    """Keeps the tensors' memory from being handed out again before the work that is
+    now on `stream` (None: the current one) is done."""
+    if stream is None:
+        return
+    for t in tensors:
+        if isinstance(t, DeviceRouting):
+            _used_on(stream, *(getattr(t, f) for f, _ in _abi.Routing._fields_))
+        elif t is not None and t.is_cuda:
+            t.record_stream(stream)
+
+
 def _dev(a: np.ndarray, device) -> torch.Tensor:
     a = np.ascontiguousarray(a)
     view = {np.dtype(np.uint32): np.int32, np.dtype(np.uint16): np.int16}.get(a.dtype, a.dtype)
@@ -153,7 +184,7 @@ def workspace(layer: DeviceLayer, T: int, device="cuda") -> torch.Tensor:
 def route(layer: DeviceLayer, x: torch.Tensor, routing: DeviceRouting | None = None,
           logits_in: bool = False, stream=None) -> DeviceRouting:
     T = x.shape[0]
-    r = routing or DeviceRouting(T, layer.n_experts, layer.top_k, x.device)
+    r = routing or _made(stream, DeviceRouting, T, layer.n_experts, layer.top_k, x.device)
     flags = MOE_LOGITS_IN if logits_in else 0
     if not logits_in:
         _need(x, "x", torch.bfloat16, T * layer.d)
@@ -162,6 +193,7 @@ def route(layer: DeviceLayer, x: torch.Tensor, routing: DeviceRouting | None = N
     _on_gpu(x=None if logits_in else x, logits=r.logits)
     _check(_abi.lib().moe_route(C.addressof(layer.struct), _ptr(x), T, flags, C.addressof(r.struct),
                                 _stream(stream)), "moe_route")
+    _used_on(stream, x, r)
     return r
 
 
@@ -199,7 +231,7 @@ def route_scored(layer: DeviceLayer, x: torch.Tensor | None, spec: RouterSpec,
         T = x.shape[0]
         _need(x, "x", torch.bfloat16, T * layer.d)
         if routing is None:
-            routing = DeviceRouting(T, layer.n_experts, layer.top_k, x.device)
+            routing = _made(stream, DeviceRouting, T, layer.n_experts, layer.top_k, x.device)
     r = routing
     if r.T < T or r.E != layer.n_experts or r.k != layer.top_k:
         raise ValueError(f"routing is for T={r.T} E={r.E} k={r.k}, the call for T={T} "
@@ -211,6 +243,7 @@ def route_scored(layer: DeviceLayer, x: torch.Tensor | None, spec: RouterSpec,
     _check(_abi.lib().moe_route_scored(C.addressof(layer.struct), None if logits_in else _ptr(x), T,
                                        MOE_LOGITS_IN if logits_in else 0, C.addressof(spec.struct),
                                        C.addressof(r.struct), s), "moe_route_scored")
+    _used_on(stream, None if logits_in else x, spec.balance, r)
     return r
 
 
@@ -227,9 +260,9 @@ def prefill(layer: DeviceLayer, x: torch.Tensor, routing: DeviceRouting,
         raise ValueError(f"item_rows must be one of 128, 64, 32, 16, not {item_rows}")
     T = x.shape[0]
     if ws is None:
-        ws = workspace(layer, T, x.device)
+        ws = _made(stream, workspace, layer, T, x.device)
     if y is None:
-        y = torch.empty((T, layer.d), dtype=torch.bfloat16, device=x.device)
+        y = _made(stream, torch.empty, (T, layer.d), dtype=torch.bfloat16, device=x.device)
     _need(x, "x", torch.bfloat16, T * layer.d)
     _need(y, "y", torch.bfloat16, T * layer.d)
     _need(routing.perm, "routing.perm", torch.int32, T * layer.top_k)
@@ -244,6 +277,7 @@ def prefill(layer: DeviceLayer, x: torch.Tensor, routing: DeviceRouting,
                                          C.addressof(routing.struct), _ptr(ws), ws.numel(),
                                          _ptr(y), _ITEM_ROWS_FLAGS[item_rows], _stream(stream)),
                "moe_prefill_ex")
+    _used_on(stream, x, routing, ws, y)
     return y
 
 
@@ -259,7 +293,7 @@ def decode(layer: DeviceLayer, x: torch.Tensor, ws: torch.Tensor, y: torch.Tenso
     """The layer for one token.  routing_in: the selection in routing (from route or
     route_scored) is used instead of the layer's own routing."""
     if y is None:
-        y = torch.empty((1, layer.d), dtype=torch.bfloat16, device=x.device)
+        y = _made(stream, torch.empty, (1, layer.d), dtype=torch.bfloat16, device=x.device)
     flags = _decode_flags(routing, logits_in, routing_in)
     rs = C.addressof(routing.struct) if routing is not None else None
     _need(x, "x", torch.bfloat16, layer.d)
@@ -271,6 +305,7 @@ def decode(layer: DeviceLayer, x: torch.Tensor, ws: torch.Tensor, y: torch.Tenso
     _on_gpu(x=x, y=y, ws=ws)
     _check(_abi.lib().moe_decode(C.addressof(layer.struct), _ptr(x), flags, rs, _ptr(ws), ws.numel(),
                                  _ptr(y), _stream(stream)), "moe_decode")
+    _used_on(stream, x, routing, ws, y)
     return y
 
 
@@ -282,7 +317,7 @@ def decode_tokens(layer: DeviceLayer, x: torch.Tensor, ws: torch.Tensor,
     routing_in: as decode's."""
     T = x.shape[0]
     if y is None:
-        y = torch.empty((T, layer.d), dtype=torch.bfloat16, device=x.device)
+        y = _made(stream, torch.empty, (T, layer.d), dtype=torch.bfloat16, device=x.device)
     flags = _decode_flags(routing, logits_in, routing_in)
     rs = C.addressof(routing.struct) if routing is not None else None
     _need(x, "x", torch.bfloat16, T * layer.d)
@@ -294,15 +329,17 @@ def decode_tokens(layer: DeviceLayer, x: torch.Tensor, ws: torch.Tensor,
     _on_gpu(x=x, y=y, ws=ws)
     _check(_abi.lib().moe_decode_tokens(C.addressof(layer.struct), _ptr(x), T, flags, rs, _ptr(ws),
                                         ws.numel(), _ptr(y), _stream(stream)), "moe_decode_tokens")
+    _used_on(stream, x, routing, ws, y)
     return y
 
 
 def dequant(q: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor, stream=None) -> torch.Tensor:
     """bf16 [N, K] from one Q4 matrix (q int32 [N, K/8], scale/bias bf16 bits [N, K/64])."""
     N, K = q.shape[0], q.shape[1] * 8
-    out = torch.empty((N, K), dtype=torch.bfloat16, device=q.device)
+    out = _made(stream, torch.empty, (N, K), dtype=torch.bfloat16, device=q.device)
     m = _abi.Q4Mat(_ptr(q), _ptr(scale), _ptr(bias))
     _check(_abi.lib().moe_dequant(C.addressof(m), N, K, _ptr(out), _stream(stream)), "moe_dequant")
+    _used_on(stream, q, scale, bias, out)
     return out
 
 
@@ -341,9 +378,9 @@ def lm_argmax(lm: DeviceLmHead, x: torch.Tensor | None, ws: torch.Tensor,
     With logits_in the given logits are read instead of computed from x."""
     dev = ws.device
     if logits is None:
-        logits = torch.empty(lm.V, dtype=torch.float32, device=dev)
+        logits = _made(stream, torch.empty, lm.V, dtype=torch.float32, device=dev)
     if token is None:
-        token = torch.empty(1, dtype=torch.int32, device=dev)
+        token = _made(stream, torch.empty, 1, dtype=torch.int32, device=dev)
     flags = MOE_LOGITS_IN if logits_in else 0
     if not logits_in:
         _need(x, "x", torch.bfloat16, lm.d)
@@ -355,6 +392,7 @@ def lm_argmax(lm: DeviceLmHead, x: torch.Tensor | None, ws: torch.Tensor,
     _check(_abi.lib().moe_lm_argmax(C.addressof(lm.struct), _ptr(x), flags, _ptr(logits),
                                     _ptr(token), _ptr(x_next), _ptr(ws), ws.numel(),
                                     _stream(stream)), "moe_lm_argmax")
+    _used_on(stream, None if logits_in else x, logits, token, x_next, ws)
     return logits, token, x_next
 
 
@@ -384,6 +422,7 @@ def _launch_on(where: str, stream, **tensors) -> int:
         return _raw_stream(dev)
     if stream.device.index != dev:
         raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on cuda:{dev}")
+    _used_on(stream, *tensors.values())
     return stream.cuda_stream
 
 
@@ -422,9 +461,9 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
                 raise ValueError(f"{name}: {v} is not an int32")
             setattr(p, name + "_all", v)
     if token is None:
-        token = logits.new_empty(B, dtype=torch.int32)
+        token = _made(stream, logits.new_empty, B, dtype=torch.int32)
     if prob is None:
-        prob = logits.new_empty(B)
+        prob = _made(stream, logits.new_empty, B)
     _need(token, "token", torch.int32, B)
     _need(prob, "prob", torch.float32, B)
     if x_next is not None:
@@ -435,7 +474,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     else:
         head = _abi.LmHead(V)
     if ws is None:
-        ws = sample_workspace(B, V, logits.device)
+        ws = _made(stream, sample_workspace, B, V, logits.device)
     _need(ws, "ws", torch.uint8, 1)
     s = _launch_on("sample", stream, logits=logits, token=token, prob=prob, x_next=x_next, ws=ws,
                    **rows)
@@ -459,7 +498,7 @@ def linear(q: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor, x: torch.Te
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, not {out_dtype}")
     if y is None:
-        y = x.new_empty((T, N), dtype=out_dtype)
+        y = _made(stream, x.new_empty, (T, N), dtype=out_dtype)
     _need(x, "x", torch.bfloat16, T * K)
     _need(q, "q", torch.int32, N * K // 8)
     for name, t in (("scale", scale), ("bias", bias)):
@@ -500,13 +539,13 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     e4m3 = e4m3 or y8 is not None or y8_scale is not None
     if e4m3:
         if y8 is None:
-            y8 = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+            y8 = _made(stream, torch.empty_like, x, dtype=torch.float8_e4m3fn)
         if y8_scale is None:
-            y8_scale = x.new_empty((T, d // 64), dtype=torch.float32)
+            y8_scale = _made(stream, x.new_empty, (T, d // 64), dtype=torch.float32)
         _need(y8, "y8", torch.float8_e4m3fn, T * d)
         _need(y8_scale, "y8_scale", torch.float32, T * (d // 64))
     elif y is None:
-        y = torch.empty_like(x)
+        y = _made(stream, torch.empty_like, x)
     if y is not None:
         _need(y, "y", torch.bfloat16, T * d)
     s = _launch_on("add_norm", stream, x=x, weight=weight, residual=residual,
