@@ -281,9 +281,19 @@ def prefill(layer: DeviceLayer, x: torch.Tensor, routing: DeviceRouting,
     return y
 
 
-def _decode_flags(routing, logits_in: bool, routing_in: bool) -> int:
-    if routing_in and routing is None:
-        raise ValueError("routing_in needs a routing")
+def _decode_flags(layer, T: int, routing, logits_in: bool, routing_in: bool) -> int:
+    if routing is not None:
+        _need(routing.logits, "routing.logits", torch.float32, T * layer.n_experts)
+        _need(routing.topk_idx, "routing.topk_idx", torch.int32, T * layer.top_k)
+        _need(routing.topk_w, "routing.topk_w", torch.float32, T * layer.top_k)
+    if routing_in:
+        if routing is None:
+            raise ValueError("routing_in needs a routing")
+        # rows of another length would be read across each other
+        if routing.E != layer.n_experts or routing.k != layer.top_k:
+            raise ValueError(f"the routing is for E={routing.E} k={routing.k}, the layer has "
+                             f"E={layer.n_experts} k={layer.top_k}")
+        _on_gpu(**{"routing.topk_idx": routing.topk_idx, "routing.topk_w": routing.topk_w})
     return (MOE_LOGITS_IN if logits_in else 0) | (_abi.MOE_ROUTING_IN if routing_in else 0)
 
 
@@ -294,14 +304,10 @@ def decode(layer: DeviceLayer, x: torch.Tensor, ws: torch.Tensor, y: torch.Tenso
     route_scored) is used instead of the layer's own routing."""
     if y is None:
         y = _made(stream, torch.empty, (1, layer.d), dtype=torch.bfloat16, device=x.device)
-    flags = _decode_flags(routing, logits_in, routing_in)
     rs = C.addressof(routing.struct) if routing is not None else None
     _need(x, "x", torch.bfloat16, layer.d)
     _need(y, "y", torch.bfloat16, layer.d)
-    if routing is not None:
-        _need(routing.logits, "routing.logits", torch.float32, layer.n_experts)
-        _need(routing.topk_idx, "routing.topk_idx", torch.int32, layer.top_k)
-        _need(routing.topk_w, "routing.topk_w", torch.float32, layer.top_k)
+    flags = _decode_flags(layer, 1, routing, logits_in, routing_in)
     _on_gpu(x=x, y=y, ws=ws)
     _check(_abi.lib().moe_decode(C.addressof(layer.struct), _ptr(x), flags, rs, _ptr(ws), ws.numel(),
                                  _ptr(y), _stream(stream)), "moe_decode")
@@ -318,14 +324,10 @@ def decode_tokens(layer: DeviceLayer, x: torch.Tensor, ws: torch.Tensor,
     T = x.shape[0]
     if y is None:
         y = _made(stream, torch.empty, (T, layer.d), dtype=torch.bfloat16, device=x.device)
-    flags = _decode_flags(routing, logits_in, routing_in)
     rs = C.addressof(routing.struct) if routing is not None else None
     _need(x, "x", torch.bfloat16, T * layer.d)
     _need(y, "y", torch.bfloat16, T * layer.d)
-    if routing is not None:
-        _need(routing.logits, "routing.logits", torch.float32, T * layer.n_experts)
-        _need(routing.topk_idx, "routing.topk_idx", torch.int32, T * layer.top_k)
-        _need(routing.topk_w, "routing.topk_w", torch.float32, T * layer.top_k)
+    flags = _decode_flags(layer, T, routing, logits_in, routing_in)
     _on_gpu(x=x, y=y, ws=ws)
     _check(_abi.lib().moe_decode_tokens(C.addressof(layer.struct), _ptr(x), T, flags, rs, _ptr(ws),
                                         ws.numel(), _ptr(y), _stream(stream)), "moe_decode_tokens")

@@ -56,3 +56,13 @@ def test_decode_refuses_short_buffers():
                          y=torch.empty((4, 128), dtype=bf16))
     with pytest.raises(ValueError, match="x"):
         q4.decode(L, torch.empty((1, 128), dtype=torch.int16), ws, y=torch.empty(128, dtype=bf16))
+
+
+@pytest.mark.parametrize("E,k,what", [(8, 4, "k=4"), (8, 3, "k=3"), (16, 2, "E=16"), (8, 2, "topk_idx must be on the GPU")])
+def test_decode_refuses_the_selection_of_another_layer(E, k, what):
+    # [T][k] arrays of another k would be read with the wrong row length
+    L, ws, r = _layer(), torch.empty(16, dtype=torch.uint8), q4.DeviceRouting(8, E, k, "cpu")
+    with pytest.raises(ValueError, match=what):
+        q4.decode_tokens(L, torch.empty((4, 128), dtype=bf16), ws, routing=r, routing_in=True)
+    with pytest.raises(ValueError, match=what):
+        q4.decode(L, torch.empty((1, 128), dtype=bf16), ws, routing=r, routing_in=True)
