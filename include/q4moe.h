@@ -329,8 +329,10 @@ int moe_route_scored(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t 
      min-p      of those, the tokens with w_i >= min_p (min_p <= 0 or NaN: all;
                 above 1 counts as 1)
      token      the first kept token, in index order, at which the running sum of
-                the kept weights exceeds u times their sum
-     prob       its share of the kept weights (NULL: not stored)
+                the kept weights exceeds u times their sum (u = 0: the first one
+                whose weight is not 0)
+     prob       exp((l_token - l_max) / temperature), not rounded to 2^-43, over the
+                sum of the kept weights (NULL: not stored)
      x_next     bf16 row `token` of embed (NULL: not stored)
    temperature <= 0 or NaN is greedy: top_k = 1, whatever the others say.  u is
    taken into [0, 1).  A row without a live logit gives token 0 and prob 0.  The

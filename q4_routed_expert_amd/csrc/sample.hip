@@ -7,7 +7,9 @@
 // (0 beyond, where the rounding gives at most 1) as 64-bit integers, so every sum is
 // exact (V <= 2^20 weights of at most 2^43) and the same in any order: atomics and
 // split sums give the same token every time, and a weight's rounding, 2^-44 of the
-// largest, is far below the step of a 24-bit uniform number.
+// largest, is far below the step of a 24-bit uniform number.  Only the drawn token's
+// probability takes its weight unrounded: a rounding of 2^-44 is 2^-19 of a weight at
+// depth 17, more than fp32 keeps.
 //
 // The draw runs over the kept tokens in index order, so nothing is ever sorted: all
 // that is needed of the order is its cut, the last kept token.  It is the first at
@@ -90,12 +92,11 @@ __device__ __forceinline__ int bin_of(double x) {
     return min(kBins - 1, magic_int(__builtin_fma(x, kBins / kRange, kMagic - 0.5)));
 }
 
-// round(2^43 exp(-x)) for 0 <= x < kRange.  x = n ln 2 - r with |r| <= ln 2 / 2; exp(r) =
+// 2^43 exp(-x) for 0 <= x < kRange.  x = n ln 2 - r with |r| <= ln 2 / 2; exp(r) =
 // 1 + r g(r), g the polynomial of degree 8 through (exp(r) - 1) / r at the nine Chebyshev
 // nodes of the interval (relative error below 2^-44 = half a unit of the largest
-// weight); 2^(43 - n) by the exponent field; and the rounding by adding 2^52, which
-// leaves the integer in the low bits of the sum.  Only full-rate 64-bit arithmetic.
-__device__ __forceinline__ uint64_t weight_in(double x) {
+// weight); 2^(43 - n) by the exponent field.  Only full-rate 64-bit arithmetic.
+__device__ __forceinline__ double exp_in(double x) {
     const double t = fma_const(x, 1.4426950408889634, kMagic);
     const double n = t - kMagic;
     const double r = __builtin_fma(n, 0.69314718055994529, -x);
@@ -109,9 +110,13 @@ __device__ __forceinline__ uint64_t weight_in(double x) {
     e = fma_const(e, r, 0.49999999999797906);
     e = __builtin_fma(e, r, 1.0);
     e = __builtin_fma(e, r, 1.0);
-    const uint64_t u = (uint64_t)__double_as_longlong(e) + ((uint64_t)(uint32_t)(43 - magic_int(t)) << 52);
-    const double v = __longlong_as_double((long long)u) + 4503599627370496.0;
-    return (uint64_t)__double_as_longlong(v) & 0xFFFFFFFFFFFFFull;
+    return __longlong_as_double((long long)((uint64_t)__double_as_longlong(e) +
+                                            ((uint64_t)(uint32_t)(43 - magic_int(t)) << 52)));
+}
+
+// Its rounding: adding 2^52 leaves the integer in the low bits of the sum.
+__device__ __forceinline__ uint64_t weight_in(double x) {
+    return (uint64_t)__double_as_longlong(exp_in(x) + 4503599627370496.0) & 0xFFFFFFFFFFFFFull;
 }
 
 // The weight at any depth: 0 beyond the range and for NaN.
@@ -431,7 +436,7 @@ struct Draw {
     uint64_t sum[kRowThreads / 64];
     float m[kRowThreads / 64];
     int token;
-    uint64_t wt;
+    float logit;  // the token's
 };
 
 // Collects the region's tokens with lo <= place <= hi for ranking; false if there are
@@ -600,10 +605,11 @@ __device__ __forceinline__ uint64_t drawn_mass(float u, uint64_t total) {
 }
 
 // The element at which the running sum of w, in index order, exceeds `draw`: element
-// PER tid + j has weight w[j] in thread tid.  s.token = its number or -1, s.wt = its
-// weight; visible after the call.
+// PER tid + j has logit l[j] and weight w[j] in thread tid.  s.token = its number or -1,
+// s.logit = its logit; visible after the call.
 template <int NT, int PER>
-__device__ __forceinline__ void find_drawn(Draw& s, const uint64_t (&w)[PER], uint64_t draw) {
+__device__ __forceinline__ void find_drawn(Draw& s, const float (&l)[PER], const uint64_t (&w)[PER],
+                                           uint64_t draw) {
     constexpr int NW = NT / 64;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     uint64_t sum = 0;
@@ -614,7 +620,7 @@ __device__ __forceinline__ void find_drawn(Draw& s, const uint64_t (&w)[PER], ui
     if (lane == 63) s.sum[wave] = inc;
     if (tid == 0) {
         s.token = -1;
-        s.wt = 0;
+        s.logit = -INFINITY;
     }
     __syncthreads();
     uint64_t run = inc - sum;
@@ -625,7 +631,7 @@ __device__ __forceinline__ void find_drawn(Draw& s, const uint64_t (&w)[PER], ui
         for (int j = 0; j < PER; ++j) {
             if (run <= draw && run + w[j] > draw) {
                 s.token = PER * tid + j;
-                s.wt = w[j];
+                s.logit = l[j];
             }
             run += w[j];
         }
@@ -633,14 +639,14 @@ __device__ __forceinline__ void find_drawn(Draw& s, const uint64_t (&w)[PER], ui
     __syncthreads();
 }
 
-// The chosen token's outputs.
+// The chosen token's outputs; x is its depth (it has a weight, so x < kRange), and total
+// the sum of the kept weights, 0 in a row without a live logit.
 template <int NT>
-__device__ __forceinline__ void write_token(const SampleArgs& a, int b, int token, uint64_t wt,
-                                            uint64_t total) {
+__device__ __forceinline__ void write_token(const SampleArgs& a, int b, int token, double x, uint64_t total) {
     const int tid = threadIdx.x;
     if (tid == 0) {
         a.token[b] = token;
-        if (a.prob) a.prob[b] = total ? (float)((double)wt / (double)total) : 0.0f;
+        if (a.prob) a.prob[b] = total ? (float)(exp_in(x) / (double)total) : 0.0f;
     }
     if (!a.x_next) return;
     const int d = a.d;
@@ -727,7 +733,7 @@ __global__ __launch_bounds__(NT) void sample_pick_kernel(const SampleArgs a) {
     if (tid == 0) {
         s_at = -1;
         s.token = 0;
-        s.wt = 0;
+        s.logit = -INFINITY;
     }
     __syncthreads();
     uint64_t run = inc_w - mine, total = 0;
@@ -743,7 +749,7 @@ __global__ __launch_bounds__(NT) void sample_pick_kernel(const SampleArgs a) {
     }
     __syncthreads();
     int token = 0;
-    uint64_t wt = 0;
+    float logit = -INFINITY;
     const int chunk = s_at;
     if (chunk >= 0) {  // (uniform; a row without a live logit has total 0 and token 0)
         const int i0 = chunk << a.chunk_sh;
@@ -794,7 +800,7 @@ __global__ __launch_bounds__(NT) void sample_pick_kernel(const SampleArgs a) {
                         const uint64_t w = kept_weight(l[r][j], base + j);
                         if (at <= want && at + w > want) {
                             s.token = base + j;
-                            s.wt = w;
+                            s.logit = l[r][j];
                         }
                         at += w;
                     }
@@ -803,9 +809,9 @@ __global__ __launch_bounds__(NT) void sample_pick_kernel(const SampleArgs a) {
         }
         __syncthreads();
         token = s.token;
-        wt = s.wt;
+        logit = s.logit;
     }
-    write_token<NT>(a, b, token, wt, total);
+    write_token<NT>(a, b, token, depth(logit, m, p.inv_t), total);
 }
 
 // A short row (V <= NT PER): element PER tid + j in register j of thread tid.  Weights are
@@ -865,8 +871,8 @@ __global__ __launch_bounds__(NT) void sample_row_kernel(const SampleArgs a) {
         sum += w[j];
     }
     const uint64_t total = group_sum_u64<NT>(sum, s.sum);
-    find_drawn<NT, PER>(s, w, drawn_mass(p.u, total));
-    write_token<NT>(a, b, max(s.token, 0), s.wt, total);
+    find_drawn<NT, PER>(s, l, w, drawn_mass(p.u, total));
+    write_token<NT>(a, b, max(s.token, 0), depth(s.logit, m, p.inv_t), total);
 }
 
 }  // namespace
