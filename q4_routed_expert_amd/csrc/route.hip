@@ -340,7 +340,8 @@ hipError_t launch_topk(const float* logits, int T, int E, int k, int32_t* idx, f
 //        (a fixed-order sum over the count table);
 //     2. one wave scans the totals, ceil(totals/32) and ceil(totals/128) over
 //        the experts: offsets and the first entry of each expert's tiles in
-//        both maps (the blocks share the writing of counts, offsets and both maps);
+//        both maps (block 0 writes counts, offsets and both maps, or, where there are
+//        many blocks, all of them share the writing);
 //     3. stable scatter: each wave owns 64 consecutive tokens; each lane ORs
 //        its bit into a 64-bit mask per expert, and the sorted row of
 //        (token, slot) is offsets[e] + rows of e in earlier blocks + rows of e
@@ -350,10 +351,11 @@ hipError_t launch_topk(const float* logits, int T, int E, int k, int32_t* idx, f
 // ---------------------------------------------------------------------------
 constexpr int kRouteBlock = MOE_ROUTE_BLOCK;
 constexpr int kRouteWaves = kRouteBlock / 64;
-constexpr int kScatterGroups = 4;  // of kRouteBlock threads share the count table's rows, at most
 static_assert(kRouteBlock % 64 == 0 && kRouteBlock >= kMaxExperts, "route block");
 
-__global__ __launch_bounds__(kScatterGroups * kRouteBlock) void route_scatter_kernel(
+// GROUPS of kRouteBlock threads share the count table's rows.
+template <int GROUPS>
+__global__ __launch_bounds__(GROUPS * kRouteBlock) void route_scatter_kernel(
     const int32_t* __restrict__ idx, int T, int k, int E, const int32_t* __restrict__ blk_counts,
     int n_blk, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
     int32_t* __restrict__ perm, int32_t* __restrict__ inv_perm, int32_t* __restrict__ block_map,
@@ -361,10 +363,9 @@ __global__ __launch_bounds__(kScatterGroups * kRouteBlock) void route_scatter_ke
     __shared__ unsigned long long mask[kRouteWaves][kMaxExperts];
     __shared__ int run[kRouteWaves][kMaxExperts];
     __shared__ int s_cnt[kMaxExperts], s_before[kMaxExperts];
-    __shared__ int s_tot4[kScatterGroups][kMaxExperts], s_bef4[kScatterGroups][kMaxExperts];
     __shared__ int s_off[kMaxExperts + 1], s_b32[kMaxExperts + 1], s_b128[kMaxExperts + 1];
     const int tid = threadIdx.x, lane = tid & 63, g = blockIdx.x;
-    const bool token = tid < kRouteBlock;            // the block's tokens: one per thread
+    const bool token = GROUPS == 1 || tid < kRouteBlock;  // the block's tokens: one per thread
     const int wave = token ? tid >> 6 : 0;
     // this block's selections, loaded first so that their round trip overlaps
     // the count-table reads below
@@ -376,13 +377,12 @@ __global__ __launch_bounds__(kScatterGroups * kRouteBlock) void route_scatter_ke
 
     // 1. totals and earlier-block counts: the groups of threads take runs of sixteen blocks
     // in turn (integer sums: the same in any order)
-    const int q = tid / kRouteBlock, ec = tid % kRouteBlock, n_threads = blockDim.x;
-    const int n_grp = n_threads / kRouteBlock;
+    const int q = GROUPS == 1 ? 0 : tid / kRouteBlock, ec = tid - q * kRouteBlock;
+    int tot = 0, before = 0;
     if (ec < E) {
         // sixteen blocks' counts in flight at a time (one load after another,
         // each waited for, would cost one memory round trip per block)
-        int tot = 0, before = 0;
-        for (int b0 = 16 * q; b0 < n_blk; b0 += 16 * n_grp) {
+        for (int b0 = 16 * q; b0 < n_blk; b0 += 16 * GROUPS) {
             int c[16];
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
@@ -397,17 +397,25 @@ __global__ __launch_bounds__(kScatterGroups * kRouteBlock) void route_scatter_ke
                 tot += v;
             }
         }
-        s_tot4[q][ec] = tot;
-        s_bef4[q][ec] = before;
     }
-    for (int i = tid; i < kRouteWaves * kMaxExperts; i += n_threads) (&mask[0][0])[i] = 0ull;
-    __syncthreads();
-    if (tid < E) {
-        int tot = 0, before = 0;
-        for (int p = 0; p < n_grp; ++p) {
-            tot += s_tot4[p][tid];
-            before += s_bef4[p][tid];
+    for (int i = tid; i < kRouteWaves * kMaxExperts; i += GROUPS * kRouteBlock) (&mask[0][0])[i] = 0ull;
+    if constexpr (GROUPS > 1) {
+        __shared__ int s_tot[GROUPS][kMaxExperts], s_bef[GROUPS][kMaxExperts];
+        if (ec < E) {
+            s_tot[q][ec] = tot;
+            s_bef[q][ec] = before;
         }
+        __syncthreads();
+        tot = before = 0;
+        if (tid < E) {
+#pragma unroll
+            for (int p = 0; p < GROUPS; ++p) {
+                tot += s_tot[p][tid];
+                before += s_bef[p][tid];
+            }
+        }
+    }
+    if (tid < E) {
         s_cnt[tid] = tot;
         s_before[tid] = before;
     }
@@ -461,7 +469,8 @@ __global__ __launch_bounds__(kScatterGroups * kRouteBlock) void route_scatter_ke
     for (int s = 0; s < kMaxTopK; ++s)
         if (valid && s < k) atomicOr(&mask[wave][ex[s]], 1ull << lane);
     __syncthreads();
-    if (tid < E && tid % n_blk == g) {  // 2b. counts, offsets and both maps, shared out over the blocks
+    // 2b. counts, offsets and both maps
+    if (tid < E && (GROUPS == 1 ? g == 0 : tid % n_blk == g)) {
         const int c = s_cnt[tid], o = s_off[tid];
         counts[tid] = c;
         offsets[tid] = o;
@@ -506,12 +515,15 @@ __global__ __launch_bounds__(kScatterGroups * kRouteBlock) void route_scatter_ke
 hipError_t launch_route_sort(const int32_t* idx, int T, int k, int E, const moe_routing* r,
                              hipStream_t s) {
     const int n_blk = (T + kRouteBlock - 1) / kRouteBlock;
-    // one group where sixteen blocks are all there are, else four (128 blocks: 24.7 us with
-    // one and 19.2 with four)
-    const int threads = n_blk > 16 ? kScatterGroups * kRouteBlock : kRouteBlock;
-    hipLaunchKernelGGL(route_scatter_kernel, dim3(n_blk), dim3(threads), 0, s, idx, T, k, E,
-                       r->blk_counts, n_blk, r->counts, r->offsets, r->perm, r->inv_perm,
-                       r->block_map, r->n_blocks, r->tile_map, r->n_tiles);
+    // one group where sixteen blocks are all there are, else four (128 blocks: 17.8 us with
+    // one and 12.7 with four; 8 blocks: 7.9 with one)
+    auto launch = [&](auto kernel, int threads) {
+        hipLaunchKernelGGL(kernel, dim3(n_blk), dim3(threads), 0, s, idx, T, k, E, r->blk_counts,
+                           n_blk, r->counts, r->offsets, r->perm, r->inv_perm, r->block_map,
+                           r->n_blocks, r->tile_map, r->n_tiles);
+    };
+    if (n_blk > 16) launch(route_scatter_kernel<4>, 4 * kRouteBlock);
+    else launch(route_scatter_kernel<1>, kRouteBlock);
     trace_point(s);
     return hipGetLastError();
 }
