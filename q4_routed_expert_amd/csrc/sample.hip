@@ -87,9 +87,12 @@ __device__ __forceinline__ double depth(float l, double m, double inv_t) {
 constexpr double kMagic = 6755399441055744.0;
 __device__ __forceinline__ int magic_int(double v) { return (int)(uint32_t)(uint64_t)__double_as_longlong(v); }
 
-// Bin of a depth below kRange; deeper logits have higher bins.
+// Bin of a depth below kRange; deeper logits have higher bins (the nearest integer, so
+// bin 0 is half as wide as the others).  Depths start at 0; the unsigned minimum keeps
+// the index inside the histogram also where the logits change under the call, so that
+// the maximum that was read is not theirs.
 __device__ __forceinline__ int bin_of(double x) {
-    return min(kBins - 1, magic_int(__builtin_fma(x, kBins / kRange, kMagic - 0.5)));
+    return (int)min((uint32_t)kBins - 1, (uint32_t)magic_int(__builtin_fma(x, kBins / kRange, kMagic)));
 }
 
 // 2^43 exp(-x) for 0 <= x < kRange.  x = n ln 2 - r with |r| <= ln 2 / 2; exp(r) =
