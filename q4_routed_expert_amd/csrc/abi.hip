@@ -5,6 +5,7 @@
 #include <stdio.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "internal.h"
@@ -264,7 +265,7 @@ int moe_route_scored(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t 
     if (spec->score != MOE_SCORE_SOFTMAX && spec->score != MOE_SCORE_SIGMOID)
         return fail(MOE_EINVAL, "spec.score=%d", spec->score);
     if (spec->renorm != 0 && spec->renorm != 1) return fail(MOE_EINVAL, "spec.renorm=%d", spec->renorm);
-    if (!(spec->scale > -3.4e38f && spec->scale < 3.4e38f))
+    if (!std::isfinite(spec->scale))
         return fail(MOE_EINVAL, "spec.scale must be finite");
     const int G = spec->n_groups;
     if (G < 1 || spec->top_groups < 1 || spec->top_groups > G)
@@ -643,7 +644,7 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
                     MOE_MAX_D);
     if (flags & ~(MOE_NORM_PLUS_ONE | MOE_NORM_RESIDUAL_FLOAT))
         return fail(MOE_EINVAL, "unknown flags 0x%x", flags);
-    if (!(eps >= 0.0f) || eps > 3.4e38f) return fail(MOE_EINVAL, "eps must be finite and >= 0");
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(MOE_EINVAL, "eps must be finite and >= 0");
     if ((rc = check_ptr(x, "x")) || (rc = check_ptr(weight, "weight")) ||
         (rc = check_ptr(residual, "residual", true)) ||
         (rc = check_ptr(residual_out, "residual_out", true)) || (rc = check_ptr(y, "y", true)) ||

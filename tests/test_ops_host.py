@@ -240,3 +240,14 @@ def test_sample_binding_refuses():
         a.update(kw)
         with pytest.raises(ValueError, match=what):
             q4.sample(a.pop("logits"), a.pop("u"), **a)
+
+
+def test_every_finite_number_is_taken():
+    # the largest fp32 numbers get as far as the next check
+    big = torch.finfo(f32).max
+    for scale in (big, -big):
+        assert _route(_spec(scale=scale, n_groups=0)) == _abi.MOE_EINVAL
+        assert b"n_groups" in _abi.lib().moe_last_error()
+    assert _norm(eps=big, x=None) == _abi.MOE_EINVAL
+    assert b"x is NULL" in _abi.lib().moe_last_error()
+
