@@ -154,12 +154,15 @@ void launch(const NormArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// One wave a row up to 512 columns (32768 rows of 512: 11.9 us, and 21.8 with four waves, of
-// which three would idle), else four (2048 columns: 39.9 us against 39.6 with one wave and
-// four pieces a lane; one row: 3.0 against 3.1).  32768 rows of 2048 with an fp32 residual
-// move 805 MB in 138 us, 5.8 TB/s.
+// As many waves a row as have a piece of 8 columns for most of their lanes: 32768 rows
+// with a bf16 residual take, for 512 columns, 24.1 us with one wave, 25.2 with two and
+// 36.2 with four; for 576 / 1024 28.8 / 46.2 with two and 39.9 / 47.4 with four (one wave
+// with two pieces a lane: 32.2 / 48.5); for 1088 / 2048 50.9 / 90.8 with four, 53.5 / 93.1
+// with two.  One row: 1.9 us in every form, but 2.3 to 3.0 with more than one piece.
+// 32768 rows of 2048 with an fp32 residual move 805 MB in 138 us, 5.8 TB/s.
 hipError_t launch_add_norm(const NormArgs& a, hipStream_t s) {
     if (a.d <= 512) launch<1, 1>(a, s);
+    else if (a.d <= 1024) launch<2, 1>(a, s);
     else if (a.d <= 2048) launch<4, 1>(a, s);
     else if (a.d <= 4096) launch<4, 2>(a, s);
     else launch<4, 4>(a, s);
