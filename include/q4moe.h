@@ -341,7 +341,8 @@ int moe_route_scored(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t 
    Of lm only V, and with x_next also d and embed, are used.  logits and x_next
    are 16-byte aligned, the other arrays 4-byte.  1 <= B <= MOE_MAX_SAMPLE_ROWS.
    ws must hold moe_sample_workspace_bytes(V, B) bytes (no initialisation, not
-   preserved); a workspace for more rows of the same V serves fewer. */
+   preserved); a workspace for more rows of the same V serves fewer.  Calls that may
+   run at the same time (on two streams, or replays of two graphs) need one each. */
 #define MOE_MAX_SAMPLE_ROWS 1024
 typedef struct {
     const float* u;             /* [B] uniform numbers */
@@ -365,7 +366,8 @@ int moe_sample(const moe_lm_head* lm, const float* logits, int32_t B, const moe_
      y[t][n] = sum_k w(n, k) * x[t][k]      w = bf16(q * scale + bias), fp32 sums
    for matrix 0 of m, N rows by K columns.  x: bf16 [T][K]; y: fp32 [T][N], or
    bf16 (one rounding of the fp32 sum) with MOE_OUT_BF16.  Each weight is read
-   and dequantised once for all rows.  1 <= T <= MOE_MAX_LINEAR_TOKENS,
+   and dequantised once for all rows of x (N >= 8192) or for every 16 of them (fewer
+   rows of m).  1 <= T <= MOE_MAX_LINEAR_TOKENS,
    1 <= N <= MOE_MAX_VOCAB, K a multiple of 64, <= MOE_MAX_D.  y must not overlap
    x or m.  A row's result does not depend on the other rows of x or on their
    number: T rows at once give what T calls of one row give.  One kernel, no

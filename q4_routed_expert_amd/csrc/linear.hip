@@ -2,10 +2,11 @@
 // 4-bit matrix (moe_linear): projections and the output head of a decode step
 // for several sequences or drafted tokens.
 //
-// Work: N K / 2 bytes of codes and N K / 16 of scales and biases, each read once,
-// 2 T N K operations on the matrix cores.  A weight is dequantised once for all
-// T tokens (2.4 vector operations per weight), so up to the widest batch the
-// bound is the weight stream, with the dequantisation close behind.
+// Work: N K / 2 bytes of codes and N K / 16 of scales and biases, 2 T N K operations on
+// the matrix cores.  With many rows (the streaming kernel) a weight is read and
+// dequantised once for all T tokens (2.4 vector operations per weight), and for few
+// tokens the bound is the weight stream, with the dequantisation close behind; with few
+// rows (the split kernel) once for every 16 tokens.
 //
 // Matrix operands: v_mfma_f32_16x16x32_bf16 with 16 weight rows as A and 16
 // tokens as B.  Lane (r = lane & 15, g = lane >> 4) holds row r's codes of columns
@@ -20,8 +21,9 @@
 //                         share K and whose sums meet in LDS (else most CUs would idle)
 //   linear_stream_kernel  many rows: every wave or pair of waves owns its tiles; x goes
 //                         through LDS
-// Measured: 248320 x 2048 for 8 tokens in 61 us (4.8 TB/s), for 64 in 154; 30011 x 8192 for
-// 8 in 40, for 64 in 76; 2048 x 2048 for one in 4.4.
+// Measured (graph replays over three or four matrices in turn), for 8 / 16 / 32 / 64 tokens:
+// 248320 x 2048 in 62 / 64 / 75 / 134 us (8: 4.7 TB/s), 30011 x 8192 in 39 / 44 / 52 / 69;
+// 2048 x 2048 for one in 4.0, for 64 in 8.4.
 #include "ops.h"
 
 namespace q4moe {
@@ -147,6 +149,10 @@ __device__ __forceinline__ u32x4 shift_groups(const Unaligned& v, int n) {
 // from that lane.  Loaded per chunk, 16 bytes from each of 16 rows, they cost as much time
 // as the codes: the vector caches serve cache lines, not bytes (measured at N = 30011,
 // K = 8192, one token: 46.5 us, and 35 without any scale loads).
+// Registers: with room for 64 tokens 16 waves have too few of them in some forms.  kWave
+// (K <= 1024) keeps 9 to 12 of a lane's values in scratch memory, kChunked 4 to 8 where K
+// is not a multiple of 2048 (64 tokens, 40000 x 1024: 17 us; 30011 x 8128: 74 us, and
+// 69 at 8192 columns).
 // FULL: K is a multiple of 2048 (no branches between the loads).  VEC: of 512 (no chunk is
 // cut short, a row's scales start on 16 bytes).
 constexpr int kChunk = 512;
@@ -379,15 +385,23 @@ template <int NB, Mode MODE>
 void launch_stream(const LinearArgs& a, hipStream_t s) {
     const int tiles = (a.N + 15) / 16, units = MODE == kChunked ? (tiles + 7) / 8 : tiles;
     const int grid = units < kCus ? units : kCus;
-    if (a.K % 2048 == 0) linear_stream_kernel<NB, MODE, true, true><<<grid, kThreads, 0, s>>>(a);
-    else if (a.K % kChunk == 0) linear_stream_kernel<NB, MODE, false, true><<<grid, kThreads, 0, s>>>(a);
+    if constexpr (MODE == kChunked || NB <= 32) {  // (64 tokens of 2048 columns do not fit the LDS)
+        if (a.K % 2048 == 0) {
+            linear_stream_kernel<NB, MODE, true, true><<<grid, kThreads, 0, s>>>(a);
+            return;
+        }
+    }
+    if (a.K % kChunk == 0) linear_stream_kernel<NB, MODE, false, true><<<grid, kThreads, 0, s>>>(a);
     else linear_stream_kernel<NB, MODE, false, false><<<grid, kThreads, 0, s>>>(a);
 }
 
-// By rows, one token / 64 tokens, K = 2048: 4096 rows 4.5 / 15.1 us split and 6.1 / 17.9
-// streamed; 6000 rows 6.8 / 16.7 (two tiles) and 6.7 / 19.1; 8192 rows 7.0 / 19.3 streamed
-// and 10.9 / 19.7 split with four tiles.  Pairs of waves: 16384 rows 8.0 us against 8.8 with
-// one wave a tile, 30011 x 8192 38.6 against 39.8.
+// By rows, from both sides' times (us; the choice has to go by N and K alone, so that T
+// tokens give the bits of T single ones).  At 4096 rows, one token / 64 tokens, split with
+// one tile and streamed: K = 512 2.9 / 5.9 and 3.6 / 6.2, 2048 4.2 / 14.7 and 5.9 / 17.2,
+// 8192 9.6 / 51 and 15.8 / 56.  At 6000, split with two tiles and streamed: 3.3 / 6.4 and
+// 3.6 / 6.3, 6.2 / 16.4 and 6.2 / 17.9, 15.7 / 55 and 16.9 / 56.  At 8192: 3.4 / 7.2 and
+// 3.7 / 6.5, 6.6 / 20.8 and 6.3 / 18.3, 15.9 / 72 and 17.1 / 57.  Pairs of waves against one
+// wave a tile, 16384 rows, one token: 4.0 and 4.3, 7.0 and 7.9, 20.6 and 22.2.
 template <int NB>
 void launch(const LinearArgs& a, hipStream_t s) {
     const bool fits = NB * ((a.K + kStep - 1) / kStep) <= 512;  // x in 128 KB

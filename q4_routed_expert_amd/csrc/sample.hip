@@ -25,9 +25,12 @@
 //   4. sample_pick_kernel    one work group per row: the exact cut, the chunk that holds
 //                            the drawn mass, the token in it, its embedding row
 // A row without top-k and top-p needs no cut: kernel 2 writes the chunks' masses
-// itself.  If the list overflows (more than 4096 tokens, or 2048 of one chunk:
-// thousands of equal logits at the cut, or such a top-k), kernel 4 narrows over the whole
-// row instead.
+// itself.  If the list overflows (more than 4096 tokens, or 2048 of one chunk), kernel 4
+// narrows over the whole row instead, some 70 us a pass at V = 248320.  That takes
+// thousands of equal logits at the cut, a top-k in the thousands, or a flat row under
+// top-p: a bin is 0.0148 wide, and 248320 normal logits of spread / temperature 0.36 put
+// 4096 into the one at their middle (one row and 64 rows of 248320: 0.13 and 0.35 ms at
+// 0.2 with top-p 0.9, 0.38 and 0.36 with top-k 20000; all logits equal, one row: 0.58).
 // Short rows (sample_row_kernel): one work group does all of it with the row in its
 // registers.
 #include <float.h>
