@@ -56,9 +56,8 @@ def _check(code: int, where: str):
         raise MoEError(code, where)
 
 
-def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+def _stream() -> int:
+    return int(torch.cuda.current_stream().cuda_stream)
 
 
 def _ptr(t):
@@ -85,30 +84,31 @@ def _on_gpu(**tensors):
             raise ValueError(f"{name} must be on the GPU")
 
 
-def _made(stream, make, *args, **kw):
-    """make(*args, **kw), a tensor or a DeviceRouting of the call's own, on the stream
-    that the call launches on.  Memory taken from another stream's pool may still be in
-    use by that stream's queued work, its fills are not ordered before the call's
-    kernels, and once dropped it goes to that stream's next tensor, which does not
-    wait for them either."""
-    if stream is None:
-        return make(*args, **kw)
+def _on_stream(call, args: dict):
+    """call(**args) with args["stream"] current.  A call's own buffers (outputs,
+    routings, workspaces) then come from the stream it launches on: memory from another
+    stream's pool may still be in use by that stream's queued work, its fills are not
+    ordered before the call's kernels, and once dropped it goes to that stream's next
+    tensor, which does not wait for them either."""
+    stream = args.pop("stream")
+    caller = torch.cuda.current_stream(stream.device)
     with torch.cuda.stream(stream):
-        out = make(*args, **kw)
-    _used_on(torch.cuda.current_stream(stream.device), out)  # by the caller, after a wait
+        out = call(**args)
+    _used_on(stream, *args.values())
+    _used_on(caller, *(out if isinstance(out, tuple) else (out,)))  # after a wait
     return out
 
 
-def _used_on(stream, *tensors):
-    """Keeps the tensors' memory from being handed out again before the work that is
-    now on `stream` (None: the current one) is done."""
-    if stream is None:
-        return
-    for t in tensors:
-        if isinstance(t, DeviceRouting):
-            _used_on(stream, *(getattr(t, f) for f, _ in _abi.Routing._fields_))
-        elif t is not None and t.is_cuda:
-            t.record_stream(stream)
+def _used_on(stream, *values):
+    """Keeps the memory of the tensors among the values from being handed out again
+    before the work that is now on `stream` is done."""
+    for v in values:
+        if isinstance(v, DeviceRouting):
+            _used_on(stream, *(getattr(v, f) for f, _ in _abi.Routing._fields_))
+        elif isinstance(v, RouterSpec):
+            _used_on(stream, v.balance)
+        elif isinstance(v, torch.Tensor) and v.is_cuda:
+            v.record_stream(stream)
 
 
 def _dev(a: np.ndarray, device) -> torch.Tensor:
@@ -183,8 +183,10 @@ def workspace(layer: DeviceLayer, T: int, device="cuda") -> torch.Tensor:
 
 def route(layer: DeviceLayer, x: torch.Tensor, routing: DeviceRouting | None = None,
           logits_in: bool = False, stream=None) -> DeviceRouting:
+    if stream is not None:
+        return _on_stream(route, locals())
     T = x.shape[0]
-    r = routing or _made(stream, DeviceRouting, T, layer.n_experts, layer.top_k, x.device)
+    r = routing or DeviceRouting(T, layer.n_experts, layer.top_k, x.device)
     flags = MOE_LOGITS_IN if logits_in else 0
     if not logits_in:
         _need(x, "x", torch.bfloat16, T * layer.d)
@@ -192,8 +194,7 @@ def route(layer: DeviceLayer, x: torch.Tensor, routing: DeviceRouting | None = N
     _need(r.perm, "routing.perm", torch.int32, T * layer.top_k)
     _on_gpu(x=None if logits_in else x, logits=r.logits)
     _check(_abi.lib().moe_route(C.addressof(layer.struct), _ptr(x), T, flags, C.addressof(r.struct),
-                                _stream(stream)), "moe_route")
-    _used_on(stream, x, r)
+                                _stream()), "moe_route")
     return r
 
 
@@ -223,6 +224,8 @@ def route_scored(layer: DeviceLayer, x: torch.Tensor | None, spec: RouterSpec,
     """Routing with the scores and the selection of `spec`.  Follow it with prefill,
     or with decode / decode_tokens and routing_in=True.  With logits_in the T =
     routing.T rows of routing.logits are routed; x is not used."""
+    if stream is not None:
+        return _on_stream(route_scored, locals())
     if logits_in:
         if routing is None:
             raise ValueError("logits_in needs a routing that holds the logits")
@@ -231,19 +234,18 @@ def route_scored(layer: DeviceLayer, x: torch.Tensor | None, spec: RouterSpec,
         T = x.shape[0]
         _need(x, "x", torch.bfloat16, T * layer.d)
         if routing is None:
-            routing = _made(stream, DeviceRouting, T, layer.n_experts, layer.top_k, x.device)
+            routing = DeviceRouting(T, layer.n_experts, layer.top_k, x.device)
     r = routing
     if r.T < T or r.E != layer.n_experts or r.k != layer.top_k:
         raise ValueError(f"routing is for T={r.T} E={r.E} k={r.k}, the call for T={T} "
                          f"E={layer.n_experts} k={layer.top_k}")
     if spec.balance is not None:
         _need(spec.balance, "balance", torch.float32, layer.n_experts)
-    s = _launch_on("route_scored", stream, x=None if logits_in else x, logits=r.logits,
+    s = _launch_on("route_scored", x=None if logits_in else x, logits=r.logits,
                    balance=spec.balance)
     _check(_abi.lib().moe_route_scored(C.addressof(layer.struct), None if logits_in else _ptr(x), T,
                                        MOE_LOGITS_IN if logits_in else 0, C.addressof(spec.struct),
                                        C.addressof(r.struct), s), "moe_route_scored")
-    _used_on(stream, None if logits_in else x, spec.balance, r)
     return r
 
 
@@ -256,13 +258,15 @@ def prefill(layer: DeviceLayer, x: torch.Tensor, routing: DeviceRouting,
             stream=None, item_rows: int = 128) -> torch.Tensor:
     """moe_prefill (item_rows = 128) or moe_prefill_ex with the gate/up work-item
     height item_rows (64, 32 or 16)."""
+    if stream is not None:
+        return _on_stream(prefill, locals())
     if item_rows not in _ITEM_ROWS_FLAGS:
         raise ValueError(f"item_rows must be one of 128, 64, 32, 16, not {item_rows}")
     T = x.shape[0]
     if ws is None:
-        ws = _made(stream, workspace, layer, T, x.device)
+        ws = workspace(layer, T, x.device)
     if y is None:
-        y = _made(stream, torch.empty, (T, layer.d), dtype=torch.bfloat16, device=x.device)
+        y = torch.empty((T, layer.d), dtype=torch.bfloat16, device=x.device)
     _need(x, "x", torch.bfloat16, T * layer.d)
     _need(y, "y", torch.bfloat16, T * layer.d)
     _need(routing.perm, "routing.perm", torch.int32, T * layer.top_k)
@@ -270,14 +274,13 @@ def prefill(layer: DeviceLayer, x: torch.Tensor, routing: DeviceRouting,
     if item_rows == 128:
         _check(_abi.lib().moe_prefill(C.addressof(layer.struct), _ptr(x), T,
                                       C.addressof(routing.struct), _ptr(ws), ws.numel(), _ptr(y),
-                                      _stream(stream)),
+                                      _stream()),
                "moe_prefill")
     else:
         _check(_abi.lib().moe_prefill_ex(C.addressof(layer.struct), _ptr(x), T,
                                          C.addressof(routing.struct), _ptr(ws), ws.numel(),
-                                         _ptr(y), _ITEM_ROWS_FLAGS[item_rows], _stream(stream)),
+                                         _ptr(y), _ITEM_ROWS_FLAGS[item_rows], _stream()),
                "moe_prefill_ex")
-    _used_on(stream, x, routing, ws, y)
     return y
 
 
@@ -302,16 +305,17 @@ def decode(layer: DeviceLayer, x: torch.Tensor, ws: torch.Tensor, y: torch.Tenso
            stream=None, routing_in: bool = False) -> torch.Tensor:
     """The layer for one token.  routing_in: the selection in routing (from route or
     route_scored) is used instead of the layer's own routing."""
+    if stream is not None:
+        return _on_stream(decode, locals())
     if y is None:
-        y = _made(stream, torch.empty, (1, layer.d), dtype=torch.bfloat16, device=x.device)
+        y = torch.empty((1, layer.d), dtype=torch.bfloat16, device=x.device)
     rs = C.addressof(routing.struct) if routing is not None else None
     _need(x, "x", torch.bfloat16, layer.d)
     _need(y, "y", torch.bfloat16, layer.d)
     flags = _decode_flags(layer, 1, routing, logits_in, routing_in)
     _on_gpu(x=x, y=y, ws=ws)
     _check(_abi.lib().moe_decode(C.addressof(layer.struct), _ptr(x), flags, rs, _ptr(ws), ws.numel(),
-                                 _ptr(y), _stream(stream)), "moe_decode")
-    _used_on(stream, x, routing, ws, y)
+                                 _ptr(y), _stream()), "moe_decode")
     return y
 
 
@@ -321,27 +325,29 @@ def decode_tokens(layer: DeviceLayer, x: torch.Tensor, ws: torch.Tensor,
                   routing_in: bool = False) -> torch.Tensor:
     """The decode layer for T = x.shape[0] tokens (1 <= T <= MAX_DECODE_TOKENS).
     routing_in: as decode's."""
+    if stream is not None:
+        return _on_stream(decode_tokens, locals())
     T = x.shape[0]
     if y is None:
-        y = _made(stream, torch.empty, (T, layer.d), dtype=torch.bfloat16, device=x.device)
+        y = torch.empty((T, layer.d), dtype=torch.bfloat16, device=x.device)
     rs = C.addressof(routing.struct) if routing is not None else None
     _need(x, "x", torch.bfloat16, T * layer.d)
     _need(y, "y", torch.bfloat16, T * layer.d)
     flags = _decode_flags(layer, T, routing, logits_in, routing_in)
     _on_gpu(x=x, y=y, ws=ws)
     _check(_abi.lib().moe_decode_tokens(C.addressof(layer.struct), _ptr(x), T, flags, rs, _ptr(ws),
-                                        ws.numel(), _ptr(y), _stream(stream)), "moe_decode_tokens")
-    _used_on(stream, x, routing, ws, y)
+                                        ws.numel(), _ptr(y), _stream()), "moe_decode_tokens")
     return y
 
 
 def dequant(q: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor, stream=None) -> torch.Tensor:
     """bf16 [N, K] from one Q4 matrix (q int32 [N, K/8], scale/bias bf16 bits [N, K/64])."""
+    if stream is not None:
+        return _on_stream(dequant, locals())
     N, K = q.shape[0], q.shape[1] * 8
-    out = _made(stream, torch.empty, (N, K), dtype=torch.bfloat16, device=q.device)
+    out = torch.empty((N, K), dtype=torch.bfloat16, device=q.device)
     m = _abi.Q4Mat(_ptr(q), _ptr(scale), _ptr(bias))
-    _check(_abi.lib().moe_dequant(C.addressof(m), N, K, _ptr(out), _stream(stream)), "moe_dequant")
-    _used_on(stream, q, scale, bias, out)
+    _check(_abi.lib().moe_dequant(C.addressof(m), N, K, _ptr(out), _stream()), "moe_dequant")
     return out
 
 
@@ -378,11 +384,13 @@ def lm_argmax(lm: DeviceLmHead, x: torch.Tensor | None, ws: torch.Tensor,
               x_next: torch.Tensor | None = None, logits_in: bool = False, stream=None):
     """Greedy token hand-off: (logits fp32 [V], token int32 [1], x_next or None).
     With logits_in the given logits are read instead of computed from x."""
+    if stream is not None:
+        return _on_stream(lm_argmax, locals())
     dev = ws.device
     if logits is None:
-        logits = _made(stream, torch.empty, lm.V, dtype=torch.float32, device=dev)
+        logits = torch.empty(lm.V, dtype=torch.float32, device=dev)
     if token is None:
-        token = _made(stream, torch.empty, 1, dtype=torch.int32, device=dev)
+        token = torch.empty(1, dtype=torch.int32, device=dev)
     flags = MOE_LOGITS_IN if logits_in else 0
     if not logits_in:
         _need(x, "x", torch.bfloat16, lm.d)
@@ -393,8 +401,7 @@ def lm_argmax(lm: DeviceLmHead, x: torch.Tensor | None, ws: torch.Tensor,
     _on_gpu(x=None if logits_in else x, logits=logits, token=token, x_next=x_next, ws=ws)
     _check(_abi.lib().moe_lm_argmax(C.addressof(lm.struct), _ptr(x), flags, _ptr(logits),
                                     _ptr(token), _ptr(x_next), _ptr(ws), ws.numel(),
-                                    _stream(stream)), "moe_lm_argmax")
-    _used_on(stream, None if logits_in else x, logits, token, x_next, ws)
+                                    _stream()), "moe_lm_argmax")
     return logits, token, x_next
 
 
@@ -402,10 +409,10 @@ def lm_argmax(lm: DeviceLmHead, x: torch.Tensor | None, ws: torch.Tensor,
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _launch_on(where: str, stream, **tensors) -> int:
-    """Stream handle for a call whose tensors are `tensors` (None: absent).  All of
-    them have to be on one GPU, and that GPU has to be the current one, because the
-    library launches on the current device."""
+def _launch_on(where: str, **tensors) -> int:
+    """The current stream's handle for a call whose tensors are `tensors` (None: absent).
+    All of them have to be on one GPU, and that GPU has to be the current one, because
+    the library launches on the current device."""
     dev = -1
     for name, t in tensors.items():
         if t is None:
@@ -420,12 +427,7 @@ def _launch_on(where: str, stream, **tensors) -> int:
     if dev != torch.cuda.current_device():
         raise ValueError(f"{where}: the tensors are on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    if stream is None:
-        return _raw_stream(dev)
-    if stream.device.index != dev:
-        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on cuda:{dev}")
-    _used_on(stream, *tensors.values())
-    return stream.cuda_stream
+    return _raw_stream(dev)
 
 
 def sample_workspace(B: int, V: int, device="cuda") -> torch.Tensor:
@@ -445,6 +447,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     (0: off), top_p (1: off) and min_p (0: off) are numbers for all rows or tensors [B]
     on the GPU (fp32; top_k int32).  x_next [B, d] needs lm, whose embedding rows it
     gets.  ws: sample_workspace(B, V) or larger."""
+    if stream is not None:
+        return _on_stream(sample, locals())
     if logits.dim() != 2:
         raise ValueError(f"logits must be [B, V], not {tuple(logits.shape)}")
     B, V = logits.shape
@@ -463,9 +467,9 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
                 raise ValueError(f"{name}: {v} is not an int32")
             setattr(p, name + "_all", v)
     if token is None:
-        token = _made(stream, logits.new_empty, B, dtype=torch.int32)
+        token = logits.new_empty(B, dtype=torch.int32)
     if prob is None:
-        prob = _made(stream, logits.new_empty, B)
+        prob = logits.new_empty(B)
     _need(token, "token", torch.int32, B)
     _need(prob, "prob", torch.float32, B)
     if x_next is not None:
@@ -476,9 +480,9 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     else:
         head = _abi.LmHead(V)
     if ws is None:
-        ws = _made(stream, sample_workspace, B, V, logits.device)
+        ws = sample_workspace(B, V, logits.device)
     _need(ws, "ws", torch.uint8, 1)
-    s = _launch_on("sample", stream, logits=logits, token=token, prob=prob, x_next=x_next, ws=ws,
+    s = _launch_on("sample", logits=logits, token=token, prob=prob, x_next=x_next, ws=ws,
                    **rows)
     _check(_abi.lib().moe_sample(C.addressof(head), _ptr(logits), B, C.addressof(p), _ptr(token),
                                  _ptr(prob), _ptr(x_next), _ptr(ws), ws.numel(), s), "moe_sample")
@@ -491,6 +495,8 @@ def linear(q: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor, x: torch.Te
     """y [T, N] = x [T, K] times the transposed Q4 matrix (q int32 [N, K/8], scale and
     bias bf16 or their bits [N, K/64]), 1 <= T <= MAX_LINEAR_TOKENS; out_dtype fp32
     or bf16."""
+    if stream is not None:
+        return _on_stream(linear, locals())
     if x.dim() != 2 or q.dim() != 2:
         raise ValueError(f"x must be [T, K] and q [N, K/8], not {tuple(x.shape)}, {tuple(q.shape)}")
     T, K = x.shape
@@ -500,13 +506,13 @@ def linear(q: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor, x: torch.Te
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, not {out_dtype}")
     if y is None:
-        y = _made(stream, x.new_empty, (T, N), dtype=out_dtype)
+        y = x.new_empty((T, N), dtype=out_dtype)
     _need(x, "x", torch.bfloat16, T * K)
     _need(q, "q", torch.int32, N * K // 8)
     for name, t in (("scale", scale), ("bias", bias)):
         _need(t, name, torch.int16 if t.dtype == torch.int16 else torch.bfloat16, N * (K // 64))
     _need(y, "y", out_dtype, T * N)
-    s = _launch_on("linear", stream, q=q, scale=scale, bias=bias, x=x, y=y)
+    s = _launch_on("linear", q=q, scale=scale, bias=bias, x=x, y=y)
     m = _abi.Q4Mat(_ptr(q), _ptr(scale), _ptr(bias))
     _check(_abi.lib().moe_linear(C.addressof(m), N, K, _ptr(x), T,
                                  _abi.MOE_OUT_BF16 if out_dtype == torch.bfloat16 else 0, _ptr(y),
@@ -525,6 +531,8 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     y (bf16) is written when given, and by default when no 8-bit output is asked
     for; e4m3=True (or y8 and y8_scale given) asks for e4m3 codes [T, d] with one
     fp32 scale per 64 columns [T, d / 64]."""
+    if stream is not None:
+        return _on_stream(add_norm, locals())
     if x.dim() != 2:
         raise ValueError(f"x must be [T, d], not {tuple(x.shape)}")
     T, d = x.shape
@@ -541,16 +549,16 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     e4m3 = e4m3 or y8 is not None or y8_scale is not None
     if e4m3:
         if y8 is None:
-            y8 = _made(stream, torch.empty_like, x, dtype=torch.float8_e4m3fn)
+            y8 = torch.empty_like(x, dtype=torch.float8_e4m3fn)
         if y8_scale is None:
-            y8_scale = _made(stream, x.new_empty, (T, d // 64), dtype=torch.float32)
+            y8_scale = x.new_empty((T, d // 64), dtype=torch.float32)
         _need(y8, "y8", torch.float8_e4m3fn, T * d)
         _need(y8_scale, "y8_scale", torch.float32, T * (d // 64))
     elif y is None:
-        y = _made(stream, torch.empty_like, x)
+        y = torch.empty_like(x)
     if y is not None:
         _need(y, "y", torch.bfloat16, T * d)
-    s = _launch_on("add_norm", stream, x=x, weight=weight, residual=residual,
+    s = _launch_on("add_norm", x=x, weight=weight, residual=residual,
                    residual_out=residual_out, y=y, y8=y8, y8_scale=y8_scale)
     _check(_abi.lib().moe_add_norm(_ptr(x), T, d, _ptr(residual), _ptr(residual_out), _ptr(weight),
                                    eps, flags, _ptr(y), _ptr(y8), _ptr(y8_scale), s),
