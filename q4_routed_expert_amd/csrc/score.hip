@@ -258,8 +258,9 @@ __global__ __launch_bounds__(64 * kWaves) void select_kernel(const ScoreArgs a) 
 // The whole sort for a few tokens by one work group, in one launch: wave w selects for
 // token w; a mask of tokens per expert then gives counts (its population) and places (the
 // population below a token); the first wave scans counts, 32-row tiles and 128-row tiles
-// over the experts.  One token a wave: at 1 / 8 / 16 tokens 6.0 / 7.2 / 9.9 us against 10.8 /
-// 11.6 / 11.8 of the three launches, at 32 tokens (two a wave) 15.3 against 11.6.
+// over the experts.  One token a wave: 1 / 8 / 16 tokens of 256 sigmoid scores in groups
+// take 4.8 / 6.2 / 8.1 us against 9.0 / 9.9 / 9.8 of the three launches (graph replays);
+// two tokens a wave, at 32, took 15.3 against 11.6.
 constexpr int kSmallWaves = 16;
 constexpr int kSmallTokens = kSmallWaves;
 
