@@ -79,8 +79,8 @@ def linear(q, scale, bias, x):
 
 
 def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
-    """(token, prob) of one row, with weights in units of 2^-43 as exact integers; the
-    parameters are fp32 values."""
+    """(token, prob) of one row, with weights in units of 2^-43 as exact integers, the
+    token's own in prob unrounded; the parameters are fp32 values."""
     l = np.asarray(logits, np.float32).astype(np.float64)
     u, temperature, top_p, min_p = (float(np.float32(v)) for v in (u, temperature, top_p, min_p))
     V = l.size
@@ -110,4 +110,5 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     total = int(cum[-1])
     draw = min(int(Fraction(max(float(u), 0.0)) * total), total - 1)
     at = int(np.searchsorted(cum, np.uint64(draw), side="right"))
-    return int(kept[at]), int(w[kept[at]]) / total
+    token = int(kept[at])
+    return token, math.exp((min(l[token], big) - m) / t) * 2.0 ** 43 / total
