@@ -390,7 +390,8 @@ int moe_linear(const moe_q4mat* m, int32_t N, int32_t K, const uint16_t* x, int3
        without a residual it has to be NULL
      y: bf16 [T][d] (one rounding), or NULL
      y8, y8_scale: the row in 8 bits, or both NULL: y8 e4m3 (OCP) [T][d] and one
-       fp32 scale per 64 columns, [T][d/64]: scale = max|y| / 448 over the group,
+       fp32 scale per 64 columns, [T][d/64], or with MOE_NORM_GROUP_128 per 128
+       (the 8-bit products' x_scale), [T][ceil(d/128)]: scale = max|y| / 448 over the group,
        y8 = e4m3(y / scale), to nearest even, from the unrounded y and the stored
        scale, at most 448.  Where the scale is 0 (a group of zeros, or of values
        up to 448 * 2^-150) the codes are 0; an infinite y makes its group's scale
@@ -401,12 +402,116 @@ int moe_linear(const moe_q4mat* m, int32_t N, int32_t K, const uint16_t* x, int3
    of 64, <= MOE_MAX_D; eps finite, >= 0.  One kernel, no workspace. */
 #define MOE_NORM_PLUS_ONE 1u
 #define MOE_NORM_RESIDUAL_FLOAT 2u
+#define MOE_NORM_GROUP_128 8u
 int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
                  void* residual_out, const uint16_t* weight, float eps, uint32_t flags,
                  uint16_t* y, uint8_t* y8, float* y8_scale, void* stream);
 
+/* Products in 8 bits: e4m3 (OCP) codes with one fp32 scale per token and
+   MOE_E4M3_BLOCK columns of x, and one per MOE_E4M3_BLOCK x MOE_E4M3_BLOCK block of
+   the matrix:
+     y[t][n] = sum_b xs[t][b] * ws[n / 128][b] * sum_{k in block b} x[t][k] * w(n, k)
+   with exact products, a block's sum in fp32 and the blocks added in
+   fp32.  A last block of columns or rows may be shorter than 128.  A NaN code or a scale
+   that is not finite gives what the formula gives.
+   y: fp32 [T][N], or bf16 (one rounding) with MOE_OUT_BF16, or with MOE_GATED 8 bits:
+   then w and scale hold two matrices of I = N / 2 rows each, [2][I][K] and
+   [2][ceil(I/128)][ceil(K/128)], the gate's and the up matrix's, and
+     h[t][i] = silu(gate sum) * up sum            (fp32, silu(g) = g / (1 + exp(-g)))
+     y_scale[t][j] = max |h| / 448 over columns 128 j .. + 127,  y = e4m3(h / y_scale)
+   to nearest even, y [T][I] and y_scale [T][ceil(I/128)], with moe_add_norm's rules for
+   zeros, infinities and NaN: the next product's x and x_scale.  y_scale is NULL
+   otherwise.
+   x: [T][K] codes; x_scale: [T][ceil(K/128)].  K a multiple of 64, <= MOE_MAX_D;
+   1 <= N <= MOE_MAX_VOCAB, with MOE_GATED a multiple of 128; 1 <= T <= MOE_MAX_TOKENS.
+   Outputs must not overlap inputs.  One kernel, no workspace; equal calls give equal
+   results. */
+#define MOE_E4M3_BLOCK 128
+#define MOE_GATED 2u
+typedef struct {
+    const uint8_t* w;     /* [n_mat][N][K] e4m3 codes */
+    const float* scale;   /* [n_mat][ceil(N/128)][ceil(K/128)] */
+} moe_e4m3mat;
+int moe_linear_scaled(const moe_e4m3mat* m, int32_t N, int32_t K, const uint8_t* x,
+                    const float* x_scale, int32_t T, uint32_t flags, void* y, float* y_scale,
+                    void* stream);
+/* The same products over expert-sorted rows, a matrix per expert: m holds E of them
+   (gated: E times two), x and x_scale have T * k rows in the order of a routing
+   of T tokens (what moe_dispatch writes), and row j of expert e, offsets[e] <= j <
+   offsets[e + 1], is multiplied with matrix e.  Of r, offsets, block_map, n_blocks,
+   tile_map and n_tiles are read.  1 <= E <= MOE_MAX_EXPERTS, 1 <= k <= min(MOE_MAX_TOPK,
+   E). */
+int moe_experts_scaled(const moe_e4m3mat* m, int32_t E, int32_t N, int32_t K, const uint8_t* x,
+                     const float* x_scale, int32_t T, int32_t k, const moe_routing* r,
+                     uint32_t flags, void* y, float* y_scale, void* stream);
+
+/* Token rows into expert order and back, for expert products other than moe_prefill's,
+   which has both built in.  Of r, inv_perm is read, and topk_w where weights are used.
+   All rows have d columns, d a multiple of 64, <= MOE_MAX_D; 1 <= T <= MOE_MAX_TOKENS,
+   1 <= k <= MOE_MAX_TOPK.  Outputs must not overlap inputs or each other, but for base
+   and d_rows as said below.
+   moe_dispatch: rows[inv_perm[t * k + s]] = x[t] for every slot s.  x: bf16 [T][d]; rows:
+   bf16 [T * k][d] with rows_scale NULL, else e4m3 codes [T * k][d] and rows_scale
+   [T * k][ceil(d/128)]: scale = max |x| / 448 over 128 columns, codes of x / scale to
+   nearest even, with moe_add_norm's rules for zeros, infinities and NaN.
+   moe_combine: y[t] = sum_s w[t][s] * rows[inv_perm[t * k + s]] + base[t], in fp32,
+   slots in order, base last, rounded once.  w = topk_w, or 1 with MOE_UNWEIGHTED (the
+   gradient of moe_dispatch).  A slot of weight 0 is left out, whatever its row holds.
+   rows: bf16 [T * k][d]; base: bf16 [T][d] or NULL (the shared expert's output, say);
+   y: bf16 [T][d], may be base.
+   moe_combine_grad: with dy = the gradient of y, bf16 [T][d],
+     d_rows[inv_perm[t * k + s]] = w[t][s] * dy[t]     bf16 [T * k][d], may be rows
+     d_w[t][s] = sum over columns of rows[inv_perm[t * k + s]] * dy[t]   fp32 [T][k]
+   (base's gradient is dy itself).  d_w is that of the weights as they are used, before
+   any renormalisation that made them. */
+#define MOE_UNWEIGHTED 1u
+int moe_dispatch(const uint16_t* x, int32_t T, int32_t k, int32_t d, const moe_routing* r,
+                 void* rows, float* rows_scale, void* stream);
+int moe_combine(const uint16_t* rows, int32_t T, int32_t k, int32_t d, const moe_routing* r,
+                uint32_t flags, const uint16_t* base, uint16_t* y, void* stream);
+int moe_combine_grad(const uint16_t* dy, const uint16_t* rows, int32_t T, int32_t k, int32_t d,
+                     const moe_routing* r, uint16_t* d_rows, float* d_w, void* stream);
+
+/* Penalties for repeated tokens, biases and a grammar's mask on B rows of logits, before
+   moe_sample.  Per row, with parameters from the per-row arrays or, where an array is
+   NULL, from the *_all value, and for every token v with logit l:
+     seen   v is among the row's first n_tokens tokens
+     n      how often v is among them from position n_prompt on (the answer)
+     l      seen: l / repetition where l > 0, else l * repetition
+     l      l - frequency * n - presence (n > 0 only)
+     l      l + the row's biases of v, in list order
+     out    l where bit v % 32 of the row's mask word v / 32 is 1, else -inf
+   in fp32, one rounding an operation.  repetition <= 0 or NaN: 1.  n_tokens is taken into
+   0 .. stride, n_prompt may be anything (<= 0: all is answer).  Ids outside 0 .. V - 1, in
+   tokens and in bias_ids, are passed over.  A row whose mask leaves nothing is -inf throughout
+   (moe_sample gives token 0 and prob 0 for it).  Bits behind V are not looked at.
+   logits and out: fp32 [B][V], 16-byte aligned, out may be logits; the other arrays are
+   4-byte aligned.  1 <= B <= MOE_MAX_SAMPLE_ROWS, 1 <= V <= MOE_MAX_VOCAB, 0 <= n_bias <=
+   MOE_MAX_BIASES.  One kernel, no workspace; equal calls give equal results. */
+#define MOE_MAX_BIASES 1024
+typedef struct {
+    const int32_t* tokens;      /* [B][stride] or NULL */
+    const int32_t* n_tokens;    /* [B] or NULL: all of them */
+    const int32_t* n_prompt;    /* [B] or NULL: 0 */
+    const float* repetition;    /* [B] or NULL */
+    const float* frequency;     /* [B] or NULL */
+    const float* presence;      /* [B] or NULL */
+    const int32_t* bias_ids;    /* [B][n_bias] or NULL */
+    const float* bias;          /* [B][n_bias], with bias_ids */
+    const uint32_t* mask;       /* [B][ceil(V/32)] or NULL: all allowed */
+    int32_t stride;
+    int32_t n_bias;
+    float repetition_all;
+    float frequency_all;
+    float presence_all;
+} moe_penalties;
+int moe_penalize(const float* logits, int32_t B, int32_t V, const moe_penalties* p, float* out,
+                 void* stream);
+
 /* Timing hook.  While `events` is non-NULL, every moe_route, moe_route_scored, moe_prefill,
-   moe_decode, moe_decode_tokens, moe_lm_argmax, moe_sample, moe_linear and moe_add_norm call made on this host thread records events[0] on its stream
+   moe_decode, moe_decode_tokens, moe_lm_argmax, moe_sample, moe_linear, moe_add_norm,
+   moe_linear_scaled, moe_experts_scaled, moe_dispatch, moe_combine, moe_combine_grad and
+   moe_penalize call made on this host thread records events[0] on its stream
    before its first kernel and events[i] right after its i-th kernel, for
    i < n (moe_route: router logits (with MOE_LOGITS_IN: the clearing of
    the histogram), top-k + histogram, scan + scatter + maps; moe_route_scored
@@ -417,8 +522,8 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
    partial sums + shared gate/up, logits + top-k + routed gate/up, down +
    combine; moe_lm_argmax: output head (with MOE_LOGITS_IN: the scan of the
    given logits), pick + embedding row).  moe_sample: its one kernel (V <= 8192), or
-   chunk maxima, histogram, gathering, pick; the one-kernel calls moe_linear and
-   moe_add_norm record events[0] and events[1].  The
+   chunk maxima, histogram, gathering, pick; the other calls have one kernel and
+   record events[0] and events[1].  The
    elapsed time between consecutive events is one kernel's duration.  events
    are hipEvent_t handles created and owned by the caller; pass NULL to stop. */
 void moe_trace_events(void* const* events, int32_t n);

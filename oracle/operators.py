@@ -112,3 +112,75 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     at = int(np.searchsorted(cum, np.uint64(draw), side="right"))
     token = int(kept[at])
     return token, math.exp((min(l[token], big) - m) / t) * 2.0 ** 43 / total
+
+
+BLOCK = 128  # columns (and weight rows) that share a scale of the 8-bit products
+
+
+def expand(scale, rows: int, n: int, k: int) -> np.ndarray:
+    """[n, k] in 64 bits: the scale of every element of a matrix with one per rows x 128."""
+    s = np.asarray(scale, np.float64)
+    return np.repeat(np.repeat(s, rows, 0)[:n], BLOCK, 1)[:, :k]
+
+
+def product(w, w_scale, x, x_scale):
+    """(y, the sum of the terms' magnitudes) of values w [N, K] and x [T, K] with their
+    scales, in 64 bits."""
+    wv = np.asarray(w, np.float64) * expand(w_scale, BLOCK, *w.shape)
+    xv = np.asarray(x, np.float64) * expand(x_scale, 1, *x.shape)
+    return xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+
+
+def group_scales(h) -> np.ndarray:
+    """max |h| / 448 of every 128 columns."""
+    n = h.shape[1]
+    return np.stack([np.abs(h[:, j:j + BLOCK]).max(1) for j in range(0, n, BLOCK)], 1) / 448.0
+
+
+def combine(rows, inv, w=None, base=None):
+    """y [T, d] of expert rows [T k, d] with inv [T, k]; slots of weight 0 are left out."""
+    T, k = inv.shape
+    y = np.zeros((T, rows.shape[1]))
+    for t in range(T):
+        for s in range(k):
+            if w is None or w[t, s] != 0:
+                y[t] += (1.0 if w is None else float(w[t, s])) * rows[inv[t, s]]
+    return y if base is None else y + base
+
+
+def combine_grad(dy, rows, inv, w):
+    """(d_rows, d_w) of combine."""
+    T, k = inv.shape
+    d_rows, d_w = np.empty_like(rows), np.empty((T, k))
+    for t in range(T):
+        for s in range(k):
+            d_rows[inv[t, s]] = float(w[t, s]) * dy[t]
+            d_w[t, s] = (rows[inv[t, s]] * dy[t]).sum()
+    return d_rows, d_w
+
+
+def penalize(logits, tokens=(), n_prompt=0, repetition=1.0, frequency=0.0, presence=0.0,
+             bias_ids=(), bias=(), allowed=None):
+    """(out, the sum of the terms' magnitudes) of one row of logits; tokens: those that count."""
+    y = np.asarray(logits, np.float32).astype(np.float64)
+    V = y.size
+    rep, freq, pres = (float(np.float32(v)) for v in (repetition, frequency, presence))
+    rep = rep if rep > 0 else 1.0
+    toks = [(i, int(v)) for i, v in enumerate(tokens) if 0 <= int(v) < V]
+    for v in {v for _, v in toks}:
+        y[v] = y[v] / rep if y[v] > 0 else y[v] * rep
+    size = np.abs(y)
+    count = {}
+    for i, v in toks:
+        if i >= n_prompt:
+            count[v] = count.get(v, 0) + 1
+    for v, n in count.items():
+        y[v] -= freq * n + pres
+        size[v] += abs(freq) * n + abs(pres)
+    for v, b in zip(bias_ids, bias):
+        if 0 <= int(v) < V:
+            y[int(v)] += float(np.float32(b))
+            size[int(v)] += abs(float(np.float32(b)))
+    if allowed is not None:
+        y[~np.asarray(allowed, bool)] = -np.inf
+    return y, size

@@ -22,7 +22,16 @@ The operators around the layer:
     r = route_scored(layer, y, RouterSpec(score="sigmoid", balance=b))
     y = decode_tokens(layer, y, ws, routing=r, routing_in=True)  # or prefill(layer, y, r)
     logits = linear(q, scale, bias, h)                         # fp32 [T, N], T <= 64
+    logits = penalize(logits, tokens=history, repetition=1.1, mask=grammar, out=logits)
     token, prob, _ = sample(logits, u, temperature=0.8, top_k=50, top_p=0.95)
+
+Experts in 8 bits (e4m3, a scale per token and 128 columns and per 128 x 128 weights):
+
+    w13, s13 = quantize_blocks(gate_up)        # [E, 2, I, d], once
+    rows, rows_s = dispatch(x, r, e4m3=True)   # expert-sorted rows
+    h, h_s = experts_e4m3(w13, s13, rows, rows_s, r, gated=True)
+    y = combine(experts_e4m3(w2, s2, h, h_s, r), r, base=shared)
+    logits = linear_e4m3(w, s, *add_norm(x, w, e4m3=True, group=128)[1:])
 """
 from __future__ import annotations
 
@@ -520,23 +529,32 @@ def linear(q: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor, x: torch.Te
     return y
 
 
+def _blocks(n: int, size: int = _abi.MOE_E4M3_BLOCK) -> int:
+    return -(-n // size)
+
+
 def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
              eps: float = 1e-6, plus_one: bool = False, residual_out: torch.Tensor | None = None,
              y: torch.Tensor | None = None, e4m3: bool = False, y8: torch.Tensor | None = None,
-             y8_scale: torch.Tensor | None = None, stream=None):
+             y8_scale: torch.Tensor | None = None, stream=None, group: int = 64):
     """Residual addition and RMS norm of the rows of x [T, d] (bf16): (y, y8, y8_scale).
 
     residual: bf16 or fp32 [T, d]; x + residual goes to residual_out (which may be
     residual itself; None: not stored).  plus_one: the weight used is weight + 1.
     y (bf16) is written when given, and by default when no 8-bit output is asked
     for; e4m3=True (or y8 and y8_scale given) asks for e4m3 codes [T, d] with one
-    fp32 scale per 64 columns [T, d / 64]."""
+    fp32 scale per `group` columns [T, ceil(d / group)], 64 or 128 (what linear_e4m3
+    takes)."""
     if stream is not None:
         return _on_stream(add_norm, locals())
     if x.dim() != 2:
         raise ValueError(f"x must be [T, d], not {tuple(x.shape)}")
     T, d = x.shape
     flags = _abi.MOE_NORM_PLUS_ONE if plus_one else 0
+    if group not in (64, 128):
+        raise ValueError(f"group must be 64 or 128, not {group}")
+    if group == 128:
+        flags |= _abi.MOE_NORM_GROUP_128
     _need(x, "x", torch.bfloat16, T * d)
     _need(weight, "weight", torch.bfloat16, d)
     if residual is not None:
@@ -551,9 +569,9 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
         if y8 is None:
             y8 = torch.empty_like(x, dtype=torch.float8_e4m3fn)
         if y8_scale is None:
-            y8_scale = x.new_empty((T, d // 64), dtype=torch.float32)
+            y8_scale = x.new_empty((T, _blocks(d, group)), dtype=torch.float32)
         _need(y8, "y8", torch.float8_e4m3fn, T * d)
-        _need(y8_scale, "y8_scale", torch.float32, T * (d // 64))
+        _need(y8_scale, "y8_scale", torch.float32, T * _blocks(d, group))
     elif y is None:
         y = torch.empty_like(x)
     if y is not None:
@@ -564,6 +582,255 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
                                    eps, flags, _ptr(y), _ptr(y8), _ptr(y8_scale), s),
            "moe_add_norm")
     return y, y8, y8_scale
+
+
+def quantize_blocks(w: torch.Tensor):
+    """e4m3 codes of matrices w [..., N, K] (any floating type) and fp32 scales
+    [..., ceil(N / 128), ceil(K / 128)], max |w| / 448 of each 128 x 128 block: what
+    linear_e4m3 and experts_e4m3 take.  Done once, when weights are loaded (elementary
+    torch operations)."""
+    B = _abi.MOE_E4M3_BLOCK
+    if w.dim() < 2 or not w.is_floating_point():
+        raise ValueError(f"w must be floating [..., N, K], not {w.dtype} {tuple(w.shape)}")
+    N, K = w.shape[-2:]
+    nb, kb = _blocks(N), _blocks(K)
+    g = torch.nn.functional.pad(w.float(), (0, kb * B - K, 0, nb * B - N))
+    g = g.reshape(*w.shape[:-2], nb, B, kb, B)
+    scale = g.abs().amax((-3, -1)) / 448.0
+    s = scale[..., :, None, :, None]
+    codes = torch.where(s > 0, g / s, 0.0).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    codes = codes.reshape(*w.shape[:-2], nb * B, kb * B)[..., :N, :K]
+    return codes.contiguous(), scale.contiguous()
+
+
+def _product(where, w, w_scale, x, x_scale, lead, rows, out_dtype, gated, y, y_scale):
+    """Checks and outputs shared by the 8-bit products: the C call's matrix, N (both parts
+    of a gated matrix), K, flags, y, y_scale."""
+    lead = lead + (2,) if gated else lead
+    if x.dim() != 2 or w.dim() != len(lead) + 2 or tuple(w.shape[:-2]) != lead:
+        raise ValueError(f"{where}: x must be [rows, K] and w {[*lead, 'N', 'K']}, not "
+                         f"{tuple(x.shape)}, {tuple(w.shape)}")
+    N, K = w.shape[-2:]
+    if x.shape[1] != K:
+        raise ValueError(f"{where}: w has {K} columns, x has {x.shape[1]}")
+    if gated:
+        out_dtype = torch.float8_e4m3fn
+    elif out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, not {out_dtype}")
+    mats = 1
+    for n in lead:
+        mats *= n
+    _need(x, "x", torch.float8_e4m3fn, rows * K)
+    _need(x_scale, "x_scale", torch.float32, rows * _blocks(K))
+    _need(w, "w", torch.float8_e4m3fn, mats * N * K)
+    _need(w_scale, "w_scale", torch.float32, mats * _blocks(N) * _blocks(K))
+    if y is None:
+        y = x.new_empty((rows, N), dtype=out_dtype)
+    _need(y, "y", out_dtype, rows * N)
+    if gated:
+        if y_scale is None:
+            y_scale = x_scale.new_empty((rows, _blocks(N)))
+        _need(y_scale, "y_scale", torch.float32, rows * _blocks(N))
+    elif y_scale is not None:
+        raise ValueError("y_scale is of gated products")
+    flags = (_abi.MOE_GATED if gated else
+             _abi.MOE_OUT_BF16 if out_dtype == torch.bfloat16 else 0)
+    return _abi.E4m3Mat(w.data_ptr(), w_scale.data_ptr()), N * (2 if gated else 1), K, flags, y, y_scale
+
+
+def linear_e4m3(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor,
+                out_dtype: torch.dtype = torch.bfloat16, gated: bool = False,
+                y: torch.Tensor | None = None, y_scale: torch.Tensor | None = None, stream=None):
+    """y [T, N] = x times the transposed matrix w, both e4m3: x [T, K] with x_scale
+    [T, ceil(K / 128)], w [N, K] with w_scale [ceil(N / 128), ceil(K / 128)]; out_dtype
+    bf16 or fp32.  gated: w is [2, I, K] (gate, up) with w_scale [2, ceil(I / 128), ...],
+    and (y e4m3 [T, I], y_scale [T, ceil(I / 128)]) of silu(gate) * up is returned."""
+    if stream is not None:
+        return _on_stream(linear_e4m3, locals())
+    T = x.shape[0]
+    m, N, K, flags, y, y_scale = _product("linear_e4m3", w, w_scale, x, x_scale, (), T, out_dtype,
+                                          gated, y, y_scale)
+    s = _launch_on("linear_e4m3", w=w, w_scale=w_scale, x=x, x_scale=x_scale, y=y, y_scale=y_scale)
+    _check(_abi.lib().moe_linear_scaled(C.addressof(m), N, K, _ptr(x), _ptr(x_scale), T, flags,
+                                      _ptr(y), _ptr(y_scale), s), "moe_linear_scaled")
+    return (y, y_scale) if gated else y
+
+
+def _routed(where: str, routing: DeviceRouting, rows: int | None = None, T: int | None = None) -> int:
+    """T of a call on expert rows (T * k of them) or tokens, which the routing has to hold."""
+    if rows is not None:
+        if rows % routing.k or rows == 0:
+            raise ValueError(f"{where}: {rows} rows, the routing has {routing.k} for each token")
+        if T is not None and T * routing.k != rows:
+            raise ValueError(f"{where}: {rows} rows for {T} tokens of {routing.k} each")
+        T = rows // routing.k
+    if T > routing.T:
+        raise ValueError(f"{where}: the routing is for T={routing.T}, the call for T={T}")
+    return T
+
+
+def experts_e4m3(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor,
+                 routing: DeviceRouting, out_dtype: torch.dtype = torch.bfloat16,
+                 gated: bool = False, y: torch.Tensor | None = None,
+                 y_scale: torch.Tensor | None = None, stream=None):
+    """linear_e4m3 over the expert-sorted rows of a routing (dispatch's), with a matrix per
+    expert: x [T * k, K], w [E, N, K] (gated: [E, 2, I, K]), the scales likewise."""
+    if stream is not None:
+        return _on_stream(experts_e4m3, locals())
+    rows = x.shape[0]
+    T = _routed("experts_e4m3", routing, rows)
+    m, N, K, flags, y, y_scale = _product("experts_e4m3", w, w_scale, x, x_scale, (routing.E,),
+                                          rows, out_dtype, gated, y, y_scale)
+    s = _launch_on("experts_e4m3", w=w, w_scale=w_scale, x=x, x_scale=x_scale, y=y, y_scale=y_scale,
+                   offsets=routing.offsets)
+    _check(_abi.lib().moe_experts_scaled(C.addressof(m), routing.E, N, K, _ptr(x), _ptr(x_scale), T,
+                                       routing.k, C.addressof(routing.struct), flags, _ptr(y),
+                                       _ptr(y_scale), s), "moe_experts_scaled")
+    return (y, y_scale) if gated else y
+
+
+def dispatch(x: torch.Tensor, routing: DeviceRouting, e4m3: bool = False,
+             rows: torch.Tensor | None = None, rows_scale: torch.Tensor | None = None, stream=None):
+    """Token rows x [T, d] (bf16) in expert order, k of each: (rows [T * k, d], None), or
+    with e4m3 (or rows_scale given) codes and a scale per 128 columns [T * k, ceil(d / 128)].
+    Its gradient is combine(d_rows, routing, weighted=False)."""
+    if stream is not None:
+        return _on_stream(dispatch, locals())
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, d], not {tuple(x.shape)}")
+    T, d = x.shape
+    _routed("dispatch", routing, T=T)
+    n = T * routing.k
+    e4m3 = e4m3 or rows_scale is not None
+    dt = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    if rows is None:
+        rows = x.new_empty((n, d), dtype=dt)
+    if e4m3 and rows_scale is None:
+        rows_scale = x.new_empty((n, _blocks(d)), dtype=torch.float32)
+    _need(x, "x", torch.bfloat16, T * d)
+    _need(rows, "rows", dt, n * d)
+    if e4m3:
+        _need(rows_scale, "rows_scale", torch.float32, n * _blocks(d))
+    s = _launch_on("dispatch", x=x, rows=rows, rows_scale=rows_scale, inv_perm=routing.inv_perm)
+    _check(_abi.lib().moe_dispatch(_ptr(x), T, routing.k, d, C.addressof(routing.struct),
+                                   _ptr(rows), _ptr(rows_scale), s), "moe_dispatch")
+    return rows, rows_scale
+
+
+def combine(rows: torch.Tensor, routing: DeviceRouting, weighted: bool = True,
+            base: torch.Tensor | None = None, y: torch.Tensor | None = None,
+            stream=None) -> torch.Tensor:
+    """y [T, d] (bf16): the sum over every token's slots of its expert rows [T * k, d] (bf16)
+    times routing.topk_w (weighted=False: unweighted), plus base [T, d] (bf16)."""
+    if stream is not None:
+        return _on_stream(combine, locals())
+    if rows.dim() != 2:
+        raise ValueError(f"rows must be [T * k, d], not {tuple(rows.shape)}")
+    n, d = rows.shape
+    T = _routed("combine", routing, n)
+    if y is None:
+        y = torch.empty((T, d), dtype=torch.bfloat16, device=rows.device)
+    _need(rows, "rows", torch.bfloat16, n * d)
+    _need(y, "y", torch.bfloat16, T * d)
+    if base is not None:
+        _need(base, "base", torch.bfloat16, T * d)
+    s = _launch_on("combine", rows=rows, base=base, y=y, inv_perm=routing.inv_perm)
+    _check(_abi.lib().moe_combine(_ptr(rows), T, routing.k, d, C.addressof(routing.struct),
+                                  0 if weighted else _abi.MOE_UNWEIGHTED, _ptr(base), _ptr(y), s),
+           "moe_combine")
+    return y
+
+
+def combine_grad(dy: torch.Tensor, rows: torch.Tensor, routing: DeviceRouting,
+                 d_rows: torch.Tensor | None = None, d_w: torch.Tensor | None = None, stream=None):
+    """combine's gradients from dy [T, d] (bf16): (d_rows bf16 [T * k, d], d_w fp32 [T, k]).
+    d_rows may be rows; base's gradient is dy."""
+    if stream is not None:
+        return _on_stream(combine_grad, locals())
+    if dy.dim() != 2 or rows.dim() != 2 or dy.shape[1] != rows.shape[1]:
+        raise ValueError(f"dy must be [T, d] and rows [T * k, d], not {tuple(dy.shape)}, "
+                         f"{tuple(rows.shape)}")
+    T, d = dy.shape
+    n, k = rows.shape[0], routing.k
+    _routed("combine_grad", routing, n, T)
+    if d_rows is None:
+        d_rows = torch.empty_like(rows)
+    if d_w is None:
+        d_w = dy.new_empty((T, k), dtype=torch.float32)
+    _need(dy, "dy", torch.bfloat16, T * d)
+    _need(rows, "rows", torch.bfloat16, n * d)
+    _need(d_rows, "d_rows", torch.bfloat16, n * d)
+    _need(d_w, "d_w", torch.float32, n)
+    s = _launch_on("combine_grad", dy=dy, rows=rows, d_rows=d_rows, d_w=d_w,
+                   inv_perm=routing.inv_perm)
+    _check(_abi.lib().moe_combine_grad(_ptr(dy), _ptr(rows), T, k, d, C.addressof(routing.struct),
+                                       _ptr(d_rows), _ptr(d_w), s), "moe_combine_grad")
+    return d_rows, d_w
+
+
+def penalize(logits: torch.Tensor, tokens: torch.Tensor | None = None,
+             n_tokens: torch.Tensor | None = None, n_prompt: torch.Tensor | None = None,
+             repetition=1.0, frequency=0.0, presence=0.0, bias_ids: torch.Tensor | None = None,
+             bias: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Penalties, biases and a mask on rows of logits [B, V] (fp32), into out (which may be
+    logits).  tokens: int32 [B, L], of which the first n_tokens [B] count (None: all) and
+    those from n_prompt [B] on (None: all) are the answer; repetition (over all of them),
+    frequency and presence (over the answer) are numbers for all rows or fp32 tensors [B];
+    bias (fp32) is added at bias_ids (int32), both [B, n]; mask: int32 [B, ceil(V / 32)], bit
+    v % 32 of word v / 32 is 1 where token v is allowed.  Ids outside 0 .. V - 1 (padding)
+    are passed over."""
+    if stream is not None:
+        return _on_stream(penalize, locals())
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [B, V], not {tuple(logits.shape)}")
+    B, V = logits.shape
+    _need(logits, "logits", torch.float32, B * V)
+    p = _abi.Penalties()
+    given = {}
+    if tokens is not None:
+        if tokens.dim() != 2 or tokens.shape[0] != B:
+            raise ValueError(f"tokens must be [{B}, L], not {tuple(tokens.shape)}")
+        _need(tokens, "tokens", torch.int32, 0)
+        p.stride = tokens.shape[1]
+        # (without a column there is nothing to point at)
+        given["tokens"] = tokens if p.stride else None
+    for name, t in (("n_tokens", n_tokens), ("n_prompt", n_prompt)):
+        if t is not None:
+            if tokens is None:
+                raise ValueError(f"{name} needs tokens")
+            _need(t, name, torch.int32, B)
+            given[name] = t if p.stride else None
+    for name, v in (("repetition", repetition), ("frequency", frequency), ("presence", presence)):
+        if isinstance(v, torch.Tensor):
+            _need(v, name, torch.float32, B)
+            given[name] = v
+        else:
+            setattr(p, name + "_all", v)
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias come together")
+    if bias is not None:
+        if bias_ids.dim() != 2 or bias_ids.shape[0] != B or bias.shape != bias_ids.shape:
+            raise ValueError(f"bias_ids and bias must be [{B}, n], not {tuple(bias_ids.shape)}, "
+                             f"{tuple(bias.shape)}")
+        _need(bias_ids, "bias_ids", torch.int32, 0)
+        _need(bias, "bias", torch.float32, 0)
+        p.n_bias = bias.shape[1]
+        if p.n_bias:
+            given["bias_ids"], given["bias"] = bias_ids, bias
+    if mask is not None:
+        if mask.dim() != 2 or tuple(mask.shape) != (B, -(-V // 32)):
+            raise ValueError(f"mask must be [{B}, {-(-V // 32)}], not {tuple(mask.shape)}")
+        _need(mask, "mask", torch.int32, 0)
+        given["mask"] = mask
+    if out is None:
+        out = torch.empty_like(logits)
+    _need(out, "out", torch.float32, B * V)
+    s = _launch_on("penalize", logits=logits, out=out, **given)
+    for name, t in given.items():
+        setattr(p, name, _ptr(t))
+    _check(_abi.lib().moe_penalize(_ptr(logits), B, V, C.addressof(p), _ptr(out), s), "moe_penalize")
+    return out
 
 
 def library_path() -> str:

@@ -9,11 +9,14 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libq4moe.so
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, -1, -2, -3, -4
 MOE_LOGITS_IN = 1
 MOE_ITEM_ROWS_64, MOE_ITEM_ROWS_32, MOE_ITEM_ROWS_16 = 2, 4, 8
-MOE_NORM_PLUS_ONE, MOE_NORM_RESIDUAL_FLOAT = 1, 2
+MOE_NORM_PLUS_ONE, MOE_NORM_RESIDUAL_FLOAT, MOE_NORM_GROUP_128 = 1, 2, 8
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_ROUTING_IN = 32
 MOE_MAX_GROUPS = 64
-MOE_OUT_BF16 = 1
+MOE_OUT_BF16, MOE_GATED = 1, 2
+MOE_UNWEIGHTED = 1
+MOE_E4M3_BLOCK = 128
+MOE_MAX_BIASES = 1024
 MOE_MAX_LINEAR_TOKENS = 64
 MOE_MAX_SAMPLE_ROWS = 1024
 MOE_BLOCK_ROWS = 32
@@ -31,7 +34,8 @@ EXPORTS = ("moe_block_map_capacity", "moe_workspace_bytes", "moe_route", "moe_pr
            "moe_decode", "moe_decode_tokens", "moe_dequant", "moe_strerror", "moe_last_error",
            "moe_lm_workspace_bytes", "moe_lm_argmax", "moe_decode_tokens_static",
            "moe_add_norm", "moe_route_scored", "moe_linear",
-           "moe_sample_workspace_bytes", "moe_sample")
+           "moe_sample_workspace_bytes", "moe_sample", "moe_linear_scaled", "moe_experts_scaled",
+           "moe_dispatch", "moe_combine", "moe_combine_grad", "moe_penalize")
 
 
 class Q4Mat(C.Structure):
@@ -59,6 +63,17 @@ class Sampling(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("u", "temperature", "top_k", "top_p", "min_p")] + [
         ("temperature_all", C.c_float), ("top_k_all", C.c_int32), ("top_p_all", C.c_float),
         ("min_p_all", C.c_float)]
+
+
+class E4m3Mat(C.Structure):
+    _fields_ = [("w", C.c_void_p), ("scale", C.c_void_p)]
+
+
+class Penalties(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("tokens", "n_tokens", "n_prompt", "repetition",
+                                          "frequency", "presence", "bias_ids", "bias", "mask")] + [
+        ("stride", C.c_int32), ("n_bias", C.c_int32), ("repetition_all", C.c_float),
+        ("frequency_all", C.c_float), ("presence_all", C.c_float)]
 
 
 class Routing(C.Structure):
@@ -106,9 +121,18 @@ def lib():
         L.moe_sample_workspace_bytes.restype = C.c_size_t
         L.moe_sample.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, C.c_size_t, vp]
         L.moe_add_norm.argtypes = [vp, i32, i32, vp, vp, vp, C.c_float, C.c_uint32, vp, vp, vp, vp]
+        L.moe_linear_scaled.argtypes = [vp, i32, i32, vp, vp, i32, C.c_uint32, vp, vp, vp]
+        L.moe_experts_scaled.argtypes = [vp, i32, i32, i32, vp, vp, i32, i32, vp, C.c_uint32, vp, vp,
+                                       vp]
+        L.moe_dispatch.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp]
+        L.moe_combine.argtypes = [vp, i32, i32, i32, vp, C.c_uint32, vp, vp, vp]
+        L.moe_combine_grad.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp]
+        L.moe_penalize.argtypes = [vp, i32, i32, vp, vp, vp]
         for f in ("moe_route", "moe_prefill", "moe_prefill_ex", "moe_decode", "moe_decode_tokens", "moe_dequant",
                   "moe_lm_argmax", "moe_decode_tokens_static", "moe_add_norm",
-                  "moe_route_scored", "moe_linear", "moe_sample"):
+                  "moe_route_scored", "moe_linear", "moe_sample", "moe_linear_scaled",
+                  "moe_experts_scaled", "moe_dispatch", "moe_combine", "moe_combine_grad",
+                  "moe_penalize"):
             getattr(L, f).restype = C.c_int
         L.moe_trace_events.argtypes = [vp, i32]
         L.moe_trace_events.restype = None

@@ -642,7 +642,7 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
     if (d % MOE_GROUP || d > MOE_MAX_D)
         return fail(MOE_EUNSUPPORTED, "d=%d must be a multiple of %d and <= %d", d, MOE_GROUP,
                     MOE_MAX_D);
-    if (flags & ~(MOE_NORM_PLUS_ONE | MOE_NORM_RESIDUAL_FLOAT))
+    if (flags & ~(MOE_NORM_PLUS_ONE | MOE_NORM_RESIDUAL_FLOAT | MOE_NORM_GROUP_128))
         return fail(MOE_EINVAL, "unknown flags 0x%x", flags);
     if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(MOE_EINVAL, "eps must be finite and >= 0");
     if ((rc = check_ptr(x, "x")) || (rc = check_ptr(weight, "weight")) ||
@@ -669,10 +669,224 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
     a.T = T;
     a.d = d;
     a.eps = eps;
+    a.group = (flags & MOE_NORM_GROUP_128) ? 128 : 64;
     a.w_add = (flags & MOE_NORM_PLUS_ONE) ? 1.0f : 0.0f;
     a.res_f32 = (flags & MOE_NORM_RESIDUAL_FLOAT) != 0;
     trace_begin((hipStream_t)stream);
     return hip_status(q4moe::launch_add_norm(a, (hipStream_t)stream), "add norm");
+}
+
+}  // extern "C"
+
+namespace {
+
+// Validation shared by the 8-bit products.
+int check_product(const moe_e4m3mat* m, int32_t N, int32_t K, const uint8_t* x, const float* x_scale,
+                  uint32_t flags, const void* y, const float* y_scale) {
+    int rc;
+    if (!m) return fail(MOE_EINVAL, "matrix is NULL");
+    if (N <= 0 || K <= 0) return fail(MOE_EINVAL, "N=%d and K=%d must be positive", N, K);
+    if (K % MOE_GROUP || K > MOE_MAX_D)
+        return fail(MOE_EUNSUPPORTED, "K=%d must be a multiple of %d and <= %d", K, MOE_GROUP,
+                    MOE_MAX_D);
+    if (N > MOE_MAX_VOCAB) return fail(MOE_EUNSUPPORTED, "N=%d > %d", N, MOE_MAX_VOCAB);
+    if (flags & ~(MOE_OUT_BF16 | MOE_GATED)) return fail(MOE_EINVAL, "unknown flags 0x%x", flags);
+    const bool gated = flags & MOE_GATED;
+    if (gated && (flags & MOE_OUT_BF16))
+        return fail(MOE_EINVAL, "MOE_GATED and MOE_OUT_BF16 exclude each other");
+    if (gated && N % (2 * MOE_GROUP))
+        return fail(MOE_EUNSUPPORTED, "N=%d: a gated product needs a multiple of %d", N, 2 * MOE_GROUP);
+    if ((rc = check_ptr(m->w, "m.w")) || (rc = check_ptr(m->scale, "m.scale")) || (rc = check_ptr(x, "x")) ||
+        (rc = check_ptr(x_scale, "x_scale")) || (rc = check_ptr(y, "y")) ||
+        (rc = check_ptr(y_scale, "y_scale", !gated)))
+        return rc;
+    if (!gated && y_scale) return fail(MOE_EINVAL, "y_scale without MOE_GATED");
+    if (y == (const void*)x || y == (const void*)x_scale || (gated && (y == (const void*)y_scale || y_scale == x_scale)))
+        return fail(MOE_EINVAL, "an output shares a buffer with an input or another output");
+    return MOE_OK;
+}
+
+q4moe::ProductArgs product_args(const moe_e4m3mat* m, int32_t N, int32_t K, const uint8_t* x,
+                                const float* x_scale, int32_t rows, uint32_t flags, void* y,
+                                float* y_scale) {
+    q4moe::ProductArgs a{};
+    a.w = m->w;
+    a.w_scale = m->scale;
+    a.x = x;
+    a.x_scale = x_scale;
+    a.y = y;
+    a.y_scale = y_scale;
+    a.rows = rows;
+    a.gated = (flags & MOE_GATED) != 0;
+    a.N = a.gated ? N / 2 : N;
+    a.K = K;
+    a.out_bf16 = (flags & MOE_OUT_BF16) != 0;
+    a.E = 1;
+    return a;
+}
+
+// Sizes and indices shared by the calls that move rows between token and expert order.
+int check_sort(int32_t T, int32_t k, int32_t d, const moe_routing* r) {
+    int rc;
+    if ((rc = check_tokens(T))) return rc;
+    if (k <= 0 || d <= 0) return fail(MOE_EINVAL, "k=%d and d=%d must be positive", k, d);
+    if (k > MOE_MAX_TOPK) return fail(MOE_EUNSUPPORTED, "k=%d > %d", k, MOE_MAX_TOPK);
+    if (d % MOE_GROUP || d > MOE_MAX_D)
+        return fail(MOE_EUNSUPPORTED, "d=%d must be a multiple of %d and <= %d", d, MOE_GROUP,
+                    MOE_MAX_D);
+    if (!r) return fail(MOE_EINVAL, "routing is NULL");
+    return check_ptr(r->inv_perm, "routing.inv_perm");
+}
+
+q4moe::SortArgs sort_args(int32_t T, int32_t k, int32_t d, const moe_routing* r) {
+    q4moe::SortArgs a{};
+    a.inv_perm = r->inv_perm;
+    a.T = T;
+    a.k = k;
+    a.d = d;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_linear_scaled(const moe_e4m3mat* m, int32_t N, int32_t K, const uint8_t* x, const float* x_scale,
+                    int32_t T, uint32_t flags, void* y, float* y_scale, void* stream) {
+    int rc;
+    if ((rc = check_product(m, N, K, x, x_scale, flags, y, y_scale)) || (rc = check_tokens(T))) return rc;
+    const q4moe::ProductArgs a = product_args(m, N, K, x, x_scale, T, flags, y, y_scale);
+    trace_begin((hipStream_t)stream);
+    return hip_status(q4moe::launch_product(a, (hipStream_t)stream), "linear e4m3");
+}
+
+int moe_experts_scaled(const moe_e4m3mat* m, int32_t E, int32_t N, int32_t K, const uint8_t* x,
+                     const float* x_scale, int32_t T, int32_t k, const moe_routing* r, uint32_t flags,
+                     void* y, float* y_scale, void* stream) {
+    int rc;
+    if ((rc = check_product(m, N, K, x, x_scale, flags, y, y_scale)) || (rc = check_tokens(T))) return rc;
+    if (E <= 0 || k <= 0) return fail(MOE_EINVAL, "E=%d and k=%d must be positive", E, k);
+    if (E > MOE_MAX_EXPERTS) return fail(MOE_EUNSUPPORTED, "E=%d > %d", E, MOE_MAX_EXPERTS);
+    if (k > MOE_MAX_TOPK || k > E)
+        return fail(MOE_EUNSUPPORTED, "k=%d must be <= min(%d, E=%d)", k, MOE_MAX_TOPK, E);
+    if (!r) return fail(MOE_EINVAL, "routing is NULL");
+    if ((rc = check_ptr(r->offsets, "routing.offsets")) ||
+        (rc = check_ptr(r->block_map, "routing.block_map")) ||
+        (rc = check_ptr(r->n_blocks, "routing.n_blocks")) ||
+        (rc = check_ptr(r->tile_map, "routing.tile_map")) ||
+        (rc = check_ptr(r->n_tiles, "routing.n_tiles")))
+        return rc;
+    q4moe::ProductArgs a = product_args(m, N, K, x, x_scale, T * k, flags, y, y_scale);
+    a.E = E;
+    a.offsets = r->offsets;
+    a.map = r->block_map;
+    a.n_map = r->n_blocks;
+    a.map_bound = moe_block_map_capacity(T, k, E, MOE_BLOCK_ROWS);
+    a.map128 = r->tile_map;
+    a.n_map128 = r->n_tiles;
+    a.map128_bound = moe_block_map_capacity(T, k, E, MOE_TILE_ROWS);
+    trace_begin((hipStream_t)stream);
+    return hip_status(q4moe::launch_product(a, (hipStream_t)stream), "experts e4m3");
+}
+
+int moe_dispatch(const uint16_t* x, int32_t T, int32_t k, int32_t d, const moe_routing* r, void* rows,
+                 float* rows_scale, void* stream) {
+    int rc;
+    if ((rc = check_sort(T, k, d, r)) || (rc = check_ptr(x, "x")) || (rc = check_ptr(rows, "rows")) ||
+        (rc = check_ptr(rows_scale, "rows_scale", true)))
+        return rc;
+    if (rows == (const void*)x || rows == (void*)rows_scale || (const void*)rows_scale == (const void*)x)
+        return fail(MOE_EINVAL, "an output shares a buffer with x or another output");
+    q4moe::SortArgs a = sort_args(T, k, d, r);
+    a.x = x;
+    a.rows_out = rows;
+    a.scale_out = rows_scale;
+    trace_begin((hipStream_t)stream);
+    return hip_status(q4moe::launch_dispatch(a, (hipStream_t)stream), "dispatch");
+}
+
+int moe_combine(const uint16_t* rows, int32_t T, int32_t k, int32_t d, const moe_routing* r,
+                uint32_t flags, const uint16_t* base, uint16_t* y, void* stream) {
+    int rc;
+    if ((rc = check_sort(T, k, d, r))) return rc;
+    if (flags & ~MOE_UNWEIGHTED) return fail(MOE_EINVAL, "unknown flags 0x%x", flags);
+    const bool weighted = !(flags & MOE_UNWEIGHTED);
+    if ((rc = check_ptr(rows, "rows")) || (rc = check_ptr(r->topk_w, "routing.topk_w", !weighted)) ||
+        (rc = check_ptr(base, "base", true)) || (rc = check_ptr(y, "y")))
+        return rc;
+    if (y == rows) return fail(MOE_EINVAL, "y shares a buffer with rows");
+    q4moe::SortArgs a = sort_args(T, k, d, r);
+    a.rows = rows;
+    a.w = weighted ? r->topk_w : nullptr;
+    a.base = base;
+    a.y = y;
+    trace_begin((hipStream_t)stream);
+    return hip_status(q4moe::launch_combine(a, (hipStream_t)stream), "combine");
+}
+
+int moe_combine_grad(const uint16_t* dy, const uint16_t* rows, int32_t T, int32_t k, int32_t d,
+                     const moe_routing* r, uint16_t* d_rows, float* d_w, void* stream) {
+    int rc;
+    if ((rc = check_sort(T, k, d, r)) || (rc = check_ptr(dy, "dy")) ||
+        (rc = check_ptr(r->topk_w, "routing.topk_w")) || (rc = check_ptr(d_rows, "d_rows")) ||
+        (rc = check_ptr(rows, "rows")) || (rc = check_ptr(d_w, "d_w")))
+        return rc;
+    if (d_rows == dy || (const void*)d_w == dy || (const void*)d_w == rows ||
+        (const void*)d_w == (const void*)d_rows)
+        return fail(MOE_EINVAL, "an output shares a buffer with an input or another output");
+    q4moe::SortArgs a = sort_args(T, k, d, r);
+    a.dy = dy;
+    a.rows = rows;
+    a.w = r->topk_w;
+    a.rows_out = d_rows;
+    a.d_w = d_w;
+    trace_begin((hipStream_t)stream);
+    return hip_status(q4moe::launch_combine_grad(a, (hipStream_t)stream), "combine grad");
+}
+
+int moe_penalize(const float* logits, int32_t B, int32_t V, const moe_penalties* p, float* out,
+                 void* stream) {
+    int rc;
+    if (!p) return fail(MOE_EINVAL, "penalties is NULL");
+    if ((rc = check_sample_sizes(V, B)) || (rc = check_ptr(logits, "logits")) || (rc = check_ptr(out, "out")) ||
+        (rc = check_row_array(p->tokens, "tokens", true)) ||
+        (rc = check_row_array(p->n_tokens, "n_tokens", true)) ||
+        (rc = check_row_array(p->n_prompt, "n_prompt", true)) ||
+        (rc = check_row_array(p->repetition, "repetition", true)) ||
+        (rc = check_row_array(p->frequency, "frequency", true)) ||
+        (rc = check_row_array(p->presence, "presence", true)) ||
+        (rc = check_row_array(p->bias_ids, "bias_ids", true)) ||
+        (rc = check_row_array(p->bias, "bias", true)) || (rc = check_row_array(p->mask, "mask", true)))
+        return rc;
+    if (p->tokens && p->stride < 0) return fail(MOE_EINVAL, "stride=%d", p->stride);
+    if (!p->tokens && (p->n_tokens || p->n_prompt))
+        return fail(MOE_EINVAL, "n_tokens and n_prompt need tokens");
+    if (!p->bias_ids != !p->bias) return fail(MOE_EINVAL, "bias_ids and bias come together");
+    if (p->bias_ids && p->n_bias < 0) return fail(MOE_EINVAL, "n_bias=%d", p->n_bias);
+    if (p->bias_ids && p->n_bias > MOE_MAX_BIASES)
+        return fail(MOE_EUNSUPPORTED, "n_bias=%d > %d", p->n_bias, MOE_MAX_BIASES);
+    q4moe::PenalizeArgs a{};
+    a.logits = logits;
+    a.out = out;
+    a.B = B;
+    a.V = V;
+    a.tokens = p->tokens;
+    a.n_tokens = p->n_tokens;
+    a.n_prompt = p->n_prompt;
+    a.stride = p->stride;
+    a.repetition = p->repetition;
+    a.frequency = p->frequency;
+    a.presence = p->presence;
+    a.repetition_all = p->repetition_all;
+    a.frequency_all = p->frequency_all;
+    a.presence_all = p->presence_all;
+    a.bias_ids = p->bias_ids;
+    a.bias = p->bias;
+    a.n_bias = p->bias_ids ? p->n_bias : 0;
+    a.mask = p->mask;
+    a.mask_words = (V + 31) / 32;
+    trace_begin((hipStream_t)stream);
+    return hip_status(q4moe::launch_penalize(a, (hipStream_t)stream), "penalize");
 }
 
 const char* moe_strerror(int code) {

@@ -3,7 +3,7 @@
 //   r = x + residual                 (fp32 sum, rounded once to the residual's type, stored)
 //   y = r / sqrt(mean(r^2) + eps) * w
 //
-// in fp32 from the stored r, rounded once to bf16; or, per 64 columns, to e4m3
+// in fp32 from the stored r, rounded once to bf16; or, per 64 or 128 columns, to e4m3
 // codes of y / scale with the fp32 scale max|y| / 448 (448 = the largest e4m3
 // value), from the unrounded y.  The quotient is by the scale that is stored: a
 // factor 448 / max|y| rounds otherwise (one code in 10^5 lands on the other side of a
@@ -12,6 +12,7 @@
 // Every input is read once and every output written once: a row stays in the
 // registers between its sum of squares and its scaling.  The kernel is bound by
 // HBM for long chunks and by the launch for a few tokens.
+#include "e4m3.h"
 #include "ops.h"
 
 namespace q4moe {
@@ -19,8 +20,8 @@ namespace {
 
 // One row per W waves; a lane holds NV pieces of 8 columns: piece j of thread
 // t covers columns 8 (t + 64 W j) .. + 7, so a 64-column group is eight
-// neighbouring lanes.
-template <int W, int NV, bool RES, bool F32>
+// neighbouring lanes and one of 128 sixteen.
+template <int W, int NV, bool RES, bool F32, int G>
 __global__ __launch_bounds__(W * 64) void add_norm_kernel(const NormArgs a) {
     __shared__ float s_sum[W];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -102,54 +103,38 @@ __global__ __launch_bounds__(W * 64) void add_norm_kernel(const NormArgs a) {
             if (live) *(u32x4*)(a.y + row + c) = yv;
         }
         if (a.y8) {
-            // largest magnitude of the 64-column group, by bit pattern (a NaN is the largest)
+            // largest magnitude of the group, by bit pattern (a NaN is the largest)
             uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+            for (int i = 0; i < 8; ++i) m = max_magnitude(m, y[i]);
+            if (!live) m = 0;  // a last group of 64 of 128 columns
             m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));
             m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));
             m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, false));
-            const float amax = __uint_as_float(m);
-            float scale, z[8];
-            if (amax > 0x1p-70f && amax < 0x1p80f) {
-                // Both quotients as products by a reciprocal and their exact remainder: the
-                // scale is amax / 448 correctly rounded (checked for every mantissa), and
-                // y / scale unless it lies within 2^-22 of a step from the middle of two fp32
-                // numbers.  (2048 x 2048 with eight IEEE divisions: 8.6 us instead of 7.7.)
-                scale = amax * (1.0f / 448.0f);
-                scale = __builtin_fmaf(__builtin_fmaf(-scale, 448.0f, amax), 1.0f / 448.0f, scale);
-                const float inv_s = __builtin_amdgcn_rcpf(scale);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float t = y[i] * inv_s;
-                    z[i] = __builtin_fmaf(__builtin_fmaf(-t, scale, y[i]), inv_s, t);
-                }
-            } else {  // where a remainder could leave fp32's range
-                scale = amax / 448.0f;  // (0 for the smallest subnormals too)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) z[i] = scale == 0.0f ? 0.0f : y[i] / scale;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = z[i] > 448.0f ? 448.0f : z[i] < -448.0f ? -448.0f : z[i];  // (a NaN stays one)
+            if (G == 128) m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xF, 0xF, false));
+            // (2048 x 2048 with eight IEEE divisions for the codes: 8.6 us instead of 7.7)
+            float scale;
             uint32_t w8[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int w = __builtin_amdgcn_cvt_pk_fp8_f32(z[4 * h], z[4 * h + 1], 0, false);
-                w8[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(z[4 * h + 2], z[4 * h + 3], w, true);
-            }
+            e4m3_codes<8>(y, __uint_as_float(m), &scale, w8);
             if (live) {
                 *(uint2*)(a.y8 + row + c) = uint2{w8[0], w8[1]};
-                if ((tid & 7) == 0) a.y8_scale[(row + c) / kGroup] = scale;
+                if ((tid & (G / 8 - 1)) == 0) a.y8_scale[(size_t)blockIdx.x * ((d + G - 1) / G) + c / G] = scale;
             }
         }
     }
 }
 
+template <int W, int NV, int G>
+void launch_group(const NormArgs& a, hipStream_t s) {
+    if (!a.residual) add_norm_kernel<W, NV, false, false, G><<<a.T, W * 64, 0, s>>>(a);
+    else if (a.res_f32) add_norm_kernel<W, NV, true, true, G><<<a.T, W * 64, 0, s>>>(a);
+    else add_norm_kernel<W, NV, true, false, G><<<a.T, W * 64, 0, s>>>(a);
+}
+
 template <int W, int NV>
 void launch(const NormArgs& a, hipStream_t s) {
-    if (!a.residual) add_norm_kernel<W, NV, false, false><<<a.T, W * 64, 0, s>>>(a);
-    else if (a.res_f32) add_norm_kernel<W, NV, true, true><<<a.T, W * 64, 0, s>>>(a);
-    else add_norm_kernel<W, NV, true, false><<<a.T, W * 64, 0, s>>>(a);
+    if (a.group == 128) launch_group<W, NV, 128>(a, s);
+    else launch_group<W, NV, 64>(a, s);
 }
 
 }  // namespace

@@ -1,6 +1,7 @@
 // ops.h -- launchers of the operators around the MoE layer (scored routing,
-// 4-bit products for a few rows, sampling, residual + RMS norm), shared by
-// abi.hip and their translation units.
+// 4-bit products for a few rows, sampling, residual + RMS norm, 8-bit products,
+// rows into expert order and back, penalties on logits), shared by abi.hip and
+// their translation units.
 #pragma once
 #include "internal.h"
 
@@ -27,8 +28,9 @@ struct NormArgs {
     const uint16_t* weight;   // bf16 [d]
     uint16_t* y;              // bf16 [T][d], or NULL
     uint8_t* y8;              // e4m3 [T][d], or NULL
-    float* y8_scale;          // [T][d/64], with y8
+    float* y8_scale;          // [T][ceil(d/group)], with y8
     int T, d;
+    int group;                // 64 or 128
     float eps, w_add;         // the weight used is weight + w_add
     bool res_f32;
 };
@@ -107,5 +109,66 @@ struct SampleArgs {
 };
 int sample_chunk_sh(int V, int B);  // log2 of the logits per chunk
 hipError_t launch_sample(const SampleArgs& a, hipStream_t s);
+
+// Products in e4m3 (moe_linear_scaled, moe_experts_scaled).
+struct ProductArgs {
+    const uint8_t* w;         // [E][parts][N][K], parts = 2 when gated
+    const float* w_scale;     // [E][parts][ceil(N/128)][ceil(K/128)]
+    const uint8_t* x;         // [rows][K]
+    const float* x_scale;     // [rows][ceil(K/128)]
+    void* y;                  // fp32 or bf16 [rows][N], or e4m3 when gated
+    float* y_scale;           // [rows][ceil(N/128)] when gated
+    int rows, N, K;           // N: rows of one part
+    bool gated, out_bf16;
+    // expert-sorted rows (E = 1 and NULL otherwise)
+    int E;
+    const int32_t* offsets;   // [E + 1]
+    const int32_t* map;       // (expert, first row) per tile
+    const int32_t* n_map;
+    int map_bound;            // host upper bound on *n_map
+    const int32_t* map128;    // the same for tiles of 128 rows
+    const int32_t* n_map128;
+    int map128_bound;
+};
+hipError_t launch_product(const ProductArgs& a, hipStream_t s);
+
+// Rows into expert order and back (moe_dispatch, moe_combine, moe_combine_grad).
+struct SortArgs {
+    const int32_t* inv_perm;  // [T][k]
+    int T, k, d;
+    const uint16_t* x;        // dispatch: bf16 [T][d]
+    void* rows_out;           // bf16 or e4m3 [T*k][d] (combine_grad: d_rows or NULL)
+    float* scale_out;         // dispatch in e4m3: [T*k][ceil(d/128)], or NULL
+    const uint16_t* rows;     // combine, combine_grad: bf16 [T*k][d]
+    const float* w;           // [T][k] or NULL (all 1)
+    const uint16_t* base;     // combine: bf16 [T][d] or NULL
+    uint16_t* y;              // combine: bf16 [T][d]
+    const uint16_t* dy;       // combine_grad: bf16 [T][d]
+    float* d_w;               // combine_grad: [T][k] or NULL
+};
+hipError_t launch_dispatch(const SortArgs& a, hipStream_t s);
+hipError_t launch_combine(const SortArgs& a, hipStream_t s);
+hipError_t launch_combine_grad(const SortArgs& a, hipStream_t s);
+
+// Penalties, biases and a mask on logits (moe_penalize).
+struct PenalizeArgs {
+    const float* logits;      // [B][V]
+    float* out;               // [B][V], may be logits
+    int B, V, chunk_sh;
+    const int32_t* tokens;    // [B][stride] or NULL
+    const int32_t* n_tokens;  // [B] or NULL (all stride)
+    const int32_t* n_prompt;  // [B] or NULL (0)
+    int stride;
+    const float* repetition;  // [B] or NULL (then repetition_all), and so on
+    const float* frequency;
+    const float* presence;
+    float repetition_all, frequency_all, presence_all;
+    const int32_t* bias_ids;  // [B][n_bias]
+    const float* bias;        // [B][n_bias]
+    int n_bias;
+    const uint32_t* mask;     // [B][mask_words] or NULL
+    int mask_words;
+};
+hipError_t launch_penalize(const PenalizeArgs& a, hipStream_t s);
 
 }  // namespace q4moe

@@ -1,0 +1,226 @@
+"""linear_e4m3 and experts_e4m3 against the formula in 64 bits.
+
+Bars, from the arithmetic.  Let S be the sum of the magnitudes of an output's terms.
+  - a sum: products of two e4m3 values are exact in fp32; a block's 128 are added in
+    fp32 in some order, each addition off by at most one step (2^-23) of a partial sum,
+    which is at most the block's S; the factor xs * ws is rounded once and every block
+    once more when it is added, and up to 16 partial sums meet: (128 + blocks + 18) 2^-23 S.
+  - bf16 out: half a step more, 2^-8 of the value.
+  - gated: h = silu(g) u with |silu'| <= 1.1 and |silu(g)| <= |g|: the sums' errors e_g, e_u
+    give 1.1 e_g (|u| + e_u) + |silu(g)| e_u; the exponential of -g has an error of at most
+    (|g| + 2) 2^-22 relative (its argument times log2 e is rounded, then 2 steps), and four
+    roundings of 2^-23 follow.  y_scale: the largest of these errors / 448 and 2^-23 of itself.
+    Codes: half an e4m3 step, 2^-4 of the value or 2^-10 of the scale, and the error of h (an
+    error moves a value over a border by no more than itself) and of the scale."""
+import numpy as np
+import pytest
+import torch
+
+import q4_routed_expert_amd as q4
+from oracle import operators as plain
+from routings import device_routing, quantised_rows, selections, values
+
+pytestmark = pytest.mark.gpu
+f8 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+def weights(rng, *shape):
+    w = torch.from_numpy(rng.standard_normal(shape).astype(np.float32) * shape[-1] ** -0.5)
+    return q4.quantize_blocks(w)
+
+
+def bar_of(size, K):
+    return (128 + -(-K // 128) + 18) * 2.0 ** -23 * size + 1e-37
+
+
+def check(y, want, bar):
+    y = y.float().cpu().numpy().astype(np.float64)
+    assert np.isfinite(y).all()
+    err = np.abs(y - want)
+    assert (err <= bar).all(), (err / bar).max()
+
+
+def gated(w, ws, x, xs):
+    """(h, its error bar) in 64 bits."""
+    (g, sg), (u, su) = (plain.product(values(w[i]), ws[i].numpy(), values(x), xs.numpy())
+                        for i in range(2))
+    eg, eu = bar_of(sg, x.shape[1]), bar_of(su, x.shape[1])
+    silu = g / (1 + np.exp(-g))
+    h = silu * u
+    return h, 1.1 * eg * (np.abs(u) + eu) + np.abs(silu) * eu + np.abs(h) * (np.abs(g) + 6) * 2.0 ** -22
+
+
+def check_gated(y, y_scale, h, eh):
+    s, es = plain.group_scales(h), plain.group_scales(eh)
+    got = y_scale.cpu().numpy().astype(np.float64)
+    assert (np.abs(got - s) <= es + s * 2.0 ** -23).all()
+    T, n = h.shape
+    scale = plain.expand(got, 1, T, n)
+    back = values(y) * scale
+    bar = np.maximum(np.abs(h) * 2.0 ** -4, 2.0 ** -10 * scale) + 2 * eh + plain.expand(es, 1, T, n) * 448
+    assert (np.abs(back - h) <= bar).all(), (np.abs(back - h) / bar).max()
+
+
+# tokens around every tile height, rows and columns off every tile width, half blocks
+LINEAR = [(1, 1, 64), (1, 2048, 2048), (2, 16, 128), (3, 37, 192), (8, 300, 1088), (16, 129, 448),
+          (17, 1000, 512), (31, 64, 8192), (33, 257, 576), (64, 2050, 320), (65, 4100, 256),
+          (127, 130, 640), (128, 512, 1024), (129, 700, 2112), (200, 255, 64), (255, 1030, 192),
+          (257, 1024, 128), (300, 513, 1216), (520, 900, 704), (1030, 770, 384)]
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("T,N,K", LINEAR)
+def test_linear_matches_the_formula(dev, T, N, K, out):
+    rng = np.random.default_rng(T * 7919 + N * 31 + K)
+    x, xs = quantised_rows(rng, T, K)
+    w, ws = weights(rng, N, K)
+    want, size = plain.product(values(w), ws.numpy(), values(x), xs.numpy())
+    room = torch.full((T + 2, N), 7.0, dtype=out, device=dev)  # rows behind the last stay as they were
+    y = q4.linear_e4m3(w.to(dev), ws.to(dev), x.to(dev), xs.to(dev), out_dtype=out, y=room)
+    torch.cuda.synchronize()
+    assert y is room and bool((room[T:] == 7.0).all())
+    check(room[:T], want, bar_of(size, K) + (np.abs(want) * 2.0 ** -8 if out == torch.bfloat16 else 0))
+
+
+@pytest.mark.parametrize("T,I,K", [(1, 64, 64), (1, 512, 2048), (2, 128, 192), (7, 192, 320),
+                                   (16, 320, 128), (33, 512, 1088), (64, 448, 2048), (100, 128, 8192),
+                                   (129, 576, 256), (260, 1024, 448), (600, 384, 1024)])
+def test_gated_matches_the_formula(dev, T, I, K):
+    rng = np.random.default_rng(T * 101 + I + K)
+    x, xs = quantised_rows(rng, T, K)
+    w, ws = weights(rng, 2, I, K)
+    h, eh = gated(w, ws, x, xs)
+    y, y_scale = q4.linear_e4m3(w.to(dev), ws.to(dev), x.to(dev), xs.to(dev), gated=True)
+    assert y.dtype == f8 and y.shape == (T, I) and y_scale.shape == (T, -(-I // 128))
+    check_gated(y, y_scale, h, eh)
+
+
+# decode steps, chunks with experts of no, few and many rows, odd numbers of experts
+EXPERTS = [(1, 2, 1, 64, 64, 0.0), (1, 256, 8, 256, 512, 0.0), (3, 7, 2, 128, 192, 1.0),
+           (8, 32, 8, 192, 320, 0.5), (40, 5, 3, 320, 448, 1.0), (70, 3, 1, 130, 128, 2.0),
+           (150, 33, 4, 64, 192, 1.0), (300, 4, 2, 258, 576, 1.5), (64, 64, 8, 128, 64, 0.0),
+           (500, 16, 4, 512, 256, 1.0)]
+
+
+@pytest.mark.parametrize("T,E,k,N,K,skew", EXPERTS)
+def test_experts_match_the_formula(dev, T, E, k, N, K, skew):
+    rng = np.random.default_rng(T + E * 17 + N)
+    idx, wt = selections(rng, T, E, k, skew)
+    r, o = device_routing(idx, wt, E, dev, room=T % 3)
+    x, xs = quantised_rows(rng, T * k, K)
+    parts = 2 if N % 64 == 0 else 1
+    w, ws = weights(rng, E, parts, N, K)
+    xd, xsd = x.to(dev), xs.to(dev)
+    want, size = np.empty((T * k, N)), np.empty((T * k, N))
+    h, eh = np.empty((T * k, N)), np.empty((T * k, N))
+    for e in range(E):
+        a, b = int(o["offsets"][e]), int(o["offsets"][e + 1])
+        if a < b:
+            want[a:b], size[a:b] = plain.product(values(w[e, 0]), ws[e, 0].numpy(), values(x[a:b]),
+                                                 xs[a:b].numpy())
+            if parts == 2:
+                h[a:b], eh[a:b] = gated(w[e], ws[e], x[a:b], xs[a:b])
+    w0, ws0 = w[:, 0].contiguous().to(dev), ws[:, 0].contiguous().to(dev)
+    y = q4.experts_e4m3(w0, ws0, xd, xsd, r, out_dtype=torch.float32)
+    check(y, want, bar_of(size, K))
+    y = q4.experts_e4m3(w0, ws0, xd, xsd, r)
+    assert y.dtype == torch.bfloat16
+    check(y, want, bar_of(size, K) + np.abs(want) * 2.0 ** -8)
+    if parts == 2:
+        y, y_scale = q4.experts_e4m3(w.to(dev), ws.to(dev), xd, xsd, r, gated=True)
+        check_gated(y, y_scale, h, eh)
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 70, 192), (140, 300, 320), (300, 260, 448)])
+def test_special_values(dev, T, N, K):
+    rng = np.random.default_rng(N)
+    x, xs = quantised_rows(rng, T, K)
+    w, ws = weights(rng, N, K)
+    want, size = plain.product(values(w), ws.numpy(), values(x), xs.numpy())
+    nan = torch.tensor([0x7F], dtype=torch.uint8)
+    x.view(torch.uint8)[1, K - 1] = nan          # that token only
+    w.view(torch.uint8)[N - 1, 0] = nan          # that column only
+    xs[2, 0] = float("inf")                      # an infinite scale
+    xs[0] = 0.0                                  # a token of zeros
+    y = q4.linear_e4m3(w.to(dev), ws.to(dev), x.to(dev), xs.to(dev), out_dtype=torch.float32).cpu()
+    assert y[1].isnan().all() and y[:, N - 1].isnan().all()
+    assert not y[2].isfinite().any()
+    assert (y[0, :N - 1] == 0).all()
+    keep = [t for t in range(T) if t > 2]
+    if keep:
+        check(y[keep][:, :N - 1], want[keep][:, :N - 1], bar_of(size, K)[keep][:, :N - 1])
+
+
+@pytest.mark.parametrize("T", [3, 200])
+def test_gated_special_values(dev, T):
+    rng = np.random.default_rng(5)
+    I, K = 192, 128
+    x, xs = quantised_rows(rng, T, K)
+    w, ws = weights(rng, 2, I, K)
+    x.view(torch.uint8)[1, 0] = 0x7F             # NaN: the token's codes and scales
+    xs[0] = 0.0                                  # zeros: codes and scales 0
+    w.view(torch.uint8)[1, 130, 3] = 0x7F        # a NaN column: its group only
+    y, s = q4.linear_e4m3(w.to(dev), ws.to(dev), x.to(dev), xs.to(dev), gated=True)
+    y, s = y.cpu().float(), s.cpu()
+    assert y[1].isnan().all() and s[1].isnan().all()
+    assert (y[0, :128] == 0).all() and s[0, 0] == 0
+    assert y[:, 128:].isnan().all() and s[:, 1].isnan().all()
+    assert y[2, :128].isfinite().all() and s[2, 0].isfinite()
+
+
+def test_products_with_every_code(dev):
+    # every pair of finite codes once, at K = 64: no operand bit or sign is lost
+    codes = torch.arange(256, dtype=torch.uint8)
+    codes = codes[(codes & 0x7F) != 0x7F]
+    T = N = codes.numel()
+    x = torch.zeros(T, 64, dtype=torch.uint8)
+    w = torch.zeros(N, 64, dtype=torch.uint8)
+    x[:, 13], w[:, 13] = codes, codes
+    x, w = x.view(f8), w.view(f8)
+    one = lambda *s: torch.ones(*s)                                                 # noqa: E731
+    y = q4.linear_e4m3(w.to(dev), one(2, 1).to(dev), x.to(dev), one(T, 1).to(dev),
+                       out_dtype=torch.float32)
+    v = codes.view(f8).float()
+    assert torch.equal(y.cpu(), v[:, None] * v[None, :])
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 512, 2048), (9, 300, 1024), (150, 512, 256), (400, 700, 512)])
+def test_calls_repeat_and_streams_and_graphs(dev, T, N, K):
+    rng = np.random.default_rng(T)
+    x, xs = (t.to(dev) for t in quantised_rows(rng, T, K))
+    w, ws = (t.to(dev) for t in weights(rng, N, K))
+    want = q4.linear_e4m3(w, ws, x, xs)
+    assert torch.equal(want, q4.linear_e4m3(w, ws, x, xs))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = q4.linear_e4m3(w, ws, x, xs, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    y = torch.zeros_like(want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q4.linear_e4m3(w, ws, x, xs, y=y)
+    for _ in range(3):
+        xs.mul_(-2.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, q4.linear_e4m3(w, ws, x, xs))
+
+
+def test_outputs_past_32_bits(dev):
+    # y has more than 2^31 elements, and the last row has to be right
+    T, N, K = 32768, 65600, 64
+    rng = np.random.default_rng(3)
+    x, xs = quantised_rows(rng, T, K)
+    w, ws = weights(rng, N, K)
+    y = q4.linear_e4m3(w.to(dev), ws.to(dev), x.to(dev), xs.to(dev))
+    rows = [0, 1, 16383, 32735, 32767]
+    want, size = plain.product(values(w), ws.numpy(), values(x[rows]), xs[rows].numpy())
+    check(y[rows], want, bar_of(size, K) + np.abs(want) * 2.0 ** -8)
