@@ -154,7 +154,7 @@ hipError_t launch_combine_grad(const SortArgs& a, hipStream_t s);
 struct PenalizeArgs {
     const float* logits;      // [B][V]
     float* out;               // [B][V], may be logits
-    int B, V, chunk_sh;
+    int B, V;
     const int32_t* tokens;    // [B][stride] or NULL
     const int32_t* n_tokens;  // [B] or NULL (all stride)
     const int32_t* n_prompt;  // [B] or NULL (0)

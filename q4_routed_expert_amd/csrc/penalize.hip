@@ -7,64 +7,135 @@
 //   l <- allowed(v) ? l : -inf
 //
 // A work group owns a chunk of the vocabulary of one row: it reads the row's tokens, counts
-// those of its chunk in LDS (whole numbers: their order does not matter), then passes once
-// over the chunk's logits.  Bound by HBM: 8 bytes per logit; the tokens are read once per
-// chunk, from L2.
+// those of its chunk in LDS (whole numbers: their order does not matter) and marks the tokens
+// that have a bias, then passes once over the chunk's logits.  Bound by HBM: 8 bytes per
+// logit; the tokens are read once per chunk, from L2.  In place, logits that nothing touches
+// are neither read nor written.
 #include "ops.h"
 
 namespace q4moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr uint32_t kSeen = 0x80000000u;  // the top bit of a counter: seen at all
+constexpr uint32_t kSeen = 0x80000000u;    // top bits of a counter: seen at all,
+constexpr uint32_t kBiased = 0x40000000u;  // has a bias
+constexpr uint32_t kTimes = 0x3FFFFFFFu;
 
+// Sixteen bytes at a 4-byte address (rows of odd lengths).
+template <typename T>
+struct __attribute__((packed, aligned(4))) Four {
+    T v[4];
+};
+
+// Four logits at `at` of a row; the last ones may lie behind its end.
+__device__ __forceinline__ Four<float> load4(const float* row, int at, int n) {
+    Four<float> f;
+    if (at + 4 <= n) return *(const Four<float>*)(row + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.v[i] = at + i < n ? row[at + i] : 0.0f;
+    return f;
+}
+
+// NV pieces of four logits per thread: a chunk is 1024 NV logits.
+template <int NV, bool IN_PLACE>
 __global__ __launch_bounds__(kThreads) void penalize_kernel(const PenalizeArgs a) {
-    extern __shared__ uint32_t count[];
-    const int chunk = 1 << a.chunk_sh, v0 = (int)blockIdx.x << a.chunk_sh, b = blockIdx.y;
-    const int V = a.V, n = min(chunk, V - v0), tid = threadIdx.x;
-    for (int i = tid; i < n; i += kThreads) count[i] = 0u;
-    __syncthreads();
+    constexpr int kChunk = NV * 4 * kThreads;
+    __shared__ u32x4 count4[kChunk / 4];
+    uint32_t* count = (uint32_t*)count4;
+    const int v0 = (int)blockIdx.x * kChunk, b = blockIdx.y, tid = threadIdx.x;
+    const int V = a.V, n = min(kChunk, V - v0);
+    const float* in = a.logits + (size_t)b * V + v0;
+    float* out = a.out + (size_t)b * V + v0;
+    Four<float> l[NV];
+    if constexpr (!IN_PLACE) {  // in flight while the tokens are counted
+#pragma unroll
+        for (int j = 0; j < NV; ++j) l[j] = load4(in, 4 * (tid + kThreads * j), n);
+    }
+    if (a.tokens || a.n_bias) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) count4[tid + kThreads * j] = u32x4{0u, 0u, 0u, 0u};
+        __syncthreads();
+    }
     if (a.tokens) {
-        const int total = min(max(a.n_tokens ? a.n_tokens[b] : a.stride, 0), a.stride);
+        const int total = a.n_tokens ? min(max(a.n_tokens[b], 0), a.stride) : a.stride;
         const int prompt = a.n_prompt ? a.n_prompt[b] : 0;
         const int32_t* tok = a.tokens + (size_t)b * a.stride;
-        for (int i = tid; i < total; i += kThreads) {
-            const uint32_t at = (uint32_t)tok[i] - (uint32_t)v0;  // (a negative id is far out)
-            if (at < (uint32_t)n && tok[i] >= 0) {
+        auto add = [&](int32_t id, int i) {
+            const uint32_t at = (uint32_t)id - (uint32_t)v0;
+            if (id >= 0 && at < (uint32_t)n) {
                 if (i >= prompt) atomicAdd(&count[at], 1u);
                 else atomicOr(&count[at], kSeen);
             }
+        };
+        int i = 4 * tid;
+        for (; i + 4 <= total; i += 4 * kThreads) {
+            const Four<int32_t> t = *(const Four<int32_t>*)(tok + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) add(t.v[j], i + j);
         }
-        __syncthreads();
+        for (; i < total; ++i) add(tok[i], i);  // one thread's: the last ones
     }
+    const int32_t* ids = a.bias_ids + (size_t)b * a.n_bias;
+    for (int i = tid; i < a.n_bias; i += kThreads) {
+        const int32_t id = ids[i];
+        const uint32_t at = (uint32_t)id - (uint32_t)v0;
+        if (id >= 0 && at < (uint32_t)n) atomicOr(&count[at], kBiased);
+    }
+    if (a.tokens || a.n_bias) __syncthreads();
     const float rep0 = a.repetition ? a.repetition[b] : a.repetition_all;
     const float rep = rep0 > 0.0f ? rep0 : 1.0f;  // (NaN too)
     const float freq = a.frequency ? a.frequency[b] : a.frequency_all;
     const float pres = a.presence ? a.presence[b] : a.presence_all;
-    const size_t base = (size_t)b * V;
-    for (int i = tid; i < n; i += kThreads) {
-        const int v = v0 + i;
-        float l = a.logits[base + v];
-        const uint32_t m = count[i];
-        if (m) {
-            l = l > 0.0f ? l / rep : l * rep;
-            const uint32_t times = m & ~kSeen;
-            if (times) l = l - freq * (float)times - pres;
+    const uint32_t* mask = a.mask ? a.mask + (size_t)b * a.mask_words : nullptr;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int at = 4 * (tid + kThreads * j);
+        if (at >= n) continue;
+        // (v0 + at is a multiple of 4: the four bits are in one word)
+        const uint32_t allowed = mask ? (mask[(v0 + at) >> 5] >> ((v0 + at) & 31)) & 15u : 15u;
+        u32x4 m = {0u, 0u, 0u, 0u};
+        if (a.tokens || a.n_bias) m = count4[tid + kThreads * j];
+        if constexpr (IN_PLACE) {
+            if (allowed == 15u && (m[0] | m[1] | m[2] | m[3]) == 0u) continue;
+            l[j] = load4(in, at, n);
         }
-        for (int j = 0; j < a.n_bias; ++j)
-            if (a.bias_ids[(size_t)b * a.n_bias + j] == v) l += a.bias[(size_t)b * a.n_bias + j];
-        if (a.mask && !((a.mask[(size_t)b * a.mask_words + (v >> 5)] >> (v & 31)) & 1u)) l = -INFINITY;
-        a.out[base + v] = l;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x = l[j].v[i];
+            if (m[i]) {
+                const uint32_t times = m[i] & kTimes;
+                if (times || (m[i] & kSeen)) x = x > 0.0f ? x / rep : x * rep;
+                // (one rounding an operation)
+                if (times) x = __fsub_rn(__fsub_rn(x, __fmul_rn(freq, (float)times)), pres);
+                if (m[i] & kBiased)
+                    for (int k = 0; k < a.n_bias; ++k)
+                        if (ids[k] == v0 + at + i) x += a.bias[(size_t)b * a.n_bias + k];
+            }
+            l[j].v[i] = (allowed >> i) & 1u ? x : -INFINITY;
+        }
+        if (at + 4 <= n) {
+            *(Four<float>*)(out + at) = l[j];
+        } else {
+            for (int i = 0; at + i < n; ++i) out[at + i] = l[j].v[i];
+        }
     }
+}
+
+template <int NV>
+void launch(const PenalizeArgs& a, hipStream_t s) {
+    const dim3 grid((a.V + NV * 4 * kThreads - 1) / (NV * 4 * kThreads), a.B);
+    if (a.out == a.logits) penalize_kernel<NV, true><<<grid, kThreads, 0, s>>>(a);
+    else penalize_kernel<NV, false><<<grid, kThreads, 0, s>>>(a);
 }
 
 }  // namespace
 
-hipError_t launch_penalize(const PenalizeArgs& a0, hipStream_t s) {
-    PenalizeArgs a = a0;
-    a.chunk_sh = 12;
-    const int chunk = 1 << a.chunk_sh;
-    penalize_kernel<<<dim3((a.V + chunk - 1) / chunk, a.B), kThreads, chunk * sizeof(uint32_t), s>>>(a);
+hipError_t launch_penalize(const PenalizeArgs& a, hipStream_t s) {
+    const long long logits = (long long)a.B * a.V;
+    if (logits >= 8192LL * 1024) launch<8>(a, s);
+    else if (logits >= 4096LL * 1024) launch<4>(a, s);
+    else if (logits >= 2048LL * 512) launch<2>(a, s);
+    else launch<1>(a, s);
     trace_point(s);
     return hipGetLastError();
 }
