@@ -486,9 +486,10 @@ int moe_combine_grad(const uint16_t* dy, const uint16_t* rows, int32_t T, int32_
    tokens and in bias_ids, are passed over.  A row whose mask leaves nothing is -inf throughout
    (moe_sample gives token 0 and prob 0 for it).  Bits behind V are not looked at.
    logits and out: fp32 [B][V], 16-byte aligned, out may be logits; the other arrays are
-   4-byte aligned.  1 <= B <= MOE_MAX_SAMPLE_ROWS, 1 <= V <= MOE_MAX_VOCAB, 0 <= n_bias <=
-   MOE_MAX_BIASES.  One kernel, no workspace; equal calls give equal results. */
+   4-byte aligned.  1 <= B <= MOE_MAX_SAMPLE_ROWS, 1 <= V <= MOE_MAX_VOCAB, 0 <= stride <=
+   MOE_MAX_HISTORY, 0 <= n_bias <= MOE_MAX_BIASES.  One kernel, no workspace; equal calls give equal results. */
 #define MOE_MAX_BIASES 1024
+#define MOE_MAX_HISTORY 1048576
 typedef struct {
     const int32_t* tokens;      /* [B][stride] or NULL */
     const int32_t* n_tokens;    /* [B] or NULL: all of them */

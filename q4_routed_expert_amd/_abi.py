@@ -17,6 +17,7 @@ MOE_OUT_BF16, MOE_GATED = 1, 2
 MOE_UNWEIGHTED = 1
 MOE_E4M3_BLOCK = 128
 MOE_MAX_BIASES = 1024
+MOE_MAX_HISTORY = 1 << 20
 MOE_MAX_LINEAR_TOKENS = 64
 MOE_MAX_SAMPLE_ROWS = 1024
 MOE_BLOCK_ROWS = 32

@@ -859,6 +859,8 @@ int moe_penalize(const float* logits, int32_t B, int32_t V, const moe_penalties*
         (rc = check_row_array(p->bias, "bias", true)) || (rc = check_row_array(p->mask, "mask", true)))
         return rc;
     if (p->tokens && p->stride < 0) return fail(MOE_EINVAL, "stride=%d", p->stride);
+    if (p->tokens && p->stride > MOE_MAX_HISTORY)
+        return fail(MOE_EUNSUPPORTED, "stride=%d > %d", p->stride, MOE_MAX_HISTORY);
     if (!p->tokens && (p->n_tokens || p->n_prompt))
         return fail(MOE_EINVAL, "n_tokens and n_prompt need tokens");
     if (!p->bias_ids != !p->bias) return fail(MOE_EINVAL, "bias_ids and bias come together");

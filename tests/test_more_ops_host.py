@@ -117,12 +117,13 @@ def test_penalize_refuses():
                 dict(repetition=FAKE + 2)):
         assert penalize(penalties(**bad)) == EINVAL, bad
     assert penalize(penalties(bias_ids=FAKE, bias=FAKE, n_bias=1025)) == EUNSUPPORTED
+    assert penalize(penalties(tokens=FAKE, stride=_abi.MOE_MAX_HISTORY + 1)) == EUNSUPPORTED
 
 
 def test_struct_sizes_and_limits_match_the_header():
     text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
                              "q4moe.h")).read()
-    for name in ("MOE_E4M3_BLOCK", "MOE_MAX_BIASES", "MOE_GATED", "MOE_UNWEIGHTED",
+    for name in ("MOE_E4M3_BLOCK", "MOE_MAX_BIASES", "MOE_MAX_HISTORY", "MOE_GATED", "MOE_UNWEIGHTED",
                  "MOE_NORM_GROUP_128"):
         assert int(re.search(rf"#define {name} (\d+)", text).group(1)) == getattr(_abi, name), name
     assert C.sizeof(_abi.Penalties) == 9 * 8 + 5 * 4 + 4 and C.sizeof(_abi.E4m3Mat) == 16
