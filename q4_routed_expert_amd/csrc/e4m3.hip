@@ -289,11 +289,12 @@ struct TileOperand<true> {
 };
 
 // E4M3: the matrix cores' own 8-bit products (see the top), for bf16 outputs.
-template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAPPED>
+template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAPPED, bool ROTATE>
 __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const ProductArgs a) {
-    static_assert(WM * WN == 8 && (S == 2 || S == 3) && (!GATED || BN == 256), "shape");
+    static_assert(WM * WN == 8 && S >= 2 && S <= 4 && (!GATED || BN == 256), "shape");
     constexpr int MT = BM / WM / 16, NT = BN / WN / 16, M = GATED ? 2 : 1;
-    constexpr int kX = BN * kBlock, kXs = kX + BM * kBlock, kStage = kXs + 4 * BM;
+    constexpr int kX = BN * kBlock, kXs = kX + BM * kBlock;
+    constexpr int kScales = BM < 64 ? 256 : 4 * BM, kStage = kXs + kScales;  // (a load writes 256 bytes)
     constexpr int kWLoads = BN / 64, kXLoads = (BM + 63) / 64, kLoads = kWLoads + kXLoads + 1;
     __shared__ __attribute__((aligned(16))) unsigned char lds[S * kStage];
     __shared__ float s_ws[2][kMaxBlocks];  // the scales of W's two halves (gated: gate, up)
@@ -359,7 +360,7 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const Produc
         for (int j = 0; j < kXLoads; ++j)
             load16_lds(x_rsrc, xoff[j] - back, b * kBlock,
                        lds0 + at + kX + (1024u * (uint32_t)(wave + 8 * j)) % (uint32_t)(BM * kBlock));
-        load4_lds(s_rsrc, soff, 4 * b, lds0 + at + kXs + (256u * (uint32_t)wave) % (4u * BM));
+        load4_lds(s_rsrc, soff, 4 * b, lds0 + at + kXs + (256u * (uint32_t)wave) % (uint32_t)kScales);
     };
 
     f32x4 acc[MT][NT];
@@ -418,9 +419,13 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const Produc
             }
         }
     };
+    // Every tile begins with another block of columns: W's rows lie a power of two apart, and
+    // tiles in step would read the same few memory channels.
+    const int turn = ROTATE ? (nt + s.e) % KB : 0;
+    auto block = [&](int i) { return ROTATE ? (i + turn < KB ? i + turn : i + turn - KB) : i; };
 #pragma unroll
     for (int j = 0; j < S - 1; ++j)
-        if (j < KB) load(j * kStage, j);
+        if (j < KB) load(j * kStage, block(j));
     {
         const int h = tid >> 6;
         if (h < 2 && lane < KB) {
@@ -429,17 +434,18 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const Produc
             s_ws[h][lane] = half && lane == KB - 1 ? 0.5f * ws : ws;
         }
     }
-    // Block b: wait for its loads (those of the next S - 2 blocks stay in flight), start those
-    // of block b + S - 1 into the stage that every wave has left, multiply.
+    // Step i: wait for its block's loads (those of the next S - 2 blocks stay in flight), start
+    // those of block i + S - 1 into the stage that every wave has left, multiply.
     uint32_t here = 0;
-    for (int b = 0; b < KB; ++b) {
-        if (S > 2 && b + 1 < KB) wait_loads<(S - 2) * kLoads>();
+    for (int i = 0; i < KB; ++i) {
+        if (S > 3 && i + 2 < KB) wait_loads<(S > 3 ? 2 * kLoads : 0)>();
+        else if (S > 2 && i + 1 < KB) wait_loads<(S > 2 ? kLoads : 0)>();
         else wait_loads<0>();
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (s_ws, once)
         __builtin_amdgcn_s_barrier();
         const uint32_t free_at = here == 0 ? (S - 1) * kStage : here - kStage;
-        if (b + S - 1 < KB) load(free_at, b + S - 1);
-        compute(here, b);
+        if (i + S - 1 < KB) load(free_at, block(i + S - 1));
+        compute(here, block(i));
         here = here == (S - 1) * kStage ? 0 : here + kStage;
     }
 
@@ -491,11 +497,11 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const Produc
     }
 }
 
-template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAPPED>
+template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAPPED, bool ROTATE>
 void launch_tile(const ProductArgs& a, int tiles, hipStream_t s) {
     constexpr int kCols = GATED ? BN / 2 : BN;
     const unsigned grid = (unsigned)tiles * (unsigned)((a.N + kCols - 1) / kCols);
-    product_tile_kernel<BM, BN, WM, WN, S, E4M3, GATED, MAPPED><<<grid, kTileThreads, 0, s>>>(a);
+    product_tile_kernel<BM, BN, WM, WN, S, E4M3, GATED, MAPPED, ROTATE><<<grid, kTileThreads, 0, s>>>(a);
 }
 
 // Rows of a tile map of BM-row tiles (dense: the rows themselves).
@@ -515,26 +521,37 @@ int tiles_of(ProductArgs& a) {
 hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
     ProductArgs a = a0;
     const int per = a.map ? (a.rows + a.E - 1) / a.E : a.rows;  // rows that share a matrix
-    if (per <= 16) {
+    const long long wgs256 = (long long)((a.N + 255) / 256) * (a.map ? min(a.rows, a.E) : (a.rows + 31) / 32);
+    if (a.map) {
+        if (per <= 16) {
+            const int tiles = tiles_of<32>(a);
+            if (a.gated) launch_tile<32, 256, 1, 8, 4, false, true, true, true>(a, tiles, s);
+            else if (wgs256 >= 128) launch_tile<32, 256, 1, 8, 4, false, false, true, true>(a, tiles, s);
+            else launch_split<2, 4, false>(a, tiles, s);
+        } else if (a.gated) {
+            launch_tile<128, 256, 2, 4, 3, false, true, true, true>(a, tiles_of<128>(a), s);
+        } else {
+            launch_tile<128, 256, 2, 4, 3, false, false, true, true>(a, tiles_of<128>(a), s);
+        }
+    } else if (per <= 16) {
         const int tiles = tiles_of<32>(a);
-        if (a.gated) launch_split<2, 2, true>(a, tiles, s);
-        else launch_split<2, 4, false>(a, tiles, s);
-    } else if (a.map) {
-        if (a.gated) launch_tile<128, 256, 2, 4, 3, false, true, true>(a, tiles_of<128>(a), s);
-        else launch_tile<128, 256, 2, 4, 3, false, false, true>(a, tiles_of<128>(a), s);
+        if (a.gated) launch_split<1, 2, true>(a, tiles_of<16>(a), s);
+        else if (wgs256 >= 128) launch_tile<32, 256, 1, 8, 4, false, false, false, true>(a, tiles, s);
+        else if (a.N < 4096) launch_split<1, 16, false>(a, tiles_of<16>(a), s);
+        else launch_split<1, 8, false>(a, tiles_of<16>(a), s);
     } else if (a.gated) {
-        if (a.rows >= 2048) launch_tile<256, 256, 2, 4, 2, false, true, false>(a, tiles_of<256>(a), s);
-        else if (a.rows <= 64) launch_tile<64, 256, 2, 4, 3, false, true, false>(a, tiles_of<64>(a), s);
-        else launch_tile<128, 256, 2, 4, 3, false, true, false>(a, tiles_of<128>(a), s);
+        if (a.rows >= 2048) launch_tile<256, 256, 2, 4, 2, false, true, false, false>(a, tiles_of<256>(a), s);
+        else if (a.rows <= 64) launch_tile<64, 256, 2, 4, 3, false, true, false, true>(a, tiles_of<64>(a), s);
+        else launch_tile<128, 256, 2, 4, 3, false, true, false, false>(a, tiles_of<128>(a), s);
     } else {
         const bool wide = (long long)((a.N + 255) / 256) * ((a.rows + 255) / 256) >= 256;
         if (wide) {
-            if (a.out_bf16) launch_tile<256, 256, 2, 4, 2, true, false, false>(a, tiles_of<256>(a), s);
-            else launch_tile<256, 256, 2, 4, 2, false, false, false>(a, tiles_of<256>(a), s);
+            if (a.out_bf16) launch_tile<256, 256, 2, 4, 2, true, false, false, false>(a, tiles_of<256>(a), s);
+            else launch_tile<256, 256, 2, 4, 2, false, false, false, false>(a, tiles_of<256>(a), s);
         } else if (a.rows <= 64) {
-            launch_tile<64, 128, 2, 4, 3, false, false, false>(a, tiles_of<64>(a), s);
+            launch_tile<64, 128, 2, 4, 3, false, false, false, true>(a, tiles_of<64>(a), s);
         } else {
-            launch_tile<128, 128, 2, 4, 3, false, false, false>(a, tiles_of<128>(a), s);
+            launch_tile<128, 128, 2, 4, 3, false, false, false, false>(a, tiles_of<128>(a), s);
         }
     }
     trace_point(s);
