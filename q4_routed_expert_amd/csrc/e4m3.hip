@@ -31,6 +31,11 @@ struct RowSpan {
     int row0, n, e;
 };
 
+// The maps are read through scalar loads: nothing writes them while a kernel runs, and a vector
+// load would be waited for behind every load of a tile that is in flight.
+typedef const __attribute__((address_space(4))) int32_t* ScalarInts;
+__device__ __forceinline__ int scalar_int(const int32_t* p, size_t i) { return ((ScalarInts)(uintptr_t)p)[i]; }
+
 // Tile j of TR rows: of the rows themselves, or of the map of expert-sorted rows.  Map
 // entries come from device memory: what is out of range is brought into it.
 template <int TR>
@@ -40,13 +45,17 @@ __device__ __forceinline__ RowSpan span_of(const ProductArgs& a, int j) {
         s.row0 = j * TR;
         s.n = a.rows - s.row0;
     } else {
-        if (j >= min(*a.n_map, a.map_bound)) return s;
-        s.e = min(max(a.map[2 * j], 0), a.E - 1);
-        s.row0 = min(max(a.map[2 * j + 1], 0), a.rows);
-        s.n = min(a.offsets[s.e + 1], a.rows) - s.row0;
+        s.e = min(max(scalar_int(a.map, 2 * (size_t)j), 0), a.E - 1);
+        s.row0 = min(max(scalar_int(a.map, 2 * (size_t)j + 1), 0), a.rows - 1);
+        s.n = min(scalar_int(a.offsets, s.e + 1), a.rows) - s.row0;
     }
     s.n = min(max(s.n, 0), TR);
     return s;
+}
+
+// Tiles of the map that are there.
+__device__ __forceinline__ int mapped_tiles(const ProductArgs& a) {
+    return min(scalar_int(a.n_map, 0), a.map_bound);
 }
 
 // 32 codes of a row as four bf16 operands.
@@ -110,6 +119,7 @@ __global__ __launch_bounds__(kWaves * 64) void product_split_kernel(const Produc
     const int c = lane & 15, g = lane >> 4;
     const int p = wave % PT, ks = wave / PT;
     const int N = a.N, K = a.K, KB = (K + kBlock - 1) / kBlock, NB = (N + kBlock - 1) / kBlock;
+    if (a.map && (int)blockIdx.y >= mapped_tiles(a)) return;
     const RowSpan s = span_of<16 * TT>(a, blockIdx.y);
     if (s.n == 0) return;
     const int n0 = (blockIdx.x * PT + p) * 16;  // first weight row of the wave's tile
@@ -229,12 +239,21 @@ void launch_split(const ProductArgs& a, int tiles, hipStream_t s) {
 // Tiles: BM tokens by BN weight rows per work group of 8 waves, WM x WN of them; x and W go
 // through LDS in S stages of one block of 128 columns each, loaded straight into it.
 //
+// One work group per CU walks its share of the tiles, and its stages run on from one tile to the
+// next: the loads of the next tile are under way while the last blocks of this one are
+// multiplied and its outputs are stored.
+//
 // LDS holds a row of a stage as eight 16-byte pieces, piece c at place c ^ (row & 7): the
 // loads write LDS in lane order, so a lane fetches the piece that belongs at its place, and
 // sixteen lanes that read the same piece of sixteen rows meet all banks.
 // ---------------------------------------------------------------------------
 constexpr int kTileThreads = 512;
-constexpr int kMaxBlocks = MOE_MAX_D / kBlock;
+constexpr int kGrid = 256;  // CUs
+
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
 
 // Loads of 16 (4) bytes per lane straight into LDS at lds + 16 (4) * lane, from the buffer rsrc
 // at voff + soff; lds, rsrc and soff are the wave's.  Written out because the compiler waits
@@ -271,237 +290,298 @@ __device__ __forceinline__ void wait_loads() {
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
 
-// Tile id of this work group: work groups go to the 8 XCDs in turn, so consecutive ids of
-// one XCD are made neighbouring tiles (of which the XCD's L2 holds what they share).
-__device__ __forceinline__ int neighbour_id(int id, int total) {
-    const int per = total >> 3, rest = total & 7, xcd = id & 7, at = id >> 3;
-    return xcd * per + min(xcd, rest) + at;
-}
-
+typedef int i32x8 __attribute__((ext_vector_type(8)));
 template <bool E4M3>
 struct TileOperand {
     using type = Operand;
 };
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 template <>
 struct TileOperand<true> {
     using type = i32x8;
 };
 
+template <bool E4M3>
+__device__ __forceinline__ typename TileOperand<E4M3>::type tile_operand(const u32x4& u, const u32x4& v) {
+    if constexpr (E4M3) return i32x8{(int)u[0], (int)u[1], (int)u[2], (int)u[3], (int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+    else return operand(u, v);
+}
+
+// A block's products of NT tiles of weight rows with one of tokens; four independent chains
+// take turns, so that no product waits for the one before.
+template <int NT>
+__device__ __forceinline__ void tile_products(f32x4 (&d)[NT], const Operand (&w)[NT], const Operand& x) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                w[i].v[j], x.v[j], j == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : d[i], 0, 0, 0);
+}
+
+template <int NT>
+__device__ __forceinline__ void tile_products(f32x4 (&d)[NT], const i32x8 (&w)[NT], const i32x8& x) {
+    // formats 0 (e4m3) for both; scales 0 select the instruction without block exponents
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+        d[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[i], x, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+}
+
 // E4M3: the matrix cores' own 8-bit products (see the top), for bf16 outputs.
-template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAPPED, bool ROTATE>
+template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAPPED>
 __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const ProductArgs a) {
-    static_assert(WM * WN == 8 && S >= 2 && S <= 4 && (!GATED || BN == 256), "shape");
+    static_assert(WM * WN == 8 && S >= 2 && S <= 4 && (!GATED || BN == 256) && (!MAPPED || BM / WM <= 64), "shape");
     constexpr int MT = BM / WM / 16, NT = BN / WN / 16, M = GATED ? 2 : 1;
-    constexpr int kX = BN * kBlock, kXs = kX + BM * kBlock;
-    constexpr int kScales = BM < 64 ? 256 : 4 * BM, kStage = kXs + kScales;  // (a load writes 256 bytes)
+    constexpr bool INTER = MAPPED;
+    // a stage: W's rows, x's rows, x's scales (a load writes 256 bytes), the two scales of W
+    constexpr int kX = BN * kBlock, kXs = kX + BM * kBlock, kWs = kXs + (BM < 64 ? 256 : 4 * BM), kStage = kWs + 256;
     constexpr int kWLoads = BN / 64, kXLoads = (BM + 63) / 64, kLoads = kWLoads + kXLoads + 1;
     __shared__ __attribute__((aligned(16))) unsigned char lds[S * kStage];
-    __shared__ float s_ws[2][kMaxBlocks];  // the scales of W's two halves (gated: gate, up)
     __shared__ uint32_t amax[GATED ? WN : 1][GATED ? BM : 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4, wm = wave / WN, wn = wave % WN;
     const int N = a.N, K = a.K, KB = (K + kBlock - 1) / kBlock, NB = (N + kBlock - 1) / kBlock;
     constexpr int kCols = BN / M;  // output columns of a tile
     const int n_tiles = (N + kCols - 1) / kCols;
+    const int m_tiles = MAPPED ? mapped_tiles(a) : (a.rows + BM - 1) / BM;
 
-    RowSpan s;
-    int nt;
-    if constexpr (MAPPED) {  // neighbours: the columns of one tile of rows
-        const int total = min(*a.n_map, a.map_bound) * n_tiles;
-        if ((int)blockIdx.x >= total) return;
-        const int id = neighbour_id(blockIdx.x, total);
-        nt = id % n_tiles;
-        s = span_of<BM>(a, id / n_tiles);
-    } else {  // neighbours: 8 tiles of rows by a few of columns
-        const int m_tiles = (a.rows + BM - 1) / BM, id = neighbour_id(blockIdx.x, m_tiles * n_tiles);
-        const int group = id / (8 * n_tiles), in = id - group * 8 * n_tiles;
-        const int high = min(8, m_tiles - 8 * group);
-        nt = in / high;
-        s = span_of<BM>(a, 8 * group + in % high);
-    }
-    if (s.n == 0) return;
-    const int n0 = nt * kCols;
+    // Work groups go to the 8 XCDs in turn: an XCD takes a run of neighbouring tiles, its work
+    // groups the next ones of it in turn, so that its L2 holds what they share.
+    const int total = m_tiles * n_tiles, xcd = blockIdx.x & 7, per_xcd = gridDim.x >> 3;
+    const int end = (int)((long long)total * (xcd + 1) >> 3);
+    const int first = (int)((long long)total * xcd >> 3) + ((int)blockIdx.x >> 3);
+    if (first >= end) return;
 
-    // this lane's piece of every load: row lane / 8 of 8, place lane % 8
-    const int piece = (lane & 7) ^ (lane >> 3);
-    const uint8_t* wbase = a.w + ((size_t)s.e * M * N + n0) * (size_t)K;
-    const uint8_t* xbase = a.x + (size_t)s.row0 * K;
-    uint32_t woff[kWLoads], xoff[kXLoads];
-#pragma unroll
-    for (int j = 0; j < kWLoads; ++j) {
-        const int r = 8 * (wave + 8 * j) + (lane >> 3);
-        if (GATED) {
-            woff[j] = (uint32_t)min(r & 127, N - 1 - n0) * (uint32_t)K + 16 * piece;
+    // Tile `id`: its rows and its column tile.  Neighbours are, of expert-sorted rows, the
+    // columns of one tile of rows; else 8 tiles of rows by a few of columns.
+    auto tile = [&](int id, int* nt) {
+        if constexpr (MAPPED) {
+            *nt = id % n_tiles;
+            return span_of<BM>(a, id / n_tiles);
         } else {
-            woff[j] = (uint32_t)min(r, N - 1 - n0) * (uint32_t)K + 16 * piece;
+            const int group = id / (8 * n_tiles), in = id - group * 8 * n_tiles;
+            const int high = min(8, m_tiles - 8 * group);
+            *nt = in / high;
+            return span_of<BM>(a, 8 * group + in % high);
         }
-    }
-#pragma unroll
-    for (int j = 0; j < kXLoads; ++j) {
-        const int r = (8 * (wave + 8 * j) + (lane >> 3)) % BM;
-        xoff[j] = (uint32_t)min(r, s.n - 1) * (uint32_t)K + 16 * piece;
-    }
-    const uint32_t soff = (uint32_t)(s.row0 + min((64 * wave + lane) % BM, s.n - 1)) * (uint32_t)KB * 4u;
-    const u32x4 w_rsrc = buffer_from(wbase), x_rsrc = buffer_from(xbase), s_rsrc = buffer_from(a.x_scale);
-    const u32x4 up_rsrc = buffer_from(wbase + (GATED ? (size_t)N * K : 0));
+    };
+
+    // Loading: tile l_id, block l_b; this lane's piece of every load is row lane / 8 of 8,
+    // place lane % 8.
+    const int piece = (lane & 7) ^ (lane >> 3);
     const bool half = K & 64;  // the last block has 64 columns
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-
-    // Block b of the tile into the stage at `at` (the second half of a half block is its first
-    // again).
-    auto load = [&](uint32_t at, int b) {
-        const uint32_t back = half && b == KB - 1 && piece >= 4 ? 64u : 0u;
+    int l_id = first, l_b = 0;
+    uint32_t woff[kWLoads], xoff[kXLoads], soff;
+    u32x4 w_rsrc, up_rsrc, x_rsrc, s_rsrc;
+    auto enter = [&](int id) {
+        int nt;
+        const RowSpan s = tile(id, &nt);
+        const int n0 = nt * kCols, last = max(s.n, 1) - 1;
+        const uint8_t* w = a.w + ((size_t)s.e * M * N + n0) * (size_t)K;
+        w_rsrc = buffer_from(w);
+        up_rsrc = buffer_from(w + (GATED ? (size_t)N * K : 0));
+        x_rsrc = buffer_from(a.x + (size_t)s.row0 * K);
+#pragma unroll
+        for (int j = 0; j < kWLoads; ++j) {
+            const int r = 8 * (wave + 8 * j) + (lane >> 3);
+            woff[j] = (uint32_t)min(GATED ? r & 127 : r, N - 1 - n0) * (uint32_t)K + 16 * piece;
+        }
+#pragma unroll
+        for (int j = 0; j < kXLoads; ++j) {
+            const int r = (8 * (wave + 8 * j) + (lane >> 3)) % BM;
+            xoff[j] = (uint32_t)min(r, last) * (uint32_t)K + 16 * piece;
+        }
+        // waves 0 .. 3 fetch x's scales, the others W's: of its two halves, or of gate and up
+        if (wave < 4) {
+            s_rsrc = buffer_from(a.x_scale + (size_t)s.row0 * KB);
+            soff = 4u * (uint32_t)min((64 * wave + lane) % BM, last) * (uint32_t)KB;
+        } else {
+            const int nb = n0 / kBlock, other = GATED ? NB : BN > 128 ? min(nb + 1, NB - 1) - nb : 0;
+            s_rsrc = buffer_from(a.w_scale + ((size_t)s.e * M * NB + nb) * (size_t)KB);
+            soff = 4u * (uint32_t)((lane & 1) * other) * (uint32_t)KB;
+        }
+    };
+    // The next block into the stage at `at` (the second half of a half block is its first
+    // again); false: there is none.
+    auto load = [&](uint32_t at) {
+        if (l_id >= end) return;
+        const uint32_t back = half && l_b == KB - 1 && piece >= 4 ? 64u : 0u;
         const uint32_t to = lds0 + at + 1024u * (uint32_t)wave;
 #pragma unroll
         for (int j = 0; j < kWLoads; ++j)
-            load16_lds(GATED && j >= kWLoads / 2 ? up_rsrc : w_rsrc, woff[j] - back, b * kBlock, to + 8192u * j);
+            load16_lds(GATED && j >= kWLoads / 2 ? up_rsrc : w_rsrc, woff[j] - back, l_b * kBlock, to + 8192u * j);
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j)
-            load16_lds(x_rsrc, xoff[j] - back, b * kBlock,
+            load16_lds(x_rsrc, xoff[j] - back, l_b * kBlock,
                        lds0 + at + kX + (1024u * (uint32_t)(wave + 8 * j)) % (uint32_t)(BM * kBlock));
-        load4_lds(s_rsrc, soff, 4 * b, lds0 + at + kXs + (256u * (uint32_t)wave) % (uint32_t)kScales);
+        load4_lds(s_rsrc, soff, 4 * l_b,
+                  lds0 + at + (wave < 4 ? kXs + (256u * (uint32_t)wave) % (uint32_t)(kWs - kXs) : (uint32_t)kWs));
+        if (++l_b == KB) {
+            l_b = 0;
+            l_id += per_xcd;
+            if (l_id < end) enter(l_id);
+        }
     };
 
-    f32x4 acc[MT][NT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int i = 0; i < NT; ++i) acc[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    // row of W in the stage of this wave's tile i, and its half
+    // row of W in a stage of this wave's tile i
     auto w_row = [&](int i) {
         if (!GATED) return (wn * NT + i) * 16;
         return (i < NT / 2 ? 0 : 128) + (wn * (NT / 2) + i % (NT / 2)) * 16;
     };
-    auto compute = [&](uint32_t at, int b) {
+    // first row of this wave's 16 tokens t
+    auto x_row = [&](int t) { return INTER ? 16 * (t * WM + wm) : 16 * (wm * MT + t); };
+    f32x4 acc[MT][NT];
+    // The block in the stage at `at`, for the first TL of this wave's 16-token tiles.  The
+    // operands of 16 tokens are read while those of the 16 before are multiplied, whose sums are
+    // added one turn later still.
+    auto compute = [&](auto live, uint32_t at, float part) {
+        constexpr int TL = decltype(live)::value;
+        using Op = typename TileOperand<E4M3>::type;
         const unsigned char* buf = lds + at;
-        const int lo = ((2 * g) ^ (c & 7)) << 4, hi = ((2 * g + 1) ^ (c & 7)) << 4;
-        typename TileOperand<E4M3>::type w[NT];
+        const int lo = (g ^ (c & 7)) << 4, hi = ((g + 4) ^ (c & 7)) << 4;  // pieces g and g + 4
+        Op w[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const unsigned char* p = buf + (w_row(i) + c) * kBlock;
-            const u32x4 u = *(const u32x4*)(p + lo), v = *(const u32x4*)(p + hi);
-            if constexpr (E4M3) w[i] = i32x8{(int)u[0], (int)u[1], (int)u[2], (int)u[3], (int)v[0], (int)v[1], (int)v[2], (int)v[3]};
-            else w[i] = operand(u, v);
+            w[i] = tile_operand<E4M3>(*(const u32x4*)(p + lo), *(const u32x4*)(p + hi));
         }
+        const float* wsc = (const float*)(buf + kWs);
         float ws[M];
-        ws[0] = s_ws[!GATED && wn * NT * 16 >= 128 ? 1 : 0][b];
-        if constexpr (GATED) ws[1] = s_ws[1][b];
+        ws[0] = wsc[!GATED && wn * NT * 16 >= 128 ? 1 : 0] * part;
+        if constexpr (GATED) ws[1] = wsc[1] * part;
+        u32x4 u, v;
+        float xs;
+        auto fetch = [&](int t) {
+            const int r = x_row(t) + c;
+            const unsigned char* p = buf + kX + r * kBlock;
+            u = *(const u32x4*)(p + lo);
+            v = *(const u32x4*)(p + hi);
+            xs = *(const float*)(buf + kXs + 4 * r);
+        };
+        f32x4 d[2][NT];
+        float f[2][M];
+        auto add = [&](int t) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const int r = wm * MT * 16 + 16 * t;
-            if (MAPPED && r >= s.n) break;  // (the same for the whole wave)
-            const unsigned char* p = buf + kX + (r + c) * kBlock;
-            const u32x4 u = *(const u32x4*)(p + lo), v = *(const u32x4*)(p + hi);
-            const float xs = *(const float*)(buf + kXs + 4 * (r + c));
-            float f[M];
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int m = 0; m < M; ++m) f[m] = xs * ws[m];
-            if constexpr (E4M3) {
-                const i32x8 x = {(int)u[0], (int)u[1], (int)u[2], (int)u[3], (int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+                for (int q = 0; q < 4; ++q)
+                    acc[t][i][q] = __builtin_fmaf(d[t & 1][i][q], f[t & 1][GATED && i >= NT / 2 ? M - 1 : 0], acc[t][i][q]);
+        };
+        fetch(0);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    // formats 0 (e4m3); scales 0 select the instruction without block exponents
-                    const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        w[i], x, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+        for (int t = 0; t < TL; ++t) {
+            const Op x = tile_operand<E4M3>(u, v);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[t][i][q] = __builtin_fmaf(d[q], f[GATED && i >= NT / 2 ? M - 1 : 0], acc[t][i][q]);
+            for (int m = 0; m < M; ++m) f[t & 1][m] = xs * ws[m];
+            if (t + 1 < TL) fetch(t + 1);
+            tile_products(d[t & 1], w, x);
+            if (t > 0) add(t - 1);
+            if (t + 1 == TL) add(t);
+        }
+        // matrix instructions with the vector ones of the next and the last turn between them
+        constexpr int kMfma = TL * NT * (E4M3 ? 1 : 4);
+#pragma unroll
+        for (int i = 0; i < kMfma; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x2, E4M3 ? 4 : 3, 0);
+        }
+    };
+    // Expert-sorted rows: tiles are seldom full, and 16 rows that are not there are left out.
+    auto compute_live = [&](uint32_t at, int n, float part) {
+        if (!MAPPED || x_row(MT - 1) < n) compute(Int<MT>{}, at, part);
+        else if (MT > 3 && x_row(2) < n) compute(Int<(MT > 3 ? 3 : 1)>{}, at, part);
+        else if (MT > 2 && x_row(1) < n) compute(Int<(MT > 2 ? 2 : 1)>{}, at, part);
+        else if (MT > 1 && x_row(0) < n) compute(Int<1>{}, at, part);
+    };
+    auto store = [&](const RowSpan& s, int nt) {
+        const int n0 = nt * kCols;
+        if constexpr (!GATED) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const int r = x_row(t) + c;
+                if (r >= s.n) continue;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) store4(a, (size_t)s.row0 + r, n0 + w_row(i) + 4 * g, acc[t][i]);
+            }
+        } else {
+            constexpr int H = NT / 2;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const bool live = n0 + w_row(i) < N;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        acc[t][i][q] = silu(acc[t][i][q]) * acc[t][i + H][q];
+                        if (live) m = max_magnitude(m, acc[t][i][q]);
+                    }
                 }
-            } else {
-                const Operand x = operand(u, v);
+                m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+                m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+                if (g == 0) amax[wn][x_row(t) + c] = m;
+            }
+            // (the next tile's first barrier lies between these reads and its writes)
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const f32x4 d = block_product(w[i], x);
+            for (int t = 0; t < MT; ++t) {
+                const int r = x_row(t) + c;
+                if (r >= s.n) continue;
+                uint32_t m = 0;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[t][i][q] = __builtin_fmaf(d[q], f[GATED && i >= NT / 2 ? M - 1 : 0], acc[t][i][q]);
+                for (int j = 0; j < WN; ++j) m = max(m, amax[j][r]);
+                const size_t row = (size_t)s.row0 + r;
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const int o = n0 + w_row(i) + 4 * g;
+                    float h[4] = {acc[t][i][0], acc[t][i][1], acc[t][i][2], acc[t][i][3]}, scale;
+                    uint32_t codes[1];
+                    e4m3_codes<4>(h, __uint_as_float(m), &scale, codes);
+                    if (o < N) *(uint32_t*)((uint8_t*)a.y + row * (size_t)N + o) = codes[0];
+                    if (i == 0 && wn == 0 && g == 0) a.y_scale[row * (size_t)NB + nt] = scale;
                 }
             }
         }
     };
-    // Every tile begins with another block of columns: W's rows lie a power of two apart, and
-    // tiles in step would read the same few memory channels.
-    const int turn = ROTATE ? (nt + s.e) % KB : 0;
-    auto block = [&](int i) { return ROTATE ? (i + turn < KB ? i + turn : i + turn - KB) : i; };
-#pragma unroll
-    for (int j = 0; j < S - 1; ++j)
-        if (j < KB) load(j * kStage, block(j));
-    {
-        const int h = tid >> 6;
-        if (h < 2 && lane < KB) {
-            const int nb = GATED ? n0 / kBlock : min(n0 / kBlock + h * (BN > 128 ? 1 : 0), NB - 1);
-            const float ws = a.w_scale[(((size_t)s.e * M + (GATED ? h : 0)) * NB + nb) * (size_t)KB + lane];
-            s_ws[h][lane] = half && lane == KB - 1 ? 0.5f * ws : ws;
-        }
-    }
-    // Step i: wait for its block's loads (those of the next S - 2 blocks stay in flight), start
-    // those of block i + S - 1 into the stage that every wave has left, multiply.
-    uint32_t here = 0;
-    for (int i = 0; i < KB; ++i) {
-        if (S > 3 && i + 2 < KB) wait_loads<(S > 3 ? 2 * kLoads : 0)>();
-        else if (S > 2 && i + 1 < KB) wait_loads<(S > 2 ? kLoads : 0)>();
-        else wait_loads<0>();
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (s_ws, once)
-        __builtin_amdgcn_s_barrier();
-        const uint32_t free_at = here == 0 ? (S - 1) * kStage : here - kStage;
-        if (i + S - 1 < KB) load(free_at, block(i + S - 1));
-        compute(here, block(i));
-        here = here == (S - 1) * kStage ? 0 : here + kStage;
-    }
 
-    if constexpr (!GATED) {
+    enter(first);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const int r = wm * MT * 16 + 16 * t + c;
-            if (r >= s.n) continue;
+    for (int j = 0; j < S - 1; ++j) load(j * kStage);
+    int left = ((end - first + per_xcd - 1) / per_xcd) * KB;  // blocks still to multiply
+    uint32_t here = 0;
+    for (int id = first; id < end; id += per_xcd) {
+        int nt;
+        const RowSpan s = tile(id, &nt);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) store4(a, (size_t)s.row0 + r, n0 + w_row(i) + 4 * g, acc[t][i]);
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) acc[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        // Per block: wait for its loads (those of the next S - 2 blocks stay in flight; stores
+        // that are under way only make the wait longer), start those of the block S - 1 ahead
+        // into the stage that every wave has left, multiply.
+        for (int b = 0; b < KB; ++b) {
+            if (S > 3 && left > 2) wait_loads<(S > 3 ? 2 * kLoads : 0)>();
+            else if (S > 2 && left > 1) wait_loads<(S > 2 ? kLoads : 0)>();
+            else wait_loads<0>();
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            load(here == 0 ? (S - 1) * kStage : here - kStage);
+            compute_live(here, s.n, half && b == KB - 1 ? 0.5f : 1.0f);
+            here = here == (S - 1) * kStage ? 0 : here + kStage;
+            --left;
         }
-    } else {
-        constexpr int H = NT / 2;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const bool live = n0 + w_row(i) < N;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    acc[t][i][q] = silu(acc[t][i][q]) * acc[t][i + H][q];
-                    if (live) m = max_magnitude(m, acc[t][i][q]);
-                }
-            }
-            m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-            m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-            if (g == 0) amax[wn][wm * MT * 16 + 16 * t + c] = m;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const int r = wm * MT * 16 + 16 * t + c;
-            if (r >= s.n) continue;
-            uint32_t m = 0;
-#pragma unroll
-            for (int j = 0; j < WN; ++j) m = max(m, amax[j][r]);
-            const size_t row = (size_t)s.row0 + r;
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const int o = n0 + w_row(i) + 4 * g;
-                float h[4] = {acc[t][i][0], acc[t][i][1], acc[t][i][2], acc[t][i][3]}, scale;
-                uint32_t codes[1];
-                e4m3_codes<4>(h, __uint_as_float(m), &scale, codes);
-                if (o < N) *(uint32_t*)((uint8_t*)a.y + row * (size_t)N + o) = codes[0];
-                if (i == 0 && wn == 0 && g == 0) a.y_scale[row * (size_t)NB + nt] = scale;
-            }
-        }
+        store(s, nt);
     }
 }
 
-template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAPPED, bool ROTATE>
+template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAPPED>
 void launch_tile(const ProductArgs& a, int tiles, hipStream_t s) {
     constexpr int kCols = GATED ? BN / 2 : BN;
-    const unsigned grid = (unsigned)tiles * (unsigned)((a.N + kCols - 1) / kCols);
-    product_tile_kernel<BM, BN, WM, WN, S, E4M3, GATED, MAPPED, ROTATE><<<grid, kTileThreads, 0, s>>>(a);
+    const long long all = (long long)tiles * ((a.N + kCols - 1) / kCols);
+    const unsigned grid = (unsigned)(all < kGrid ? (all + 7) / 8 * 8 : kGrid);  // (some for every XCD)
+    product_tile_kernel<BM, BN, WM, WN, S, E4M3, GATED, MAPPED><<<grid, kTileThreads, 0, s>>>(a);
 }
 
 // Rows of a tile map of BM-row tiles (dense: the rows themselves).
@@ -525,33 +605,32 @@ hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
     if (a.map) {
         if (per <= 16) {
             const int tiles = tiles_of<32>(a);
-            if (a.gated) launch_tile<32, 256, 1, 8, 4, false, true, true, true>(a, tiles, s);
-            else if (wgs256 >= 128) launch_tile<32, 256, 1, 8, 4, false, false, true, true>(a, tiles, s);
+            if (a.gated) launch_tile<32, 256, 1, 8, 4, false, true, true>(a, tiles, s);
+            else if (wgs256 >= 128) launch_tile<32, 256, 1, 8, 4, false, false, true>(a, tiles, s);
             else launch_split<2, 4, false>(a, tiles, s);
         } else if (a.gated) {
-            launch_tile<128, 256, 2, 4, 3, false, true, true, true>(a, tiles_of<128>(a), s);
+            launch_tile<128, 256, 2, 4, 3, false, true, true>(a, tiles_of<128>(a), s);
         } else {
-            launch_tile<128, 256, 2, 4, 3, false, false, true, true>(a, tiles_of<128>(a), s);
+            launch_tile<128, 256, 2, 4, 3, false, false, true>(a, tiles_of<128>(a), s);
         }
     } else if (per <= 16) {
         const int tiles = tiles_of<32>(a);
         if (a.gated) launch_split<1, 2, true>(a, tiles_of<16>(a), s);
-        else if (wgs256 >= 128) launch_tile<32, 256, 1, 8, 4, false, false, false, true>(a, tiles, s);
+        else if (wgs256 >= 128) launch_tile<32, 256, 1, 8, 4, false, false, false>(a, tiles, s);
         else if (a.N < 4096) launch_split<1, 16, false>(a, tiles_of<16>(a), s);
         else launch_split<1, 8, false>(a, tiles_of<16>(a), s);
     } else if (a.gated) {
-        if (a.rows >= 2048) launch_tile<256, 256, 2, 4, 2, false, true, false, false>(a, tiles_of<256>(a), s);
-        else if (a.rows <= 64) launch_tile<64, 256, 2, 4, 3, false, true, false, true>(a, tiles_of<64>(a), s);
-        else launch_tile<128, 256, 2, 4, 3, false, true, false, false>(a, tiles_of<128>(a), s);
+        if (a.rows <= 64) launch_tile<64, 256, 2, 4, 3, false, true, false>(a, tiles_of<64>(a), s);
+        else launch_tile<128, 256, 2, 4, 3, false, true, false>(a, tiles_of<128>(a), s);
     } else {
         const bool wide = (long long)((a.N + 255) / 256) * ((a.rows + 255) / 256) >= 256;
         if (wide) {
-            if (a.out_bf16) launch_tile<256, 256, 2, 4, 2, true, false, false, false>(a, tiles_of<256>(a), s);
-            else launch_tile<256, 256, 2, 4, 2, false, false, false, false>(a, tiles_of<256>(a), s);
+            if (a.out_bf16) launch_tile<256, 256, 2, 4, 2, true, false, false>(a, tiles_of<256>(a), s);
+            else launch_tile<128, 256, 2, 4, 3, false, false, false>(a, tiles_of<128>(a), s);
         } else if (a.rows <= 64) {
-            launch_tile<64, 128, 2, 4, 3, false, false, false, true>(a, tiles_of<64>(a), s);
+            launch_tile<64, 128, 2, 4, 3, false, false, false>(a, tiles_of<64>(a), s);
         } else {
-            launch_tile<128, 128, 2, 4, 3, false, false, false, false>(a, tiles_of<128>(a), s);
+            launch_tile<128, 128, 2, 4, 3, false, false, false>(a, tiles_of<128>(a), s);
         }
     }
     trace_point(s);
