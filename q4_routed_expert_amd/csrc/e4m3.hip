@@ -243,9 +243,9 @@ void launch_split(const ProductArgs& a, int tiles, hipStream_t s) {
 // next: the loads of the next tile are under way while the last blocks of this one are
 // multiplied and its outputs are stored.
 //
-// LDS holds a row of a stage as eight 16-byte pieces, piece c at place c ^ (row & 7): the
-// loads write LDS in lane order, so a lane fetches the piece that belongs at its place, and
-// sixteen lanes that read the same piece of sixteen rows meet all banks.
+// LDS holds a row of a stage as eight 16-byte pieces, piece p at place p ^ (row & 7): the
+// loads write LDS in lane order, so a lane fetches the piece that belongs at its place.  A lane
+// of group g multiplies pieces g and g + 4 (with 2 g and 2 g + 1, half of the reads met in a bank).
 // ---------------------------------------------------------------------------
 constexpr int kTileThreads = 512;
 constexpr int kGrid = 256;  // CUs
@@ -477,13 +477,6 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const Produc
             tile_products(d[t & 1], w, x);
             if (t > 0) add(t - 1);
             if (t + 1 == TL) add(t);
-        }
-        // matrix instructions with the vector ones of the next and the last turn between them
-        constexpr int kMfma = TL * NT * (E4M3 ? 1 : 4);
-#pragma unroll
-        for (int i = 0; i < kMfma; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x2, E4M3 ? 4 : 3, 0);
         }
     };
     // Expert-sorted rows: tiles are seldom full, and 16 rows that are not there are left out.
