@@ -13,7 +13,7 @@ __device__ __forceinline__ uint32_t max_magnitude(uint32_t m, float v) {
     return m > u ? m : u;
 }
 
-// Codes of N values (4 or 8) of a group whose largest magnitude is amax, and the group's scale:
+// Codes of N values (4, 8, ...) of a group whose largest magnitude is amax, and the group's scale:
 // scale = amax / 448 and codes of y / scale, both correctly rounded quotients.
 template <int N>
 __device__ __forceinline__ void e4m3_codes(const float (&y)[N], float amax, float* scale_out, uint32_t (&codes)[N / 4]) {

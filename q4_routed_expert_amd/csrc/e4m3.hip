@@ -486,20 +486,39 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const Produc
         else if (MT > 2 && x_row(1) < n) compute(Int<(MT > 2 ? 2 : 1)>{}, at, part);
         else if (MT > 1 && x_row(0) < n) compute(Int<1>{}, at, part);
     };
+    // A tile's outputs (16 rows that are not there are left out, the same for the whole wave).
     auto store = [&](const RowSpan& s, int nt) {
         const int n0 = nt * kCols;
         if constexpr (!GATED) {
+            const bool pairs = NT > 1 && a.out_bf16 && (N & 7) == 0;
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
+                if (x_row(t) >= s.n) break;
                 const int r = x_row(t) + c;
-                if (r >= s.n) continue;
+                const size_t row = (size_t)s.row0 + r;
+                if (pairs) {
+                    // Two tiles of columns at once: rows of lanes trade halves, so that a lane has eight
+                    // neighbours, and the four lanes of a token 64 bytes.
 #pragma unroll
-                for (int i = 0; i < NT; ++i) store4(a, (size_t)s.row0 + r, n0 + w_row(i) + 4 * g, acc[t][i]);
+                    for (int i = 0; i + 1 < NT; i += 2) {
+                        const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16x2(acc[t][i][0], acc[t][i][1]),
+                                                                         pack_bf16x2(acc[t][i + 1][0], acc[t][i + 1][1]), false, false);
+                        const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16x2(acc[t][i][2], acc[t][i][3]),
+                                                                         pack_bf16x2(acc[t][i + 1][2], acc[t][i + 1][3]), false, false);
+                        const int o = n0 + w_row(i) + 16 * (g & 1) + 8 * (g >> 1);
+                        if (r < s.n && o < N)
+                            *(u32x4*)((uint16_t*)a.y + row * (size_t)N + o) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+                    }
+                } else if (r < s.n) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) store4(a, row, n0 + w_row(i) + 4 * g, acc[t][i]);
+                }
             }
         } else {
             constexpr int H = NT / 2;
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
+                if (x_row(t) >= s.n) break;
                 uint32_t m = 0;
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
@@ -520,21 +539,24 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const Produc
             asm volatile("" ::: "memory");
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
+                if (x_row(t) >= s.n) break;
                 const int r = x_row(t) + c;
-                if (r >= s.n) continue;
                 uint32_t m = 0;
 #pragma unroll
                 for (int j = 0; j < WN; ++j) m = max(m, amax[j][r]);
                 const size_t row = (size_t)s.row0 + r;
+                float h[4 * H], scale;
+                uint32_t codes[H];
+#pragma unroll
+                for (int i = 0; i < 4 * H; ++i) h[i] = acc[t][i / 4][i % 4];
+                e4m3_codes<4 * H>(h, __uint_as_float(m), &scale, codes);
+                if (r >= s.n) continue;
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     const int o = n0 + w_row(i) + 4 * g;
-                    float h[4] = {acc[t][i][0], acc[t][i][1], acc[t][i][2], acc[t][i][3]}, scale;
-                    uint32_t codes[1];
-                    e4m3_codes<4>(h, __uint_as_float(m), &scale, codes);
-                    if (o < N) *(uint32_t*)((uint8_t*)a.y + row * (size_t)N + o) = codes[0];
-                    if (i == 0 && wn == 0 && g == 0) a.y_scale[row * (size_t)NB + nt] = scale;
+                    if (o < N) *(uint32_t*)((uint8_t*)a.y + row * (size_t)N + o) = codes[i];
                 }
+                if (wn == 0 && g == 0) a.y_scale[row * (size_t)NB + nt] = scale;
             }
         }
     };
@@ -604,7 +626,8 @@ hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
         } else if (a.gated) {
             launch_tile<128, 256, 2, 4, 3, false, true, true>(a, tiles_of<128>(a), s);
         } else {
-            launch_tile<128, 256, 2, 4, 3, false, false, true>(a, tiles_of<128>(a), s);
+            if (a.out_bf16) launch_tile<128, 256, 2, 4, 3, true, false, true>(a, tiles_of<128>(a), s);
+            else launch_tile<128, 256, 2, 4, 3, false, false, true>(a, tiles_of<128>(a), s);
         }
     } else if (per <= 16) {
         const int tiles = tiles_of<32>(a);
