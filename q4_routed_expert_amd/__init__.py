@@ -77,6 +77,8 @@ def _need(t, name: str, dtype, n: int):
     """The C ABI sees only pointers, so the binding checks what the kernels will
     touch: a contiguous tensor of `dtype` with at least n elements (and, through
     _on_gpu, in device memory)."""
+    if t is not None and t.dtype is dtype and t.numel() >= n and t.is_contiguous():
+        return
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype != dtype:
@@ -414,14 +416,14 @@ def lm_argmax(lm: DeviceLmHead, x: torch.Tensor | None, ws: torch.Tensor,
     return logits, token, x_next
 
 
-# The current stream's handle without building a stream object (2.5 us of a call).
+# The current stream's handle without building a stream object (2.5 us of a call), and the
+# current device without asking whether the GPU is initialised (its tensors are at hand).
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _launch_on(where: str, **tensors) -> int:
-    """The current stream's handle for a call whose tensors are `tensors` (None: absent).
-    All of them have to be on one GPU, and that GPU has to be the current one, because
-    the library launches on the current device."""
+def _not_on_one_gpu(where: str, tensors: dict):
+    """The error of _launch_on for tensors that are not all on one GPU."""
     dev = -1
     for name, t in tensors.items():
         if t is None:
@@ -429,11 +431,24 @@ def _launch_on(where: str, **tensors) -> int:
         d = t.get_device()
         if d < 0:
             raise ValueError(f"{name} must be on the GPU")
-        if dev < 0:
-            dev = d
-        elif d != dev:
+        if dev >= 0 and d != dev:
             raise ValueError(f"{where}: {name} is on cuda:{d}, other arguments on cuda:{dev}")
-    if dev != torch.cuda.current_device():
+        dev = d
+
+
+def _launch_on(where: str, **tensors) -> int:
+    """The current stream's handle for a call whose tensors are `tensors` (None: absent).
+    All of them have to be on one GPU, and that GPU has to be the current one, because
+    the library launches on the current device."""
+    dev = -1
+    for t in tensors.values():
+        if t is not None:
+            d = t.get_device()
+            if d != dev or d < 0:
+                if d < 0 or dev >= 0:
+                    _not_on_one_gpu(where, tensors)
+                dev = d
+    if dev != _current_device():
         raise ValueError(f"{where}: the tensors are on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     return _raw_stream(dev)
@@ -606,31 +621,34 @@ def quantize_blocks(w: torch.Tensor):
 def _product(where, w, w_scale, x, x_scale, lead, rows, out_dtype, gated, y, y_scale):
     """Checks and outputs shared by the 8-bit products: the C call's matrix, N (both parts
     of a gated matrix), K, flags, y, y_scale."""
-    lead = lead + (2,) if gated else lead
-    if x.dim() != 2 or w.dim() != len(lead) + 2 or tuple(w.shape[:-2]) != lead:
+    if gated:
+        lead, out_dtype = lead + (2,), torch.float8_e4m3fn
+    elif out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, not {out_dtype}")
+    shape = w.shape
+    if x.dim() != 2 or len(shape) != len(lead) + 2 or shape[:-2] != lead:
         raise ValueError(f"{where}: x must be [rows, K] and w {[*lead, 'N', 'K']}, not "
-                         f"{tuple(x.shape)}, {tuple(w.shape)}")
-    N, K = w.shape[-2:]
+                         f"{tuple(x.shape)}, {tuple(shape)}")
+    N, K = shape[-2:]
     if x.shape[1] != K:
         raise ValueError(f"{where}: w has {K} columns, x has {x.shape[1]}")
-    if gated:
-        out_dtype = torch.float8_e4m3fn
-    elif out_dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, not {out_dtype}")
+    kb, nb = (K + 127) >> 7, (N + 127) >> 7
     mats = 1
     for n in lead:
         mats *= n
     _need(x, "x", torch.float8_e4m3fn, rows * K)
-    _need(x_scale, "x_scale", torch.float32, rows * _blocks(K))
+    _need(x_scale, "x_scale", torch.float32, rows * kb)
     _need(w, "w", torch.float8_e4m3fn, mats * N * K)
-    _need(w_scale, "w_scale", torch.float32, mats * _blocks(N) * _blocks(K))
+    _need(w_scale, "w_scale", torch.float32, mats * nb * kb)
     if y is None:
         y = x.new_empty((rows, N), dtype=out_dtype)
-    _need(y, "y", out_dtype, rows * N)
+    else:
+        _need(y, "y", out_dtype, rows * N)
     if gated:
         if y_scale is None:
-            y_scale = x_scale.new_empty((rows, _blocks(N)))
-        _need(y_scale, "y_scale", torch.float32, rows * _blocks(N))
+            y_scale = x_scale.new_empty((rows, nb))
+        else:
+            _need(y_scale, "y_scale", torch.float32, rows * nb)
     elif y_scale is not None:
         raise ValueError("y_scale is of gated products")
     flags = (_abi.MOE_GATED if gated else
@@ -768,6 +786,18 @@ def combine_grad(dy: torch.Tensor, rows: torch.Tensor, routing: DeviceRouting,
     return d_rows, d_w
 
 
+def _addr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _per_row(v, name: str, B: int):
+    """(tensor or None, number) of a parameter that is one number or a tensor [B]."""
+    if isinstance(v, torch.Tensor):
+        _need(v, name, torch.float32, B)
+        return v, 0.0
+    return None, v
+
+
 def penalize(logits: torch.Tensor, tokens: torch.Tensor | None = None,
              n_tokens: torch.Tensor | None = None, n_prompt: torch.Tensor | None = None,
              repetition=1.0, frequency=0.0, presence=0.0, bias_ids: torch.Tensor | None = None,
@@ -786,27 +816,19 @@ def penalize(logits: torch.Tensor, tokens: torch.Tensor | None = None,
         raise ValueError(f"logits must be [B, V], not {tuple(logits.shape)}")
     B, V = logits.shape
     _need(logits, "logits", torch.float32, B * V)
-    p = _abi.Penalties()
-    given = {}
+    stride = n_bias = 0
     if tokens is not None:
         if tokens.dim() != 2 or tokens.shape[0] != B:
             raise ValueError(f"tokens must be [{B}, L], not {tuple(tokens.shape)}")
         _need(tokens, "tokens", torch.int32, 0)
-        p.stride = tokens.shape[1]
-        # (without a column there is nothing to point at)
-        given["tokens"] = tokens if p.stride else None
+        stride = tokens.shape[1]
     for name, t in (("n_tokens", n_tokens), ("n_prompt", n_prompt)):
         if t is not None:
             if tokens is None:
                 raise ValueError(f"{name} needs tokens")
             _need(t, name, torch.int32, B)
-            given[name] = t if p.stride else None
-    for name, v in (("repetition", repetition), ("frequency", frequency), ("presence", presence)):
-        if isinstance(v, torch.Tensor):
-            _need(v, name, torch.float32, B)
-            given[name] = v
-        else:
-            setattr(p, name + "_all", v)
+    if tokens is not None and stride == 0:  # nothing to point at
+        tokens = n_tokens = n_prompt = None
     if (bias_ids is None) != (bias is None):
         raise ValueError("bias_ids and bias come together")
     if bias is not None:
@@ -815,21 +837,28 @@ def penalize(logits: torch.Tensor, tokens: torch.Tensor | None = None,
                              f"{tuple(bias.shape)}")
         _need(bias_ids, "bias_ids", torch.int32, 0)
         _need(bias, "bias", torch.float32, 0)
-        p.n_bias = bias.shape[1]
-        if p.n_bias:
-            given["bias_ids"], given["bias"] = bias_ids, bias
+        n_bias = bias.shape[1]
+        if n_bias == 0:
+            bias_ids = bias = None
     if mask is not None:
-        if mask.dim() != 2 or tuple(mask.shape) != (B, -(-V // 32)):
-            raise ValueError(f"mask must be [{B}, {-(-V // 32)}], not {tuple(mask.shape)}")
+        if mask.dim() != 2 or tuple(mask.shape) != (B, (V + 31) >> 5):
+            raise ValueError(f"mask must be [{B}, {(V + 31) >> 5}], not {tuple(mask.shape)}")
         _need(mask, "mask", torch.int32, 0)
-        given["mask"] = mask
+    rep, rep_all = _per_row(repetition, "repetition", B)
+    freq, freq_all = _per_row(frequency, "frequency", B)
+    pres, pres_all = _per_row(presence, "presence", B)
     if out is None:
         out = torch.empty_like(logits)
-    _need(out, "out", torch.float32, B * V)
-    s = _launch_on("penalize", logits=logits, out=out, **given)
-    for name, t in given.items():
-        setattr(p, name, _ptr(t))
-    _check(_abi.lib().moe_penalize(_ptr(logits), B, V, C.addressof(p), _ptr(out), s), "moe_penalize")
+    else:
+        _need(out, "out", torch.float32, B * V)
+    s = _launch_on("penalize", logits=logits, out=out, tokens=tokens, n_tokens=n_tokens,
+                   n_prompt=n_prompt, repetition=rep, frequency=freq, presence=pres,
+                   bias_ids=bias_ids, bias=bias, mask=mask)
+    # (the struct's bytes: building a ctypes structure of 14 fields costs 2 us)
+    p = _abi.PENALTIES(_addr(tokens), _addr(n_tokens), _addr(n_prompt), _addr(rep), _addr(freq),
+                       _addr(pres), _addr(bias_ids), _addr(bias), _addr(mask), stride, n_bias,
+                       rep_all, freq_all, pres_all)
+    _check(_abi.lib().moe_penalize(_ptr(logits), B, V, p, _ptr(out), s), "moe_penalize")
     return out
 
 

@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libq4moe.so")
 
@@ -75,6 +76,10 @@ class Penalties(C.Structure):
                                           "frequency", "presence", "bias_ids", "bias", "mask")] + [
         ("stride", C.c_int32), ("n_bias", C.c_int32), ("repetition_all", C.c_float),
         ("frequency_all", C.c_float), ("presence_all", C.c_float)]
+
+
+# Penalties as bytes, the padding at its end included
+PENALTIES = struct.Struct("=9Q2i3f4x").pack
 
 
 class Routing(C.Structure):

@@ -127,6 +127,8 @@ def test_struct_sizes_and_limits_match_the_header():
                  "MOE_NORM_GROUP_128"):
         assert int(re.search(rf"#define {name} (\d+)", text).group(1)) == getattr(_abi, name), name
     assert C.sizeof(_abi.Penalties) == 9 * 8 + 5 * 4 + 4 and C.sizeof(_abi.E4m3Mat) == 16
+    v = (*range(1, 10), 10, 11, 1.5, 2.5, 3.5)
+    assert bytes(_abi.Penalties(*v)) == _abi.PENALTIES(*v)
 
 
 def test_product_binding_refuses():
