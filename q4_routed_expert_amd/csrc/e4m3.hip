@@ -86,14 +86,19 @@ __device__ __forceinline__ f32x4 block_product(const Operand& w, const Operand& 
     return d;
 }
 
+// Sixteen or eight bytes at a 2-byte address (one store: the hardware takes any alignment, and
+// rows of an odd number of columns begin anywhere).
+template <int N>
+struct __attribute__((packed, aligned(2))) Words {
+    uint32_t w[N];
+};
+
 // Four sums of one token, weight rows o .. o + 3.
 __device__ __forceinline__ void store4(const ProductArgs& a, size_t row, int o, const f32x4& v) {
     const size_t at = row * (size_t)a.N + o;
-    if (o + 4 <= a.N && (a.N & 3) == 0) {  // four neighbours, aligned
-        if (a.out_bf16)
-            *(uint2*)((uint16_t*)a.y + at) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        else
-            *(f32x4*)((float*)a.y + at) = v;
+    if (o + 4 <= a.N) {
+        if (a.out_bf16) *(Words<2>*)((uint16_t*)a.y + at) = Words<2>{{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}};
+        else *(Words<4>*)((float*)a.y + at) = __builtin_bit_cast(Words<4>, v);
         return;
     }
 #pragma unroll
@@ -102,6 +107,18 @@ __device__ __forceinline__ void store4(const ProductArgs& a, size_t row, int o, 
         if (a.out_bf16) ((uint16_t*)a.y)[at + i] = f32_to_bf16(v[i]);
         else ((float*)a.y)[at + i] = v[i];
     }
+}
+
+// Eight sums of one token in bf16, weight rows o .. o + 7.
+__device__ __forceinline__ void store8(const ProductArgs& a, size_t row, int o, const Words<4>& v) {
+    uint16_t* at = (uint16_t*)a.y + row * (size_t)a.N + o;
+    if (o + 8 <= a.N) {
+        *(Words<4>*)at = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (o + i < a.N) at[i] = (uint16_t)(v.w[i / 2] >> (16 * (i & 1)));
 }
 
 constexpr int kWaves = 16;
@@ -248,7 +265,7 @@ void launch_split(const ProductArgs& a, int tiles, hipStream_t s) {
 // of group g multiplies pieces g and g + 4 (with 2 g and 2 g + 1, half of the reads met in a bank).
 // ---------------------------------------------------------------------------
 constexpr int kTileThreads = 512;
-constexpr int kGrid = 256;  // CUs
+constexpr int kCus = 256;
 
 template <int N>
 struct Int {
@@ -490,7 +507,7 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const Produc
     auto store = [&](const RowSpan& s, int nt) {
         const int n0 = nt * kCols;
         if constexpr (!GATED) {
-            const bool pairs = NT > 1 && a.out_bf16 && (N & 7) == 0;
+            const bool pairs = NT > 1 && a.out_bf16;
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 if (x_row(t) >= s.n) break;
@@ -506,8 +523,7 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const Produc
                         const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16x2(acc[t][i][2], acc[t][i][3]),
                                                                          pack_bf16x2(acc[t][i + 1][2], acc[t][i + 1][3]), false, false);
                         const int o = n0 + w_row(i) + 16 * (g & 1) + 8 * (g >> 1);
-                        if (r < s.n && o < N)
-                            *(u32x4*)((uint16_t*)a.y + row * (size_t)N + o) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+                        if (r < s.n) store8(a, row, o, Words<4>{{lo[0], hi[0], lo[1], hi[1]}});
                     }
                 } else if (r < s.n) {
 #pragma unroll
@@ -595,6 +611,7 @@ template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAP
 void launch_tile(const ProductArgs& a, int tiles, hipStream_t s) {
     constexpr int kCols = GATED ? BN / 2 : BN;
     const long long all = (long long)tiles * ((a.N + kCols - 1) / kCols);
+    constexpr int kGrid = kCus * (BM <= 64 && BN <= 128 ? 2 : 1);  // (by their LDS)
     const unsigned grid = (unsigned)(all < kGrid ? (all + 7) / 8 * 8 : kGrid);  // (some for every XCD)
     product_tile_kernel<BM, BN, WM, WN, S, E4M3, GATED, MAPPED><<<grid, kTileThreads, 0, s>>>(a);
 }
@@ -639,14 +656,16 @@ hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
         if (a.rows <= 64) launch_tile<64, 256, 2, 4, 3, false, true, false>(a, tiles_of<64>(a), s);
         else launch_tile<128, 256, 2, 4, 3, false, true, false>(a, tiles_of<128>(a), s);
     } else {
-        const bool wide = (long long)((a.N + 255) / 256) * ((a.rows + 255) / 256) >= 256;
-        if (wide) {
+        auto tiles = [&](int m, int n) { return (long long)((a.rows + m - 1) / m) * ((a.N + n - 1) / n); };
+        if (tiles(256, 256) >= kCus) {
             if (a.out_bf16) launch_tile<256, 256, 2, 4, 2, true, false, false>(a, tiles_of<256>(a), s);
             else launch_tile<128, 256, 2, 4, 3, false, false, false>(a, tiles_of<128>(a), s);
-        } else if (a.rows <= 64) {
-            launch_tile<64, 128, 2, 4, 3, false, false, false>(a, tiles_of<64>(a), s);
+        } else if (tiles(128, 128) > kCus) {
+            if (a.out_bf16) launch_tile<128, 128, 2, 4, 3, true, false, false>(a, tiles_of<128>(a), s);
+            else launch_tile<128, 128, 2, 4, 3, false, false, false>(a, tiles_of<128>(a), s);
         } else {
-            launch_tile<128, 128, 2, 4, 3, false, false, false>(a, tiles_of<128>(a), s);
+            if (a.out_bf16) launch_tile<64, 128, 2, 4, 3, true, false, false>(a, tiles_of<64>(a), s);
+            else launch_tile<64, 128, 2, 4, 3, false, false, false>(a, tiles_of<64>(a), s);
         }
     }
     trace_point(s);
