@@ -79,13 +79,6 @@ __device__ __forceinline__ Operand operand(const u32x4& lo, const u32x4& hi) {
     return o;
 }
 
-__device__ __forceinline__ f32x4 block_product(const Operand& w, const Operand& x) {
-    f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[j], x.v[j], d, 0, 0, 0);
-    return d;
-}
-
 // Sixteen or eight bytes at a 2-byte address (one store: the hardware takes any alignment, and
 // rows of an odd number of columns begin anywhere).
 template <int N>
@@ -121,139 +114,69 @@ __device__ __forceinline__ void store8(const ProductArgs& a, size_t row, int o, 
         if (o + i < a.N) at[i] = (uint16_t)(v.w[i / 2] >> (16 * (i & 1)));
 }
 
+// ---------------------------------------------------------------------------
+// Few tokens and few weight rows: 16 weight rows and 16 TT tokens per work group, whose 16
+// waves share the blocks of columns (wave w takes w, w + 16, ...) and whose sums meet in LDS in
+// wave order.  Operands come straight from memory: with one wave a block there is one round
+// trip.
+// ---------------------------------------------------------------------------
 constexpr int kWaves = 16;
 
-// 16 TT tokens per work group; wave = (tile p, slice ks) of PT = kWaves / KS tiles of 16
-// weight rows (gated: 16 gate and 16 up rows); slice ks takes the blocks b = ks, ks + KS, ...
-// and the slices' sums meet in LDS in order.
-template <int TT, int KS, bool GATED>
+template <int TT>
 __global__ __launch_bounds__(kWaves * 64) void product_split_kernel(const ProductArgs a) {
-    constexpr int PT = kWaves / KS, M = GATED ? 2 : 1;
-    static_assert(!GATED || PT == 8, "a gated work group covers one 128-column output group");
-    __shared__ f32x4 red[KS > 1 ? KS - 1 : 1][PT][M][TT][64];
-    __shared__ uint32_t amax[GATED ? 8 : 1][TT * 16];
+    __shared__ f32x4 red[kWaves][TT][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int c = lane & 15, g = lane >> 4;
-    const int p = wave % PT, ks = wave / PT;
-    const int N = a.N, K = a.K, KB = (K + kBlock - 1) / kBlock, NB = (N + kBlock - 1) / kBlock;
-    if (a.map && (int)blockIdx.y >= mapped_tiles(a)) return;
-    const RowSpan s = span_of<16 * TT>(a, blockIdx.y);
-    if (s.n == 0) return;
-    const int n0 = (blockIdx.x * PT + p) * 16;  // first weight row of the wave's tile
-    const uint8_t* wrow[M];
-    const float* ws[M];
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-        const size_t mat = (size_t)s.e * M + m;
-        const int row = min(n0 + c, N - 1);  // clamped, valid
-        wrow[m] = a.w + (mat * N + row) * (size_t)K;
-        ws[m] = a.w_scale + (mat * NB + min(n0, N - 1) / kBlock) * (size_t)KB;
-    }
+    const int N = a.N, K = a.K, KB = (K + kBlock - 1) / kBlock;
+    const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 16 * TT;
+    const uint8_t* wrow = a.w + (size_t)min(n0 + c, N - 1) * K;  // (clamped rows are not stored)
+    const float* ws = a.w_scale + (size_t)(n0 / kBlock) * KB;
     const uint8_t* xrow[TT];
     const float* xs[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-        const size_t row = s.row0 + min(16 * t + c, s.n - 1);  // clamped, valid
+        const size_t row = min(t0 + 16 * t + c, a.rows - 1);
         xrow[t] = a.x + row * (size_t)K;
         xs[t] = a.x_scale + row * (size_t)KB;
     }
-    f32x4 acc[M][TT];
+    f32x4 acc[TT];
 #pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-        for (int t = 0; t < TT; ++t) acc[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (n0 < N) {
-        for (int b = ks; b < KB; b += KS) {
-            const int k0 = b * kBlock + 32 * g;
-            const int kk = k0 < K ? k0 : k0 - 64;
-            const float part = b == KB - 1 && (K & 64) ? 0.5f : 1.0f;
-            Operand w[M];
-#pragma unroll
-            for (int m = 0; m < M; ++m) {
-                const u32x4 lo = *(const u32x4*)(wrow[m] + kk), hi = *(const u32x4*)(wrow[m] + kk + 16);
-                w[m] = operand(lo, hi);
-            }
-#pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                const u32x4 lo = *(const u32x4*)(xrow[t] + kk), hi = *(const u32x4*)(xrow[t] + kk + 16);
-                const Operand x = operand(lo, hi);
-                const float xsc = xs[t][b] * part;
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    const f32x4 d = block_product(w[m], x);
-                    const float f = xsc * ws[m][b];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[m][t][i] = __builtin_fmaf(d[i], f, acc[m][t][i]);
-                }
-            }
-        }
-    }
-    if constexpr (KS > 1) {
-        if (ks > 0) {
-#pragma unroll
-            for (int m = 0; m < M; ++m)
-#pragma unroll
-                for (int t = 0; t < TT; ++t) red[ks - 1][p][m][t][lane] = acc[m][t];
-        }
-        __syncthreads();
-        if (ks == 0) {
-#pragma unroll
-            for (int m = 0; m < M; ++m)
-#pragma unroll
-                for (int t = 0; t < TT; ++t)
-                    for (int j = 0; j < KS - 1; ++j) acc[m][t] += red[j][p][m][t][lane];
-        }
-    }
-    const int o = n0 + 4 * g;
-    if constexpr (!GATED) {
-        if (ks > 0) return;
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-            if (16 * t + c < s.n) store4(a, (size_t)s.row0 + 16 * t + c, o, acc[0][t]);
-    } else {
-        float h[TT][4];
-        if (ks == 0) {
-#pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h[t][i] = silu(acc[0][t][i]) * acc[1][t][i];
-                    if (n0 < N) m = max_magnitude(m, h[t][i]);
-                }
-                m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-                m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-                if (g == 0) amax[p][16 * t + c] = m;
-            }
-        }
-        __syncthreads();
-        if (ks > 0 || n0 >= N) return;
-        const int groups = (N + kBlock - 1) / kBlock;
+    for (int t = 0; t < TT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = wave; b < KB; b += kWaves) {
+        const int k0 = b * kBlock + 32 * g;
+        const int kk = k0 < K ? k0 : k0 - 64;
+        const float f = ws[b] * (b == KB - 1 && (K & 64) ? 0.5f : 1.0f);
+        const Operand w = operand(*(const u32x4*)(wrow + kk), *(const u32x4*)(wrow + kk + 16));
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            uint32_t m = 0;
+            const Operand x = operand(*(const u32x4*)(xrow[t] + kk), *(const u32x4*)(xrow[t] + kk + 16));
+            const float ft = xs[t][b] * f;
+            f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = max(m, amax[j][16 * t + c]);
-            float scale;
-            uint32_t codes[1];
-            e4m3_codes<4>(h[t], __uint_as_float(m), &scale, codes);
-            if (16 * t + c >= s.n) continue;
-            const size_t row = (size_t)s.row0 + 16 * t + c;
-            *(uint32_t*)((uint8_t*)a.y + row * (size_t)N + o) = codes[0];
-            if (p == 0 && g == 0) a.y_scale[row * (size_t)groups + n0 / kBlock] = scale;
+            for (int j = 0; j < 4; ++j) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[j], x.v[j], d, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(d[i], ft, acc[t][i]);
         }
     }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) red[wave][t][lane] = acc[t];
+    __syncthreads();
+    if (wave >= TT) return;
+    f32x4 sum = red[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) sum += red[w][wave][lane];
+    const int row = t0 + 16 * wave + c;
+    if (row < a.rows) store4(a, row, n0 + 4 * g, sum);
 }
 
-template <int TT, int KS, bool GATED>
-void launch_split(const ProductArgs& a, int tiles, hipStream_t s) {
-    constexpr int PT = kWaves / KS;
-    const dim3 grid((a.N + 16 * PT - 1) / (16 * PT), tiles);
-    product_split_kernel<TT, KS, GATED><<<grid, kWaves * 64, 0, s>>>(a);
+template <int TT>
+void launch_split(const ProductArgs& a, hipStream_t s) {
+    const dim3 grid((a.N + 15) / 16, (a.rows + 16 * TT - 1) / (16 * TT));
+    product_split_kernel<TT><<<grid, kWaves * 64, 0, s>>>(a);
 }
 
 // ---------------------------------------------------------------------------
-// Tiles: BM tokens by BN weight rows per work group of 8 waves, WM x WN of them; x and W go
+// Tiles: BM tokens by BN weight rows per work group of WM x WN waves; x and W go
 // through LDS in S stages of one block of 128 columns each, loaded straight into it.
 //
 // One work group per CU walks its share of the tiles, and its stages run on from one tile to the
@@ -264,7 +187,6 @@ void launch_split(const ProductArgs& a, int tiles, hipStream_t s) {
 // loads write LDS in lane order, so a lane fetches the piece that belongs at its place.  A lane
 // of group g multiplies pieces g and g + 4 (with 2 g and 2 g + 1, half of the reads met in a bank).
 // ---------------------------------------------------------------------------
-constexpr int kTileThreads = 512;
 constexpr int kCus = 256;
 
 template <int N>
@@ -345,13 +267,14 @@ __device__ __forceinline__ void tile_products(f32x4 (&d)[NT], const i32x8 (&w)[N
 
 // E4M3: the matrix cores' own 8-bit products (see the top), for bf16 outputs.
 template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAPPED>
-__global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const ProductArgs a) {
-    static_assert(WM * WN == 8 && S >= 2 && S <= 4 && (!GATED || BN == 256) && (!MAPPED || BM / WM <= 64), "shape");
+__global__ __launch_bounds__(WM * WN * 64) void product_tile_kernel(const ProductArgs a) {
+    constexpr int kW = WM * WN;
+    static_assert((kW == 8 || kW == 16) && S >= 2 && S <= 4 && (!GATED || BN == 256) && (!MAPPED || BM / WM <= 64), "shape");
     constexpr int MT = BM / WM / 16, NT = BN / WN / 16, M = GATED ? 2 : 1;
     constexpr bool INTER = MAPPED;
     // a stage: W's rows, x's rows, x's scales (a load writes 256 bytes), the two scales of W
     constexpr int kX = BN * kBlock, kXs = kX + BM * kBlock, kWs = kXs + (BM < 64 ? 256 : 4 * BM), kStage = kWs + 256;
-    constexpr int kWLoads = BN / 64, kXLoads = (BM + 63) / 64, kLoads = kWLoads + kXLoads + 1;
+    constexpr int kWLoads = BN / (8 * kW), kXLoads = (BM + 8 * kW - 1) / (8 * kW), kLoads = kWLoads + kXLoads + 1;
     __shared__ __attribute__((aligned(16))) unsigned char lds[S * kStage];
     __shared__ uint32_t amax[GATED ? WN : 1][GATED ? BM : 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -400,12 +323,12 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const Produc
         x_rsrc = buffer_from(a.x + (size_t)s.row0 * K);
 #pragma unroll
         for (int j = 0; j < kWLoads; ++j) {
-            const int r = 8 * (wave + 8 * j) + (lane >> 3);
+            const int r = 8 * (wave + kW * j) + (lane >> 3);
             woff[j] = (uint32_t)min(GATED ? r & 127 : r, N - 1 - n0) * (uint32_t)K + 16 * piece;
         }
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j) {
-            const int r = (8 * (wave + 8 * j) + (lane >> 3)) % BM;
+            const int r = (8 * (wave + kW * j) + (lane >> 3)) % BM;
             xoff[j] = (uint32_t)min(r, last) * (uint32_t)K + 16 * piece;
         }
         // waves 0 .. 3 fetch x's scales, the others W's: of its two halves, or of gate and up
@@ -426,11 +349,11 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(const Produc
         const uint32_t to = lds0 + at + 1024u * (uint32_t)wave;
 #pragma unroll
         for (int j = 0; j < kWLoads; ++j)
-            load16_lds(GATED && j >= kWLoads / 2 ? up_rsrc : w_rsrc, woff[j] - back, l_b * kBlock, to + 8192u * j);
+            load16_lds(GATED && j >= kWLoads / 2 ? up_rsrc : w_rsrc, woff[j] - back, l_b * kBlock, to + 1024u * kW * j);
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j)
             load16_lds(x_rsrc, xoff[j] - back, l_b * kBlock,
-                       lds0 + at + kX + (1024u * (uint32_t)(wave + 8 * j)) % (uint32_t)(BM * kBlock));
+                       lds0 + at + kX + (1024u * (uint32_t)(wave + kW * j)) % (uint32_t)(BM * kBlock));
         load4_lds(s_rsrc, soff, 4 * l_b,
                   lds0 + at + (wave < 4 ? kXs + (256u * (uint32_t)wave) % (uint32_t)(kWs - kXs) : (uint32_t)kWs));
         if (++l_b == KB) {
@@ -611,9 +534,9 @@ template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAP
 void launch_tile(const ProductArgs& a, int tiles, hipStream_t s) {
     constexpr int kCols = GATED ? BN / 2 : BN;
     const long long all = (long long)tiles * ((a.N + kCols - 1) / kCols);
-    constexpr int kGrid = kCus * (BM <= 64 && BN <= 128 ? 2 : 1);  // (by their LDS)
+    constexpr int kGrid = kCus * (BN <= 64 ? 3 : BM <= 64 && BN <= 128 ? 2 : 1);  // (by their LDS)
     const unsigned grid = (unsigned)(all < kGrid ? (all + 7) / 8 * 8 : kGrid);  // (some for every XCD)
-    product_tile_kernel<BM, BN, WM, WN, S, E4M3, GATED, MAPPED><<<grid, kTileThreads, 0, s>>>(a);
+    product_tile_kernel<BM, BN, WM, WN, S, E4M3, GATED, MAPPED><<<grid, WM * WN * 64, 0, s>>>(a);
 }
 
 // Rows of a tile map of BM-row tiles (dense: the rows themselves).
@@ -632,41 +555,38 @@ int tiles_of(ProductArgs& a) {
 
 hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
     ProductArgs a = a0;
-    const int per = a.map ? (a.rows + a.E - 1) / a.E : a.rows;  // rows that share a matrix
-    const long long wgs256 = (long long)((a.N + 255) / 256) * (a.map ? min(a.rows, a.E) : (a.rows + 31) / 32);
+    auto tiles = [&](int m, int n) { return (long long)((a.rows + m - 1) / m) * ((a.N + n - 1) / n); };
     if (a.map) {
-        if (per <= 16) {
-            const int tiles = tiles_of<32>(a);
-            if (a.gated) launch_tile<32, 256, 1, 8, 4, false, true, true>(a, tiles, s);
-            else if (wgs256 >= 128) launch_tile<32, 256, 1, 8, 4, false, false, true>(a, tiles, s);
-            else launch_split<2, 4, false>(a, tiles, s);
-        } else if (a.gated) {
-            launch_tile<128, 256, 2, 4, 3, false, true, true>(a, tiles_of<128>(a), s);
+        if ((a.rows + a.E - 1) / a.E <= 16) {
+            if (a.gated) launch_tile<32, 256, 1, 8, 4, false, true, true>(a, tiles_of<32>(a), s);
+            else launch_tile<32, 256, 1, 8, 4, false, false, true>(a, tiles_of<32>(a), s);
         } else {
-            if (a.out_bf16) launch_tile<128, 256, 2, 4, 3, true, false, true>(a, tiles_of<128>(a), s);
+            if (a.gated) launch_tile<128, 256, 2, 4, 3, false, true, true>(a, tiles_of<128>(a), s);
+            else if (a.out_bf16) launch_tile<128, 256, 2, 4, 3, true, false, true>(a, tiles_of<128>(a), s);
             else launch_tile<128, 256, 2, 4, 3, false, false, true>(a, tiles_of<128>(a), s);
         }
-    } else if (per <= 16) {
-        const int tiles = tiles_of<32>(a);
-        if (a.gated) launch_split<1, 2, true>(a, tiles_of<16>(a), s);
-        else if (wgs256 >= 128) launch_tile<32, 256, 1, 8, 4, false, false, false>(a, tiles, s);
-        else if (a.N < 4096) launch_split<1, 16, false>(a, tiles_of<16>(a), s);
-        else launch_split<1, 8, false>(a, tiles_of<16>(a), s);
     } else if (a.gated) {
-        if (a.rows <= 64) launch_tile<64, 256, 2, 4, 3, false, true, false>(a, tiles_of<64>(a), s);
+        if (tiles(32, 256) <= kCus) launch_tile<32, 256, 1, 8, 4, false, true, false>(a, tiles_of<32>(a), s);
+        else if (tiles(64, 256) <= kCus) launch_tile<64, 256, 1, 8, 3, false, true, false>(a, tiles_of<64>(a), s);
         else launch_tile<128, 256, 2, 4, 3, false, true, false>(a, tiles_of<128>(a), s);
+    } else if (a.rows <= 16 && a.N < 16384) {
+        launch_split<1>(a, s);
+    } else if (tiles(32, 16) <= kCus) {
+        launch_split<2>(a, s);
+    } else if (tiles(256, 256) >= kCus) {
+        if (a.out_bf16) launch_tile<256, 256, 2, 4, 2, true, false, false>(a, tiles_of<256>(a), s);
+        else launch_tile<128, 256, 2, 4, 3, false, false, false>(a, tiles_of<128>(a), s);
+    } else if (tiles(128, 128) > kCus) {
+        if (a.out_bf16) launch_tile<128, 128, 2, 4, 3, true, false, false>(a, tiles_of<128>(a), s);
+        else launch_tile<128, 128, 2, 4, 3, false, false, false>(a, tiles_of<128>(a), s);
+    } else if (tiles(64, 128) >= 224) {
+        if (a.out_bf16) launch_tile<64, 128, 2, 4, 3, true, false, false>(a, tiles_of<64>(a), s);
+        else launch_tile<64, 128, 2, 4, 3, false, false, false>(a, tiles_of<64>(a), s);
+    } else if (a.rows > 32 && tiles(64, 64) >= 160) {
+        if (a.out_bf16) launch_tile<64, 64, 2, 4, 3, true, false, false>(a, tiles_of<64>(a), s);
+        else launch_tile<64, 64, 2, 4, 3, false, false, false>(a, tiles_of<64>(a), s);
     } else {
-        auto tiles = [&](int m, int n) { return (long long)((a.rows + m - 1) / m) * ((a.N + n - 1) / n); };
-        if (tiles(256, 256) >= kCus) {
-            if (a.out_bf16) launch_tile<256, 256, 2, 4, 2, true, false, false>(a, tiles_of<256>(a), s);
-            else launch_tile<128, 256, 2, 4, 3, false, false, false>(a, tiles_of<128>(a), s);
-        } else if (tiles(128, 128) > kCus) {
-            if (a.out_bf16) launch_tile<128, 128, 2, 4, 3, true, false, false>(a, tiles_of<128>(a), s);
-            else launch_tile<128, 128, 2, 4, 3, false, false, false>(a, tiles_of<128>(a), s);
-        } else {
-            if (a.out_bf16) launch_tile<64, 128, 2, 4, 3, true, false, false>(a, tiles_of<64>(a), s);
-            else launch_tile<64, 128, 2, 4, 3, false, false, false>(a, tiles_of<64>(a), s);
-        }
+        launch_tile<32, 64, 2, 4, 4, false, false, false>(a, tiles_of<32>(a), s);
     }
     trace_point(s);
     return hipGetLastError();
