@@ -269,7 +269,7 @@ __device__ __forceinline__ void tile_products(f32x4 (&d)[NT], const i32x8 (&w)[N
 template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAPPED>
 __global__ __launch_bounds__(WM * WN * 64) void product_tile_kernel(const ProductArgs a) {
     constexpr int kW = WM * WN;
-    static_assert((kW == 8 || kW == 16) && S >= 2 && S <= 4 && (!GATED || BN == 256) && (!MAPPED || BM / WM <= 64), "shape");
+    static_assert(kW == 8 && S >= 2 && S <= 4 && (!GATED || BN == 256) && (!MAPPED || BM / WM <= 64), "shape");
     constexpr int MT = BM / WM / 16, NT = BN / WN / 16, M = GATED ? 2 : 1;
     constexpr bool INTER = MAPPED;
     // a stage: W's rows, x's rows, x's scales (a load writes 256 bytes), the two scales of W
@@ -566,8 +566,8 @@ hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
             else launch_tile<128, 256, 2, 4, 3, false, false, true>(a, tiles_of<128>(a), s);
         }
     } else if (a.gated) {
-        if (tiles(32, 256) <= kCus) launch_tile<32, 256, 1, 8, 4, false, true, false>(a, tiles_of<32>(a), s);
-        else if (tiles(64, 256) <= kCus) launch_tile<64, 256, 1, 8, 3, false, true, false>(a, tiles_of<64>(a), s);
+        if (tiles(32, 128) <= kCus) launch_tile<32, 256, 1, 8, 4, false, true, false>(a, tiles_of<32>(a), s);
+        else if (tiles(64, 128) <= kCus) launch_tile<64, 256, 1, 8, 3, false, true, false>(a, tiles_of<64>(a), s);
         else launch_tile<128, 256, 2, 4, 3, false, true, false>(a, tiles_of<128>(a), s);
     } else if (a.rows <= 16 && a.N < 16384) {
         launch_split<1>(a, s);
