@@ -233,3 +233,52 @@ def test_host_made_routings_are_what_the_kernels_take():
     assert np.array_equal(np.sort(r.inv_perm[:120].numpy()), np.arange(120))
     x, s = quantised_rows(rng, 5, 192)
     assert x.shape == (5, 192) and s.shape == (5, 2)
+
+
+def test_own_buffers_are_allocated_with_the_calls_stream_current(monkeypatch):
+    """(on the CPU: every allocation happens inside the stream's context; the calls are
+    refused afterwards, because the tensors are not on the GPU)"""
+    import contextlib
+    import types
+
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Allocations(TorchDispatchMode):
+        def __init__(self):
+            super().__init__()
+            self.seen, self.active = [], False
+
+        def __torch_dispatch__(self, func, types_, args=(), kwargs=None):
+            if "empty" in func.overloadpacket.__name__ or "zeros" in func.overloadpacket.__name__:
+                self.seen.append(self.active)
+            return func(*args, **(kwargs or {}))
+
+    r = q4.DeviceRouting(2, 8, 2, "cpu")
+    x, rows = torch.zeros(2, 128, dtype=bf16), torch.zeros(4, 128, dtype=bf16)
+    x8, xs = torch.zeros(4, 128).to(f8), torch.zeros(4, 1)
+    w, ws = torch.zeros(8, 2, 64, 128).to(f8), torch.zeros(8, 2, 1, 1)
+    calls = [(lambda s: q4.linear_e4m3(w[0], ws[0], x8, xs, gated=True, stream=s), 2),
+             (lambda s: q4.linear_e4m3(w[0, 0], ws[0, 0], x8, xs, stream=s), 1),
+             (lambda s: q4.experts_e4m3(w, ws, x8, xs, r, gated=True, stream=s), 2),
+             (lambda s: q4.dispatch(x, r, e4m3=True, stream=s), 2),
+             (lambda s: q4.combine(rows, r, stream=s), 1),
+             (lambda s: q4.combine_grad(x, rows, r, stream=s), 2),
+             (lambda s: q4.penalize(torch.zeros(2, 9), stream=s), 1)]
+    mode, stream = Allocations(), types.SimpleNamespace(device=torch.device("cuda:0"), cuda_stream=0)
+
+    @contextlib.contextmanager
+    def current(s):
+        mode.active = s is stream
+        yield
+        mode.active = False
+
+    monkeypatch.setattr(torch.cuda, "stream", current)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=0))
+    for call, n in calls:
+        mode.seen.clear()
+        if n == 1 and call is calls[-1][0]:
+            l = torch.zeros(2, 9)
+            call = lambda s: q4.penalize(l, stream=s)                                # noqa: E731
+        with mode, pytest.raises(ValueError, match="GPU"):
+            call(stream)
+        assert len(mode.seen) >= n and all(mode.seen)
