@@ -135,6 +135,7 @@ hipError_t launch_product(const ProductArgs& a, hipStream_t s);
 // Rows into expert order and back (moe_dispatch, moe_combine, moe_combine_grad).
 struct SortArgs {
     const int32_t* inv_perm;  // [T][k]
+    int pieces;               // threads a token (the launchers set it)
     int T, k, d;
     const uint16_t* x;        // dispatch: bf16 [T][d]
     void* rows_out;           // bf16 or e4m3 [T*k][d] (combine_grad: d_rows or NULL)

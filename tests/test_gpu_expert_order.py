@@ -33,7 +33,7 @@ def rows_of(rng, n, d):
     return torch.from_numpy(rng.standard_normal((n, d)).astype(np.float32)).to(bf16)
 
 
-SHAPES = [(1, 1, 1, 64), (1, 256, 8, 2048), (2, 5, 3, 192), (7, 9, 8, 448), (33, 256, 8, 576),
+SHAPES = [(1, 1, 1, 64), (70, 12, 7, 128), (9, 12, 7, 704), (1, 256, 8, 2048), (2, 5, 3, 192), (7, 9, 8, 448), (33, 256, 8, 576),
           (5, 16, 2, 2112), (3, 4, 4, 8192), (129, 3, 1, 1024), (300, 40, 5, 320), (40, 8, 6, 4160)]
 
 
