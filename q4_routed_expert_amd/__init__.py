@@ -633,6 +633,10 @@ def _product(where, w, w_scale, x, x_scale, lead, rows, out_dtype, gated, y, y_s
     if x.shape[1] != K:
         raise ValueError(f"{where}: w has {K} columns, x has {x.shape[1]}")
     kb, nb = (K + 127) >> 7, (N + 127) >> 7
+    # (a scale per 64 columns has enough elements too, and would be read as another's)
+    if x_scale.shape[-1] != kb or tuple(w_scale.shape[-2:]) != (nb, kb):
+        raise ValueError(f"{where}: x_scale must be [rows, {kb}] and w_scale {[*lead, nb, kb]}, not "
+                         f"{tuple(x_scale.shape)}, {tuple(w_scale.shape)}")
     mats = 1
     for n in lead:
         mats *= n

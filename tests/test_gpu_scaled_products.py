@@ -270,3 +270,26 @@ def test_outputs_past_32_bits(dev):
     rows = [0, 1, 16383, 32735, 32767]
     want, size = plain.product(values(w), ws.numpy(), values(x[rows]), xs[rows].numpy())
     check(y[rows], want, bar_of(size, K) + np.abs(want) * 2.0 ** -8 + CUT * size)
+
+
+def test_a_map_out_of_range_stays_in_bounds(dev):
+    # entries that no routing writes: rows and experts beyond their arrays, too many tiles
+    T, E, k, N, K = 6, 40, 2, 256, 128
+    rng = np.random.default_rng(8)
+    w, ws = (t.to(dev) for t in weights(rng, E, N, K))
+    for rows in (1, 64):  # tiles of 32 and of 128 rows
+        t = T * rows
+        idx, wt = selections(rng, t, E - 30, k)
+        r, _ = device_routing(idx, wt, E, dev)
+        x, xs = (v.to(dev) for v in quantised_rows(rng, t * k, K))
+        want = q4.experts_e4m3(w, ws, x, xs, r)
+        for m, n in ((r.block_map, r.n_blocks), (r.tile_map, r.n_tiles)):
+            used = int(n)
+            assert used + 2 <= len(m)  # (some experts have no rows)
+            m[used:] = torch.tensor([1 << 30, -(1 << 31)], dtype=torch.int32)
+            m[-1] = torch.tensor([-7, t * k], dtype=torch.int32)
+            n.fill_(1 << 30)
+        room = torch.full((t * k + 200, N), 7.0, dtype=torch.bfloat16, device=dev)
+        y = q4.experts_e4m3(w, ws, x, xs, r, y=room)
+        torch.cuda.synchronize()
+        assert torch.equal(y[:t * k], want) and bool((y[t * k:] == 7.0).all())

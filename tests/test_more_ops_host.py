@@ -137,6 +137,8 @@ def test_product_binding_refuses():
     for kw, what in ((dict(x=x.float()), "x"), (dict(x=x[0]), "x"), (dict(x=x[:, :128]), "columns"),
                      (dict(w=w.float()), "w"), (dict(w=w[None]), "w"), (dict(ws=ws[:1]), "w_scale"),
                      (dict(ws=ws.half()), "w_scale"), (dict(xs=xs[:3]), "x_scale"),
+                     (dict(xs=torch.zeros(4, 3)), "x_scale"),  # a scale per 64 columns
+                     (dict(ws=torch.zeros(3, 2)), "w_scale"), (dict(ws=ws.view(4)), "w_scale"),
                      (dict(out_dtype=torch.float16), "out_dtype"), (dict(gated=True), "w"),
                      (dict(y=torch.zeros(4, 130)), "y"), (dict(y_scale=xs), "y_scale"),
                      (dict(y=torch.zeros(4, 131, dtype=bf16)[:, :130]), "contiguous"), (dict(), "GPU")):
