@@ -286,7 +286,7 @@ __device__ __forceinline__ void tile_products(f32x4 (&d)[NT], const i32x8 (&w)[N
 template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAPPED>
 __global__ __launch_bounds__(WM * WN * 64) void product_tile_kernel(const ProductArgs a) {
     constexpr int kW = WM * WN;
-    static_assert(kW == 8 && S >= 2 && S <= 4 && (!GATED || BN == 256) && (!MAPPED || BM / WM <= 64), "shape");
+    static_assert((kW == 8 || kW == 4) && BM <= 32 * kW && S >= 2 && S <= 4 && (!GATED || BN == 256) && (!MAPPED || BM / WM <= 64), "shape");
     constexpr int MT = BM / WM / 16, NT = BN / WN / 16, M = GATED ? 2 : 1;
     // a stage: W's rows, x's rows, x's scales (a load writes 256 bytes), the two scales of W
     constexpr int kX = BN * kBlock, kXs = kX + BM * kBlock, kWs = kXs + (BM < 64 ? 256 : 4 * BM), kStage = kWs + 256;
@@ -347,8 +347,8 @@ __global__ __launch_bounds__(WM * WN * 64) void product_tile_kernel(const Produc
             const int r = (8 * (wave + kW * j) + (lane >> 3)) % BM;
             xoff[j] = (uint32_t)min(r, last) * (uint32_t)K + 16 * piece;
         }
-        // waves 0 .. 3 fetch x's scales, the others W's: of its two halves, or of gate and up
-        if (wave < 4) {
+        // half of the waves fetch x's scales, the others W's: of its two halves, or of gate and up
+        if (wave < kW / 2) {
             s_rsrc = buffer_from(a.x_scale + (size_t)s.row0 * KB);
             soff = 4u * (uint32_t)min((64 * wave + lane) % BM, last) * (uint32_t)KB;
         } else {
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_tile_kernel(const Produc
             load16_lds(x_rsrc, xoff[j] - back, l_b * kBlock,
                        lds0 + at + kX + (1024u * (uint32_t)(wave + kW * j)) % (uint32_t)(BM * kBlock));
         load4_lds(s_rsrc, soff, 4 * l_b,
-                  lds0 + at + (wave < 4 ? kXs + (256u * (uint32_t)wave) % (uint32_t)(kWs - kXs) : (uint32_t)kWs));
+                  lds0 + at + (wave < kW / 2 ? kXs + (256u * (uint32_t)wave) % (uint32_t)(kWs - kXs) : (uint32_t)kWs));
         if (++l_b == KB) {
             l_b = 0;
             l_id += per_xcd;
@@ -388,8 +388,9 @@ __global__ __launch_bounds__(WM * WN * 64) void product_tile_kernel(const Produc
     auto x_row = [&](int t) { return MAPPED ? 16 * (t * WM + wm) : 16 * (wm * MT + t); };
     f32x4 acc[MT][NT];
     // The block in the stage at `at`, for the first TL of this wave's 16-token tiles.  The
-    // operands of 16 tokens are read while those of the 16 before are multiplied, whose sums are
-    // added one turn later still.
+    // operands of 16 tokens are read while those of the 16 before are multiplied, whose sums, of
+    // bf16 products, are added one turn later still (of 8-bit ones at once: with two tiles' sums
+    // in registers the largest tile spills, 8192^3 633 instead of 567 us).
     auto compute = [&](auto live, uint32_t at, float part) {
         constexpr int TL = decltype(live)::value;
         using Op = typename TileOperand<E4M3>::type;
@@ -431,8 +432,12 @@ __global__ __launch_bounds__(WM * WN * 64) void product_tile_kernel(const Produc
             for (int m = 0; m < M; ++m) f[t & 1][m] = xs * ws[m];
             if (t + 1 < TL) fetch(t + 1);
             tile_products(d[t & 1], w, x);
-            if (t > 0) add(t - 1);
-            if (t + 1 == TL) add(t);
+            if (E4M3) {
+                add(t);
+            } else {
+                if (t > 0) add(t - 1);
+                if (t + 1 == TL) add(t);
+            }
         }
     };
     // Expert-sorted rows: tiles are seldom full, and 16 rows that are not there are left out.
@@ -550,7 +555,7 @@ template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAP
 void launch_tile(const ProductArgs& a, int tiles, hipStream_t s) {
     constexpr int kCols = GATED ? BN / 2 : BN;
     const long long all = (long long)tiles * ((a.N + kCols - 1) / kCols);
-    constexpr int kGrid = kCus * (BN <= 64 ? 3 : BM <= 64 && BN <= 128 ? 2 : 1);  // (by their LDS)
+    constexpr int kGrid = kCus * (BN <= 64 ? 3 : S * (BM + BN) <= 600 ? 2 : 1);  // (by their LDS)
     const unsigned grid = (unsigned)(all < kGrid ? (all + 7) / 8 * 8 : kGrid);  // (some for every XCD)
     product_tile_kernel<BM, BN, WM, WN, S, E4M3, GATED, MAPPED><<<grid, WM * WN * 64, 0, s>>>(a);
 }
@@ -578,7 +583,9 @@ int tiles_of(ProductArgs& a) {
 //     300 x 2 x 2048 x 2048 19, 25 with 64, 36 with 128.
 //   one token, 8192 x 8192: 15 in the few-token kernel, 30 in 32 x 64 tiles; 16 tokens, 16384 x
 //     4096: 22 and 18.  32 tokens, 4096 x 4096: 11 and 17; 128 tokens, 2048 x 2048: 13 and 10.
-//   2048 x 4096 x 4096, fp32: 88 with tiles of 128 x 128, 90 with 64 x 128; 512 rows: 43 and 31;
+//   2048 x 4096 x 4096, fp32: 79 with tiles of 128 x 128 (two work groups of four waves a CU; 88
+//     with one of eight), 90 with 64 x 128; bf16: 46 (two of eight waves; one: 52, two of four:
+//     50); 512 rows, fp32: 43 and 31;
 //     300 x 2048 x 2048: 16 with 64 x 128, 13.5 with 64 x 64, 14 with 32 x 64; 128 x 4096 x 4096:
 //     27, 21, 17.5.
 //   8 tokens, 248320 x 2048: 91 with 32 x 256, 97 with 32 x 64; 60000 rows: 28 and 26.
@@ -606,8 +613,8 @@ hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
         if (a.out_bf16) launch_tile<256, 256, 2, 4, 2, true, false, false>(a, tiles_of<256>(a), s);
         else launch_tile<128, 256, 2, 4, 3, false, false, false>(a, tiles_of<128>(a), s);
     } else if (a.rows > 64 && tiles(128, 128) > kCus) {
-        if (a.out_bf16) launch_tile<128, 128, 2, 4, 3, true, false, false>(a, tiles_of<128>(a), s);
-        else launch_tile<128, 128, 2, 4, 3, false, false, false>(a, tiles_of<128>(a), s);
+        if (a.out_bf16) launch_tile<128, 128, 2, 4, 2, true, false, false>(a, tiles_of<128>(a), s);
+        else launch_tile<128, 128, 2, 2, 2, false, false, false>(a, tiles_of<128>(a), s);
     } else if (a.rows > 32 && tiles(64, 128) >= 224) {
         if (a.out_bf16) launch_tile<64, 128, 2, 4, 3, true, false, false>(a, tiles_of<64>(a), s);
         else launch_tile<64, 128, 2, 4, 3, false, false, false>(a, tiles_of<64>(a), s);
