@@ -576,9 +576,10 @@ int tiles_of(ProductArgs& a) {
 
 // The largest tile that still gives every CU work: larger tiles read LDS and convert less per
 // product, smaller ones fill the chip.  Measured at the borders (us):
-//   experts, rows of an expert on average:  gated, 2 x 512 rows, K = 2048: 8 rows 96 with tiles of
-//     32 rows, 102 with 128; 32 rows 120 and 131; 64 rows 178 and 172.  bf16, K = 512: 8 rows 52
-//     and 54; 16 rows 55 and 54; 64 rows 95 and 72.
+//   experts, rows of an expert on average: gated, 2 x 512 rows, K = 2048: 32 rows 110 with tiles
+//     of 32 rows and two work groups a CU, 123 with one, 131 with tiles of 128; 64 rows 157, 178
+//     and 171; 128 rows 251, 292 and 232; 8 tokens (228 tiles) 25.8 and 25.1.  bf16, K = 512: 8
+//     rows 52 and 54; 16 rows 55 and 54; 64 rows 95 and 72.
 //   gated: 128 x 2 x 8192 x 2048 20 with tiles of 32 rows, 37 with 128; 512 rows 67 and 42;
 //     300 x 2 x 2048 x 2048 19, 25 with 64, 36 with 128.
 //   one token, 8192 x 8192: 15 in the few-token kernel, 30 in 32 x 64 tiles; 16 tokens, 16384 x
@@ -593,8 +594,12 @@ hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
     ProductArgs a = a0;
     auto tiles = [&](int m, int n) { return (long long)((a.rows + m - 1) / m) * ((a.N + n - 1) / n); };
     if (a.map) {
-        if ((a.rows + a.E - 1) / a.E <= (a.out_bf16 ? 16 : 32)) {
-            if (a.gated) launch_tile<32, 256, 1, 8, 4, false, true, true>(a, tiles_of<32>(a), s);
+        const int per = (a.rows + a.E - 1) / a.E;
+        if (per <= (a.gated ? 96 : a.out_bf16 ? 16 : 32)) {
+            // (one tile a CU at most: all of its LDS for loads in flight)
+            const bool few = (long long)min(a.rows, a.E) * ((a.N + (a.gated ? 127 : 255)) / (a.gated ? 128 : 256)) <= kCus;
+            if (a.gated && few) launch_tile<32, 256, 1, 8, 4, false, true, true>(a, tiles_of<32>(a), s);
+            else if (a.gated) launch_tile<32, 256, 1, 4, 2, false, true, true>(a, tiles_of<32>(a), s);
             else launch_tile<32, 256, 1, 8, 4, false, false, true>(a, tiles_of<32>(a), s);
         } else {
             if (a.gated) launch_tile<128, 256, 2, 4, 3, false, true, true>(a, tiles_of<128>(a), s);

@@ -152,7 +152,8 @@ def test_gated_matches_the_formula(dev, T, I, K):
 EXPERTS = [(1, 2, 1, 64, 64, 0.0), (1, 256, 8, 256, 512, 0.0), (3, 7, 2, 128, 192, 1.0),
            (8, 32, 8, 192, 320, 0.5), (40, 5, 3, 320, 448, 1.0), (70, 3, 1, 130, 128, 2.0),
            (150, 33, 4, 64, 192, 1.0), (300, 4, 2, 258, 576, 1.5), (64, 64, 8, 128, 64, 0.0),
-           (500, 16, 4, 512, 256, 1.0), (60, 256, 8, 320, 128, 0.0), (2000, 64, 4, 1152, 128, 1.0)]
+           (500, 16, 4, 512, 256, 1.0), (60, 256, 8, 320, 128, 0.0), (300, 64, 4, 576, 192, 1.0),
+          (2000, 64, 4, 1152, 128, 1.0)]
 
 
 @pytest.mark.parametrize("T,E,k,N,K,skew", EXPERTS)
