@@ -28,7 +28,7 @@
 // 1.13 PFLOP/s (vector ALUs: a conversion for two codes, a multiply-add for an output and block,
 // and a matrix instruction holds their issue for as long as three of them).  Expert products
 // stream weights: 8 tokens through 256 experts of 2 x 512 rows, K = 2048, 24 us (5.0 TB/s); 2048
-// tokens 170 us (130 of multiplying alone, 113 of loading alone); 4096 tokens through 2048
+// tokens 155 us (130 of multiplying alone, 113 of loading alone); 4096 tokens through 2048
 // rows, K = 512, in bf16 96 us (4.4 TB/s).  One token, 2048 x 2048: 3.7 us.
 #include "e4m3.h"
 #include "ops.h"
