@@ -588,7 +588,8 @@ int tiles_of(ProductArgs& a) {
 //     with one of eight), 90 with 64 x 128; bf16: 46 (two of eight waves; one: 52, two of four:
 //     50); 512 rows, fp32: 43 and 31;
 //     300 x 2048 x 2048: 16 with 64 x 128, 13.5 with 64 x 64, 14 with 32 x 64; 128 x 4096 x 4096:
-//     27, 21, 17.5.
+//     27, 21, 17.5.  64 x 128, two stages and three: 512 x 4096 x 4096 in fp32 29.6 and 30.6, in
+//     bf16 24.8 and 20.5 (half the work between two waits).
 //   8 tokens, 248320 x 2048: 91 with 32 x 256, 97 with 32 x 64; 60000 rows: 28 and 26.
 hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
     ProductArgs a = a0;
@@ -622,7 +623,7 @@ hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
         else launch_tile<128, 128, 2, 2, 2, false, false, false>(a, tiles_of<128>(a), s);
     } else if (a.rows > 32 && tiles(64, 128) >= 224) {
         if (a.out_bf16) launch_tile<64, 128, 2, 4, 3, true, false, false>(a, tiles_of<64>(a), s);
-        else launch_tile<64, 128, 2, 4, 3, false, false, false>(a, tiles_of<64>(a), s);
+        else launch_tile<64, 128, 2, 4, 2, false, false, false>(a, tiles_of<64>(a), s);
     } else if (a.rows > 32 && tiles(64, 64) >= 160) {
         if (a.out_bf16) launch_tile<64, 64, 2, 4, 3, true, false, false>(a, tiles_of<64>(a), s);
         else launch_tile<64, 64, 2, 4, 3, false, false, false>(a, tiles_of<64>(a), s);
