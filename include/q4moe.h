@@ -435,8 +435,8 @@ typedef struct {
     const float* scale;   /* [n_mat][ceil(N/128)][ceil(K/128)] */
 } moe_e4m3mat;
 int moe_linear_scaled(const moe_e4m3mat* m, int32_t N, int32_t K, const uint8_t* x,
-                    const float* x_scale, int32_t T, uint32_t flags, void* y, float* y_scale,
-                    void* stream);
+                      const float* x_scale, int32_t T, uint32_t flags, void* y, float* y_scale,
+                      void* stream);
 /* The same products over expert-sorted rows, a matrix per expert: m holds E of them
    (gated: E times two), x and x_scale have T * k rows in the order of a routing
    of T tokens (what moe_dispatch writes), and row j of expert e, offsets[e] <= j <
@@ -444,8 +444,8 @@ int moe_linear_scaled(const moe_e4m3mat* m, int32_t N, int32_t K, const uint8_t*
    tile_map and n_tiles are read.  1 <= E <= MOE_MAX_EXPERTS, 1 <= k <= min(MOE_MAX_TOPK,
    E). */
 int moe_experts_scaled(const moe_e4m3mat* m, int32_t E, int32_t N, int32_t K, const uint8_t* x,
-                     const float* x_scale, int32_t T, int32_t k, const moe_routing* r,
-                     uint32_t flags, void* y, float* y_scale, void* stream);
+                       const float* x_scale, int32_t T, int32_t k, const moe_routing* r,
+                       uint32_t flags, void* y, float* y_scale, void* stream);
 
 /* Token rows into expert order and back, for expert products other than moe_prefill's,
    which has both built in.  Of r, inv_perm is read, and topk_w where weights are used.

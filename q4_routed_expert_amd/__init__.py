@@ -634,7 +634,7 @@ def _product(where, w, w_scale, x, x_scale, lead, rows, out_dtype, gated, y, y_s
         raise ValueError(f"{where}: w has {K} columns, x has {x.shape[1]}")
     kb, nb = (K + 127) >> 7, (N + 127) >> 7
     # (a scale per 64 columns has enough elements too, and would be read as another's)
-    if x_scale.shape[-1] != kb or tuple(w_scale.shape[-2:]) != (nb, kb):
+    if x_scale.shape[-1:] != (kb,) or w_scale.shape[-2:] != (nb, kb):
         raise ValueError(f"{where}: x_scale must be [rows, {kb}] and w_scale {[*lead, nb, kb]}, not "
                          f"{tuple(x_scale.shape)}, {tuple(w_scale.shape)}")
     mats = 1
@@ -674,7 +674,7 @@ def linear_e4m3(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, x_scale
                                           gated, y, y_scale)
     s = _launch_on("linear_e4m3", w=w, w_scale=w_scale, x=x, x_scale=x_scale, y=y, y_scale=y_scale)
     _check(_abi.lib().moe_linear_scaled(C.addressof(m), N, K, _ptr(x), _ptr(x_scale), T, flags,
-                                      _ptr(y), _ptr(y_scale), s), "moe_linear_scaled")
+                                        _ptr(y), _ptr(y_scale), s), "moe_linear_scaled")
     return (y, y_scale) if gated else y
 
 
@@ -706,8 +706,8 @@ def experts_e4m3(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, x_scal
     s = _launch_on("experts_e4m3", w=w, w_scale=w_scale, x=x, x_scale=x_scale, y=y, y_scale=y_scale,
                    offsets=routing.offsets)
     _check(_abi.lib().moe_experts_scaled(C.addressof(m), routing.E, N, K, _ptr(x), _ptr(x_scale), T,
-                                       routing.k, C.addressof(routing.struct), flags, _ptr(y),
-                                       _ptr(y_scale), s), "moe_experts_scaled")
+                                         routing.k, C.addressof(routing.struct), flags, _ptr(y),
+                                         _ptr(y_scale), s), "moe_experts_scaled")
     return (y, y_scale) if gated else y
 
 

@@ -129,7 +129,7 @@ def lib():
         L.moe_add_norm.argtypes = [vp, i32, i32, vp, vp, vp, C.c_float, C.c_uint32, vp, vp, vp, vp]
         L.moe_linear_scaled.argtypes = [vp, i32, i32, vp, vp, i32, C.c_uint32, vp, vp, vp]
         L.moe_experts_scaled.argtypes = [vp, i32, i32, i32, vp, vp, i32, i32, vp, C.c_uint32, vp, vp,
-                                       vp]
+                                         vp]
         L.moe_dispatch.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp]
         L.moe_combine.argtypes = [vp, i32, i32, i32, vp, C.c_uint32, vp, vp, vp]
         L.moe_combine_grad.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp]

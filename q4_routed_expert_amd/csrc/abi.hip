@@ -752,7 +752,7 @@ q4moe::SortArgs sort_args(int32_t T, int32_t k, int32_t d, const moe_routing* r)
 extern "C" {
 
 int moe_linear_scaled(const moe_e4m3mat* m, int32_t N, int32_t K, const uint8_t* x, const float* x_scale,
-                    int32_t T, uint32_t flags, void* y, float* y_scale, void* stream) {
+                      int32_t T, uint32_t flags, void* y, float* y_scale, void* stream) {
     int rc;
     if ((rc = check_product(m, N, K, x, x_scale, flags, y, y_scale)) || (rc = check_tokens(T))) return rc;
     const q4moe::ProductArgs a = product_args(m, N, K, x, x_scale, T, flags, y, y_scale);
@@ -761,8 +761,8 @@ int moe_linear_scaled(const moe_e4m3mat* m, int32_t N, int32_t K, const uint8_t*
 }
 
 int moe_experts_scaled(const moe_e4m3mat* m, int32_t E, int32_t N, int32_t K, const uint8_t* x,
-                     const float* x_scale, int32_t T, int32_t k, const moe_routing* r, uint32_t flags,
-                     void* y, float* y_scale, void* stream) {
+                       const float* x_scale, int32_t T, int32_t k, const moe_routing* r,
+                       uint32_t flags, void* y, float* y_scale, void* stream) {
     int rc;
     if ((rc = check_product(m, N, K, x, x_scale, flags, y, y_scale)) || (rc = check_tokens(T))) return rc;
     if (E <= 0 || k <= 0) return fail(MOE_EINVAL, "E=%d and k=%d must be positive", E, k);

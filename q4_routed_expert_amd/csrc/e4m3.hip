@@ -238,12 +238,13 @@ __device__ __forceinline__ u32x4 buffer_from(const void* p) {
                  0x00020000u};
 }
 
-// s_waitcnt vmcnt(N), leaving the other counters alone (vmcnt in bits 3:0 and 15:14, expcnt
-// 6:4, lgkmcnt 11:8).
+// s_waitcnt vmcnt(N) lgkmcnt(0), before a barrier: all but the newest N loads are there, and this
+// wave's reads of LDS are done, so that others may write what it read (vmcnt in bits 3:0 and
+// 15:14, expcnt 6:4, lgkmcnt 11:8).
 template <int N>
 __device__ __forceinline__ void wait_loads() {
     static_assert(N >= 0 && N < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4));
 }
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
