@@ -161,6 +161,39 @@ def test_indices_out_of_range_stay_in_bounds(dev):
     assert not guard[:T * k].any() and not guard[2 * T * k:].any()
 
 
+def test_rows_past_32_bits(dev):
+    # 2^31 elements of expert rows, 2^32 bytes; tokens in reverse order
+    T, E, k, d = 32768, 8, 8, 8192
+    idx = np.tile(np.arange(8, dtype=np.int32), (T, 1))
+    w = np.random.default_rng(1).random((T, k)).astype(np.float32)
+    r, _ = device_routing(idx, w, E, dev)
+    inv = torch.arange(T * k - 1, -1, -1, dtype=torch.int32).view(T, k)
+    r.inv_perm.view(-1)[:T * k] = inv.view(-1).to(dev)
+    x = torch.randn(T, d, device=dev).to(bf16)
+    rows, _ = q4.dispatch(x, r)
+    codes, scale = q4.dispatch(x, r, e4m3=True)
+    y = q4.combine(rows, r)
+    at = [0, 1, T // 2, T - 2, T - 1]
+    for t in at:
+        mine = inv[t].tolist()
+        assert all(torch.equal(rows[i], x[t]) for i in mine), t
+        h = wide(x[t])
+        for i in mine:
+            sc = plain.expand(wide(scale[i:i + 1]), 1, 1, d)[0]
+            bar = np.maximum(np.abs(h) * 2.0 ** -4, sc * 2.0 ** -10) + np.abs(h) * 2.0 ** -20
+            assert (np.abs(values(codes[i:i + 1])[0] * sc - h) <= bar).all(), (t, i)
+        want = h * w[t].astype(np.float64).sum()
+        size = np.abs(h) * w[t].astype(np.float64).sum()
+        assert (np.abs(wide(y[t]) - want) <= (k + 1) * 2.0 ** -24 * size + np.abs(want) * 2.0 ** -8).all()
+    _, d_w = q4.combine_grad(x, rows, r, d_rows=rows)
+    for t in at:
+        h = wide(x[t])
+        for s, i in enumerate(inv[t].tolist()):
+            want = w[t, s].astype(np.float64) * h
+            assert (np.abs(wide(rows[i]) - want) <= np.abs(want) * (2.0 ** -8 + 2.0 ** -23)).all()
+        assert (np.abs(wide(d_w[t]) - (h * h).sum()) <= 50 * 2.0 ** -24 * (h * h).sum()).all()
+
+
 def test_streams_and_graphs(dev):
     T, E, k, d = 20, 16, 4, 512
     rng, r, _, _ = setup(dev, T, E, k, d)

@@ -165,6 +165,29 @@ def test_biases_of_one_token_add_in_list_order(dev):
         assert y[r, V - 1] == s
 
 
+def test_logits_past_32_bits(dev):
+    # 2^32 bytes of logits: a row in the middle and the last one, the others as they were
+    B, V, L = 1024, 1048576, 64
+    l = torch.randn(B, V, device=dev)
+    c = case(17, 2, V, L, 12, 0.3)
+    c["allowed"][1] = c["allowed"][0][::-1]
+    rows = [B // 2, B - 1]
+    c["logits"] = l[rows].cpu().numpy()
+    a = {n: torch.zeros((B,) + v.shape[1:], dtype=torch.from_numpy(v).dtype, device=dev)
+         for n, v in c.items() if n not in ("logits", "allowed")}
+    for n, t in a.items():
+        t[rows] = torch.from_numpy(c[n]).to(dev)
+    a["repetition"][a["repetition"] == 0] = 1.0
+    a["mask"] = torch.full((B, V // 32), -1, dtype=i32, device=dev)
+    a["mask"][rows] = words(c["allowed"]).to(dev)
+    y = q4.penalize(l, **a)
+    check(c, y[rows])
+    others = [0, 1, B // 2 - 1, B // 2 + 1, B - 2]
+    assert torch.equal(y[others], l[others])
+    q4.penalize(l, out=l, **a)
+    assert torch.equal(y, l)
+
+
 def test_streams_and_graphs(dev):
     c = case(3, 4, 30011, 500, 30, 0.5)
     want = call(c, dev)

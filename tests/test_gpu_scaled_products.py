@@ -205,6 +205,26 @@ def test_special_values(dev, T, N, K):
         check(y[keep][:, :N - 1], want[keep][:, :N - 1], bar_of(size, K)[keep][:, :N - 1])
 
 
+@pytest.mark.parametrize("T,N,K", [(20, 300, 320), (40, 1100, 448), (300, 2050, 320), (4100, 4100, 192)])
+def test_special_values_of_bf16_outputs(dev, T, N, K):
+    # the tiles whose products are the matrix cores' own
+    rng = np.random.default_rng(N)
+    x, xs = quantised_rows(rng, T, K)
+    w, ws = weights(rng, N, K)
+    rows = [0, 1, 2, 5, T - 1]
+    want, size = plain.product(values(w), ws.numpy(), values(x[rows]), xs[rows].numpy())
+    x.view(torch.uint8)[1, K - 1] = 0xFF         # NaN with its sign: that token only
+    w.view(torch.uint8)[N - 1, 0] = 0x7F         # that column only
+    xs[2, 0] = float("inf")
+    xs[0] = 0.0
+    y = q4.linear_e4m3(w.to(dev), ws.to(dev), x.to(dev), xs.to(dev)).cpu()
+    assert y[1].isnan().all() and y[:, N - 1].isnan().all() and not y[2].isfinite().any()
+    assert (y[0, :N - 1] == 0).all() and y[3:, :N - 1].isfinite().all()
+    keep = [3, 4]
+    check(y[[5, T - 1]][:, :N - 1], want[keep][:, :N - 1],
+          (bar_of(size, K) + np.abs(want) * 2.0 ** -8 + CUT * size)[keep][:, :N - 1])
+
+
 @pytest.mark.parametrize("T", [3, 200])
 def test_gated_special_values(dev, T):
     rng = np.random.default_rng(5)
@@ -271,6 +291,26 @@ def test_outputs_past_32_bits(dev):
     rows = [0, 1, 16383, 32735, 32767]
     want, size = plain.product(values(w), ws.numpy(), values(x[rows]), xs[rows].numpy())
     check(y[rows], want, bar_of(size, K) + np.abs(want) * 2.0 ** -8 + CUT * size)
+
+
+@pytest.mark.parametrize("T", [90, 4400])
+def test_matrices_past_32_bits(dev, T):
+    # 256 matrices of more than 2^32 bytes together, in tiles of 32 rows and of 128
+    E, k, N, K = 256, 2, 2112, 8192
+    rng = np.random.default_rng(T)
+    idx = rng.integers(0, E - 2, (T, k)).astype(np.int32)
+    idx[:, 1] = (idx[:, 0] + 1) % (E - 2)
+    idx[T - 40:] = (E - 2, E - 1)
+    wt = np.ones((T, k), np.float32)
+    r, o = device_routing(idx, wt, E, dev)
+    w = torch.randint(0, 0x78, (E, N, K), dtype=torch.uint8, device=dev).view(f8)
+    ws = torch.full((E, -(-N // 128), K // 128), 2.0 ** -12, device=dev)
+    x, xs = quantised_rows(rng, T * k, K)
+    y = q4.experts_e4m3(w, ws, x.to(dev), xs.to(dev), r, out_dtype=torch.float32)
+    for e in (0, E - 2, E - 1):
+        a, b = int(o["offsets"][e]), int(o["offsets"][e + 1])
+        want, size = plain.product(values(w[e]), ws[e].cpu().numpy(), values(x[a:b]), xs[a:b].numpy())
+        check(y[a:b], want, bar_of(size, K))
 
 
 def test_a_map_out_of_range_stays_in_bounds(dev):
