@@ -625,13 +625,13 @@ def _product(where, w, w_scale, x, x_scale, lead, rows, out_dtype, gated, y, y_s
         lead, out_dtype = lead + (2,), torch.float8_e4m3fn
     elif out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, not {out_dtype}")
-    shape = w.shape
-    if x.dim() != 2 or len(shape) != len(lead) + 2 or shape[:-2] != lead:
+    shape, given = w.shape, x.shape
+    if len(given) != 2 or len(shape) != len(lead) + 2 or shape[:-2] != lead:
         raise ValueError(f"{where}: x must be [rows, K] and w {[*lead, 'N', 'K']}, not "
-                         f"{tuple(x.shape)}, {tuple(shape)}")
+                         f"{tuple(given)}, {tuple(shape)}")
     N, K = shape[-2:]
-    if x.shape[1] != K:
-        raise ValueError(f"{where}: w has {K} columns, x has {x.shape[1]}")
+    if given[1] != K:
+        raise ValueError(f"{where}: w has {K} columns, x has {given[1]}")
     kb, nb = (K + 127) >> 7, (N + 127) >> 7
     # (a scale per 64 columns has enough elements too, and would be read as another's)
     if x_scale.shape[-1:] != (kb,) or w_scale.shape[-2:] != (nb, kb):
@@ -673,8 +673,8 @@ def linear_e4m3(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, x_scale
     m, N, K, flags, y, y_scale = _product("linear_e4m3", w, w_scale, x, x_scale, (), T, out_dtype,
                                           gated, y, y_scale)
     s = _launch_on("linear_e4m3", w=w, w_scale=w_scale, x=x, x_scale=x_scale, y=y, y_scale=y_scale)
-    _check(_abi.lib().moe_linear_scaled(C.addressof(m), N, K, _ptr(x), _ptr(x_scale), T, flags,
-                                        _ptr(y), _ptr(y_scale), s), "moe_linear_scaled")
+    _check(_abi.lib().moe_linear_scaled(C.addressof(m), N, K, x.data_ptr(), x_scale.data_ptr(), T,
+                                        flags, y.data_ptr(), _ptr(y_scale), s), "moe_linear_scaled")
     return (y, y_scale) if gated else y
 
 
@@ -751,14 +751,15 @@ def combine(rows: torch.Tensor, routing: DeviceRouting, weighted: bool = True,
     n, d = rows.shape
     T = _routed("combine", routing, n)
     if y is None:
-        y = torch.empty((T, d), dtype=torch.bfloat16, device=rows.device)
+        y = rows.new_empty((T, d), dtype=torch.bfloat16)
+    else:
+        _need(y, "y", torch.bfloat16, T * d)
     _need(rows, "rows", torch.bfloat16, n * d)
-    _need(y, "y", torch.bfloat16, T * d)
     if base is not None:
         _need(base, "base", torch.bfloat16, T * d)
     s = _launch_on("combine", rows=rows, base=base, y=y, inv_perm=routing.inv_perm)
-    _check(_abi.lib().moe_combine(_ptr(rows), T, routing.k, d, C.addressof(routing.struct),
-                                  0 if weighted else _abi.MOE_UNWEIGHTED, _ptr(base), _ptr(y), s),
+    _check(_abi.lib().moe_combine(rows.data_ptr(), T, routing.k, d, C.addressof(routing.struct),
+                                  0 if weighted else _abi.MOE_UNWEIGHTED, _ptr(base), y.data_ptr(), s),
            "moe_combine")
     return y
 
@@ -788,18 +789,6 @@ def combine_grad(dy: torch.Tensor, rows: torch.Tensor, routing: DeviceRouting,
     _check(_abi.lib().moe_combine_grad(_ptr(dy), _ptr(rows), T, k, d, C.addressof(routing.struct),
                                        _ptr(d_rows), _ptr(d_w), s), "moe_combine_grad")
     return d_rows, d_w
-
-
-def _addr(t) -> int:
-    return 0 if t is None else t.data_ptr()
-
-
-def _per_row(v, name: str, B: int):
-    """(tensor or None, number) of a parameter that is one number or a tensor [B]."""
-    if isinstance(v, torch.Tensor):
-        _need(v, name, torch.float32, B)
-        return v, 0.0
-    return None, v
 
 
 def penalize(logits: torch.Tensor, tokens: torch.Tensor | None = None,
@@ -848,9 +837,16 @@ def penalize(logits: torch.Tensor, tokens: torch.Tensor | None = None,
         if mask.dim() != 2 or tuple(mask.shape) != (B, (V + 31) >> 5):
             raise ValueError(f"mask must be [{B}, {(V + 31) >> 5}], not {tuple(mask.shape)}")
         _need(mask, "mask", torch.int32, 0)
-    rep, rep_all = _per_row(repetition, "repetition", B)
-    freq, freq_all = _per_row(frequency, "frequency", B)
-    pres, pres_all = _per_row(presence, "presence", B)
+    rep = freq = pres = None  # the parameters that are tensors
+    if isinstance(repetition, torch.Tensor):
+        _need(repetition, "repetition", torch.float32, B)
+        rep, repetition = repetition, 0.0
+    if isinstance(frequency, torch.Tensor):
+        _need(frequency, "frequency", torch.float32, B)
+        freq, frequency = frequency, 0.0
+    if isinstance(presence, torch.Tensor):
+        _need(presence, "presence", torch.float32, B)
+        pres, presence = presence, 0.0
     if out is None:
         out = torch.empty_like(logits)
     else:
@@ -859,10 +855,15 @@ def penalize(logits: torch.Tensor, tokens: torch.Tensor | None = None,
                    n_prompt=n_prompt, repetition=rep, frequency=freq, presence=pres,
                    bias_ids=bias_ids, bias=bias, mask=mask)
     # (the struct's bytes: building a ctypes structure of 14 fields costs 2 us)
-    p = _abi.PENALTIES(_addr(tokens), _addr(n_tokens), _addr(n_prompt), _addr(rep), _addr(freq),
-                       _addr(pres), _addr(bias_ids), _addr(bias), _addr(mask), stride, n_bias,
-                       rep_all, freq_all, pres_all)
-    _check(_abi.lib().moe_penalize(_ptr(logits), B, V, p, _ptr(out), s), "moe_penalize")
+    p = _abi.PENALTIES(0 if tokens is None else tokens.data_ptr(),
+                       0 if n_tokens is None else n_tokens.data_ptr(),
+                       0 if n_prompt is None else n_prompt.data_ptr(),
+                       0 if rep is None else rep.data_ptr(), 0 if freq is None else freq.data_ptr(),
+                       0 if pres is None else pres.data_ptr(),
+                       0 if bias_ids is None else bias_ids.data_ptr(),
+                       0 if bias is None else bias.data_ptr(), 0 if mask is None else mask.data_ptr(),
+                       stride, n_bias, repetition, frequency, presence)
+    _check(_abi.lib().moe_penalize(logits.data_ptr(), B, V, p, out.data_ptr(), s), "moe_penalize")
     return out
 
 
