@@ -14,8 +14,8 @@
 // gathered in list order first and compared there.
 // Bound by HBM: 8 bytes per logit; the tokens are read once per chunk, from L2.  In place,
 // logits that nothing touches are neither read nor written.
-// Measured: 64 rows of 248320 with 4000 tokens at most, masks and 100 biases 29 - 32 us (a copy of
-// the logits takes 25), with 32000 tokens 38, with 1000 biases 39; one row 3.8.
+// Measured: 64 rows of 248320 with 4000 tokens at most, masks and 100 biases 29 us (a copy of
+// the logits takes 25), with 32000 tokens 40, with 1000 biases 33; one row 3.8.
 #include "ops.h"
 
 namespace q4moe {
@@ -200,11 +200,13 @@ void launch(const PenalizeArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Chunks of 8192 logits where there are enough of them (the tokens are read once per chunk),
-// down to 1024 so that one row of 248320 still has 243 work groups.
+// Chunks of 4096 logits where there are enough of them (with 8192 there are too few work groups
+// a CU to hide the counting: 64 rows of 248320 with 4000 tokens 28.6 us instead of 30.5), of 8192
+// for long histories, which are read once per chunk (131072 tokens 82 us instead of 88, 32000
+// tokens 40 with both), down to 1024 so that one row of 248320 still has 243 work groups.
 hipError_t launch_penalize(const PenalizeArgs& a, hipStream_t s) {
     const long long logits = (long long)a.B * a.V;
-    if (logits >= 8192LL * 1024) launch<8>(a, s);
+    if (logits >= 8192LL * 1024 && a.tokens && a.stride > 32768) launch<8>(a, s);
     else if (logits >= 4096LL * 1024) launch<4>(a, s);
     else if (logits >= 2048LL * 512) launch<2>(a, s);
     else launch<1>(a, s);
