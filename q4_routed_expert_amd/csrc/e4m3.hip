@@ -217,10 +217,16 @@ struct Int {
 // here a stage's loads are waited for by count, before the barrier that hands the stage out.
 // They have no result registers.  M0 takes the LDS address (one wait state before its use); no
 // other instruction of these kernels reads it.
+// NT: not kept in the caches for others.
+template <bool NT = false>
 __device__ __forceinline__ void load16_lds(const u32x4& rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %0, %2 offen lds"
-                 ::"s"(rsrc), "v"(voff), "s"(soff), "s"(lds) : "memory");
+    if constexpr (NT)
+        asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %0, %2 offen nt lds"
+                     ::"s"(rsrc), "v"(voff), "s"(soff), "s"(lds) : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %0, %2 offen lds"
+                     ::"s"(rsrc), "v"(voff), "s"(soff), "s"(lds) : "memory");
 #endif
 }
 __device__ __forceinline__ void load4_lds(const u32x4& rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
@@ -364,9 +370,14 @@ __global__ __launch_bounds__(WM * WN * 64) void product_tile_kernel(const Produc
         if (l_id >= end) return;
         const uint32_t back = half && l_b == KB - 1 && piece >= 4 ? 64u : 0u;
         const uint32_t to = lds0 + at + 1024u * (uint32_t)wave;
+        auto load_w = [&](auto nt) {
 #pragma unroll
-        for (int j = 0; j < kWLoads; ++j)
-            load16_lds(GATED && j >= kWLoads / 2 ? up_rsrc : w_rsrc, woff[j] - back, l_b * kBlock, to + 1024u * kW * j);
+            for (int j = 0; j < kWLoads; ++j)
+                load16_lds<decltype(nt)::value != 0>(GATED && j >= kWLoads / 2 ? up_rsrc : w_rsrc, woff[j] - back,
+                                                     l_b * kBlock, to + 1024u * kW * j);
+        };
+        if (BM == 32 && BN == 256 && a.stream) load_w(Int<1>{});
+        else load_w(Int<0>{});
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j)
             load16_lds(x_rsrc, xoff[j] - back, l_b * kBlock,
@@ -591,12 +602,20 @@ int tiles_of(ProductArgs& a) {
 //     300 x 2048 x 2048: 16 with 64 x 128, 13.5 with 64 x 64, 14 with 32 x 64; 128 x 4096 x 4096:
 //     27, 21, 17.5.  64 x 128, two stages and three: 512 x 4096 x 4096 in fp32 29.6 and 30.6, in
 //     bf16 24.8 and 20.5 (half the work between two waits).
+//   Matrices that one tile of rows reads, 64 MB and more: their loads ask not to be kept (nt).  With
+//     and without: gated experts, 8 tokens 23.9 and 24.7, 64 tokens 70 and 79, 512 tokens 96 and 105,
+//     768 99 and 104, 1024 111 and 110;
+//     bf16, 64 tokens 37 and 43; 8 tokens, 248320 x 2048: 80 and 91.  Where tiles of rows share
+//     them it costs (64 rows an expert 176 and 157), and where the last-level cache may hold them
+//     from call to call (32 tokens, 2 x 8192 x 2048 gated 20 and 18).
 //   8 tokens, 248320 x 2048: 91 with 32 x 256, 97 with 32 x 64; 60000 rows: 28 and 26.
 hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
     ProductArgs a = a0;
+    const int per = (a.rows + a.E - 1) / a.E;  // rows of an expert on average
+    a.stream = per <= (a.map ? 24 : 32) &&
+               (long long)min(a.rows, a.E) * (a.gated ? 2 : 1) * a.N * a.K >= 64ll << 20;
     auto tiles = [&](int m, int n) { return (long long)((a.rows + m - 1) / m) * ((a.N + n - 1) / n); };
     if (a.map) {
-        const int per = (a.rows + a.E - 1) / a.E;
         if (per <= (a.gated ? 96 : a.out_bf16 ? 16 : 32)) {
             // (one tile a CU at most: all of its LDS for loads in flight)
             const bool few = (long long)min(a.rows, a.E) * ((a.N + (a.gated ? 127 : 255)) / (a.gated ? 128 : 256)) <= kCus;

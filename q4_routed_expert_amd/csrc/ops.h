@@ -120,6 +120,7 @@ struct ProductArgs {
     float* y_scale;           // [rows][ceil(N/128)] when gated
     int rows, N, K;           // N: rows of one part
     bool gated, out_bf16;
+    bool stream;              // matrices are read once (launch_product sets it)
     // expert-sorted rows (E = 1 and NULL otherwise)
     int E;
     const int32_t* offsets;   // [E + 1]
