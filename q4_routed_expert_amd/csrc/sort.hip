@@ -13,8 +13,8 @@
 // brought into it.
 //
 // Measured with d = 2048 and k = 8: dispatch of 2048 tokens in e4m3 8 us (43 MB), of 8192 in
-// bf16 53 us (5.7 TB/s); combine of 8192 tokens 67 us (5.0 TB/s), its gradient 111 us (5.1 TB/s,
-// half of it writes: what a copy reaches).
+// bf16 47 us (6.4 TB/s); combine of 8192 tokens 54 us (6.2 TB/s), its gradient 87 us (6.6 TB/s,
+// half of it writes; a copy reaches 5.1).
 #include "e4m3.h"
 #include "ops.h"
 
@@ -99,7 +99,14 @@ __global__ __launch_bounds__(kThreads) void dispatch_e4m3_kernel(const SortArgs 
     }
 }
 
-template <int K>
+// Sixteen bytes; ONCE: not kept in the caches for others.
+template <bool ONCE>
+__device__ __forceinline__ u32x4 load16(const void* p) {
+    if constexpr (ONCE) return __builtin_nontemporal_load((const u32x4*)p);
+    else return *(const u32x4*)p;
+}
+
+template <int K, bool ONCE>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const SortArgs a) {
     const Piece p = piece_of(a);
     if (!p.live) return;
@@ -109,7 +116,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const SortArgs a) {
     float w[K];
 #pragma unroll
     for (int s = 0; s < K; ++s) {
-        v[s] = *(const u32x4*)(a.rows + row[s] * a.d + p.c);
+        v[s] = load16<ONCE>(a.rows + row[s] * a.d + p.c);
         w[s] = a.w ? a.w[(size_t)p.t * K + s] : 1.0f;
     }
     const size_t at = (size_t)p.t * a.d + p.c;
@@ -135,14 +142,14 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const SortArgs a) {
 }
 
 // One piece of a token's gradients: d_rows of all slots, and what the piece adds to d_w.
-template <int K>
+template <int K, bool ONCE>
 __device__ __forceinline__ void grad_piece(const SortArgs& a, int t, int c, const size_t (&row)[K],
                                            const float (&w)[K], float (&dot)[K]) {
     u32x4 v[K];
     float dy[8], f[8];
 #pragma unroll
-    for (int s = 0; s < K; ++s) v[s] = *(const u32x4*)(a.rows + row[s] * a.d + c);
-    unpack8(*(const u32x4*)(a.dy + (size_t)t * a.d + c), dy);
+    for (int s = 0; s < K; ++s) v[s] = load16<ONCE>(a.rows + row[s] * a.d + c);
+    unpack8(load16<ONCE>(a.dy + (size_t)t * a.d + c), dy);
 #pragma unroll
     for (int s = 0; s < K; ++s) {
         unpack8(v[s], f);
@@ -167,7 +174,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_short_kernel(const Sort
         w[s] = a.w[(size_t)t * K + s];
         dot[s] = 0.0f;
     }
-    if (t0 < a.T && 8 * lane < a.d) grad_piece<K>(a, t, 8 * lane, row, w, dot);
+    if (t0 < a.T && 8 * lane < a.d) grad_piece<K, false>(a, t, 8 * lane, row, w, dot);
 #pragma unroll
     for (int s = 0; s < K; ++s) {
         const float v = group_sum<G>(dot[s]);
@@ -176,7 +183,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_short_kernel(const Sort
 }
 
 // A work group a token.
-template <int K>
+template <int K, bool ONCE>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const SortArgs a) {
     __shared__ float part[K][kThreads / 64];
     const int t = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -188,7 +195,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const SortArgs a
         w[s] = a.w[(size_t)t * K + s];
         dot[s] = 0.0f;
     }
-    for (int c = 8 * (int)threadIdx.x; c < a.d; c += 8 * kThreads) grad_piece<K>(a, t, c, row, w, dot);
+    for (int c = 8 * (int)threadIdx.x; c < a.d; c += 8 * kThreads) grad_piece<K, ONCE>(a, t, c, row, w, dot);
 #pragma unroll
     for (int s = 0; s < K; ++s) {
         const float v = wave_sum_dpp(dot[s]);
@@ -224,6 +231,12 @@ void with_k(int k, F f) {
 }
 static_assert(MOE_MAX_TOPK == 8, "with_k");
 
+// Expert rows that the last-level cache does not hold: loads that ask not to be kept leave it to the
+// stores (d = 2048, k = 8, us with and without: combine of 2048 tokens 16.0 and 14.4, of 3200 23.1
+// and 25.6, of 8192 54 and 64; its gradient 26.0 and 25.2, 38 and 38, 87 and 110.  Stores that ask
+// for it cost: 106).
+bool read_once(const SortArgs& a) { return 2LL * a.T * a.k * a.d >= 96LL << 20; }
+
 unsigned blocks_for(long long threads) { return (unsigned)((threads + kThreads - 1) / kThreads); }
 
 }  // namespace
@@ -244,7 +257,11 @@ hipError_t launch_combine(const SortArgs& a0, hipStream_t s) {
     SortArgs a = a0;
     a.pieces = a.d / 8;
     const unsigned n = blocks_for((long long)a.T * a.pieces);
-    with_k(a.k, [&](auto k) { combine_kernel<decltype(k)::value><<<n, kThreads, 0, s>>>(a); });
+    const bool once = read_once(a);
+    with_k(a.k, [&](auto k) {
+        if (once) combine_kernel<decltype(k)::value, true><<<n, kThreads, 0, s>>>(a);
+        else combine_kernel<decltype(k)::value, false><<<n, kThreads, 0, s>>>(a);
+    });
     trace_point(s);
     return hipGetLastError();
 }
@@ -252,13 +269,15 @@ hipError_t launch_combine(const SortArgs& a0, hipStream_t s) {
 // Rows of up to 512 columns share work groups (30000 tokens of 192 columns, k = 8: 59 us with a
 // work group each).
 hipError_t launch_combine_grad(const SortArgs& a, hipStream_t s) {
+    const bool once = read_once(a);
     with_k(a.k, [&](auto k) {
         constexpr int K = decltype(k)::value;
         if (a.d <= 64) combine_grad_short_kernel<K, 8><<<blocks_for(8LL * a.T), kThreads, 0, s>>>(a);
         else if (a.d <= 128) combine_grad_short_kernel<K, 16><<<blocks_for(16LL * a.T), kThreads, 0, s>>>(a);
         else if (a.d <= 256) combine_grad_short_kernel<K, 32><<<blocks_for(32LL * a.T), kThreads, 0, s>>>(a);
         else if (a.d <= 512) combine_grad_short_kernel<K, 64><<<blocks_for(64LL * a.T), kThreads, 0, s>>>(a);
-        else combine_grad_kernel<K><<<a.T, kThreads, 0, s>>>(a);
+        else if (once) combine_grad_kernel<K, true><<<a.T, kThreads, 0, s>>>(a);
+        else combine_grad_kernel<K, false><<<a.T, kThreads, 0, s>>>(a);
     });
     trace_point(s);
     return hipGetLastError();
