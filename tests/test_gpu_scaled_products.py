@@ -185,6 +185,47 @@ def test_experts_match_the_formula(dev, T, E, k, N, K, skew):
         check_gated(y, y_scale, h, eh)
 
 
+@pytest.mark.parametrize("T,I", [(20, 512), (70, 1024)])
+def test_large_expert_matrices_of_few_rows(dev, T, I):
+    # more than 64 MB of matrices, each read by one tile of rows; a last half block
+    E, k, K = 64, 2, 2112
+    rng = np.random.default_rng(I)
+    idx, wt = selections(rng, T, E, k)
+    r, o = device_routing(idx, wt, E, dev)
+    x, xs = quantised_rows(rng, T * k, K)
+    codes = torch.randint(0, 0x60, (E, 2, I, K), dtype=torch.uint8, device=dev)
+    w = (codes | (torch.randint(0, 2, codes.shape, dtype=torch.uint8, device=dev) << 7)).view(f8)
+    ws = torch.rand(E, 2, I // 128, -(-K // 128), device=dev) * 2.0 ** -8
+    xd, xsd = x.to(dev), xs.to(dev)
+    y, y_scale = q4.experts_e4m3(w, ws, xd, xsd, r, gated=True)
+    w0 = w.view(E, 2 * I, K)  # the two of an expert as one
+    ws0 = ws.view(E, -1, ws.shape[-1])
+    z = q4.experts_e4m3(w0, ws0, xd, xsd, r)
+    for e in range(E):
+        a, b = int(o["offsets"][e]), int(o["offsets"][e + 1])
+        if a == b:
+            continue
+        h, eh = gated(w[e].cpu(), ws[e].cpu(), x[a:b], xs[a:b])
+        check_gated(y[a:b], y_scale[a:b], h, eh)
+        want, size = plain.product(values(w0[e]), ws0[e].cpu().numpy(), values(x[a:b]), xs[a:b].numpy())
+        check(z[a:b], want, bar_of(size, K) + np.abs(want) * 2.0 ** -8 + CUT * size)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_a_large_matrix_of_few_rows(dev, out):
+    T, N, K = 5, 140001, 576
+    rng = np.random.default_rng(6)
+    x, xs = quantised_rows(rng, T, K)
+    w = torch.randint(0, 0x60, (N, K), dtype=torch.uint8, device=dev).view(f8)
+    ws = torch.rand(-(-N // 128), -(-K // 128), device=dev)
+    y = q4.linear_e4m3(w, ws, x.to(dev), xs.to(dev), out_dtype=out)
+    for a, b in ((0, 384), (70016, 70400), (N // 128 * 128 - 256, N)):
+        want, size = plain.product(values(w[a:b]), ws[a // 128:-(-b // 128)].cpu().numpy(), values(x),
+                                   xs.numpy())
+        check(y[:, a:b], want, bar_of(size, K) + (np.abs(want) * 2.0 ** -8 + CUT * size
+                                                  if out == torch.bfloat16 else 0))
+
+
 @pytest.mark.parametrize("T,N,K", [(3, 70, 192), (140, 300, 320), (300, 260, 448)])
 def test_special_values(dev, T, N, K):
     rng = np.random.default_rng(N)
