@@ -376,7 +376,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_tile_kernel(const Produc
                 load16_lds<decltype(nt)::value != 0>(GATED && j >= kWLoads / 2 ? up_rsrc : w_rsrc, woff[j] - back,
                                                      l_b * kBlock, to + 1024u * kW * j);
         };
-        if (BM == 32 && BN == 256 && a.stream) load_w(Int<1>{});
+        if ((BM == 32 || MAPPED) && BN == 256 && a.stream) load_w(Int<1>{});
         else load_w(Int<0>{});
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j)
@@ -604,7 +604,8 @@ int tiles_of(ProductArgs& a) {
 //     bf16 24.8 and 20.5 (half the work between two waits).
 //   Matrices that one tile of rows reads, 64 MB and more: their loads ask not to be kept (nt).  With
 //     and without: gated experts, 8 tokens 23.9 and 24.7, 64 tokens 70 and 79, 512 tokens 96 and 105,
-//     768 99 and 104, 1024 111 and 110;
+//     768 99 and 104, 1024 111 and 110; tiles of 128
+//     rows, bf16, K = 512: 32 rows 58 and 62, 64 rows 71 and 73, 128 rows, skewed, 105 and 96;
 //     bf16, 64 tokens 37 and 43; 8 tokens, 248320 x 2048: 80 and 91.  Where tiles of rows share
 //     them it costs (64 rows an expert 176 and 157), and where the last-level cache may hold them
 //     from call to call (32 tokens, 2 x 8192 x 2048 gated 20 and 18).
@@ -612,11 +613,12 @@ int tiles_of(ProductArgs& a) {
 hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
     ProductArgs a = a0;
     const int per = (a.rows + a.E - 1) / a.E;  // rows of an expert on average
-    a.stream = per <= (a.map ? 24 : 32) &&
+    const bool low = per <= (a.gated ? 96 : a.out_bf16 ? 16 : 32);  // mapped: tiles of 32 rows, else 128
+    a.stream = per <= (!a.map ? 32 : low ? 24 : 64) &&
                (long long)min(a.rows, a.E) * (a.gated ? 2 : 1) * a.N * a.K >= 64ll << 20;
     auto tiles = [&](int m, int n) { return (long long)((a.rows + m - 1) / m) * ((a.N + n - 1) / n); };
     if (a.map) {
-        if (per <= (a.gated ? 96 : a.out_bf16 ? 16 : 32)) {
+        if (low) {
             // (one tile a CU at most: all of its LDS for loads in flight)
             const bool few = (long long)min(a.rows, a.E) * ((a.N + (a.gated ? 127 : 255)) / (a.gated ? 128 : 256)) <= kCus;
             if (a.gated && few) launch_tile<32, 256, 1, 8, 4, false, true, true>(a, tiles_of<32>(a), s);

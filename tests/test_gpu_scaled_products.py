@@ -185,7 +185,7 @@ def test_experts_match_the_formula(dev, T, E, k, N, K, skew):
         check_gated(y, y_scale, h, eh)
 
 
-@pytest.mark.parametrize("T,I", [(20, 512), (70, 1024)])
+@pytest.mark.parametrize("T,I", [(20, 512), (70, 1024), (700, 512)])
 def test_large_expert_matrices_of_few_rows(dev, T, I):
     # more than 64 MB of matrices, each read by one tile of rows; a last half block
     E, k, K = 64, 2, 2112
