@@ -13,8 +13,9 @@
 // brought into it.
 //
 // Measured with d = 2048 and k = 8: dispatch of 2048 tokens in e4m3 8 us (43 MB), of 8192 in
-// bf16 47 us (6.4 TB/s); combine of 8192 tokens 54 us (6.2 TB/s), its gradient 87 us (6.6 TB/s,
-// half of it writes; a copy reaches 5.1).
+// bf16 61 us (5.0 TB/s); combine of 8192 tokens 54 us (6.2 TB/s), its gradient 116 us (4.9 TB/s,
+// half of it writes; a copy reaches 5.1), all with outputs that no cache holds; into the buffers of
+// the call before 47, 54 and 87.
 #include "e4m3.h"
 #include "ops.h"
 
@@ -233,8 +234,9 @@ static_assert(MOE_MAX_TOPK == 8, "with_k");
 
 // Expert rows that the last-level cache does not hold: loads that ask not to be kept leave it to the
 // stores (d = 2048, k = 8, us with and without: combine of 2048 tokens 16.0 and 14.4, of 3200 23.1
-// and 25.6, of 8192 54 and 64; its gradient 26.0 and 25.2, 38 and 38, 87 and 110.  Stores that ask
-// for it cost: 106).
+// and 25.6, of 8192 54 and 65; its gradient of 3200 38 and 38, of 8192 116 and 116, into the buffer of
+// the call before 87 and 110.  Stores that ask for it too: 111, and 106 into that buffer, so they
+// do not).
 bool read_once(const SortArgs& a) { return 2LL * a.T * a.k * a.d >= 96LL << 20; }
 
 unsigned blocks_for(long long threads) { return (unsigned)((threads + kThreads - 1) / kThreads); }
