@@ -14,8 +14,8 @@
 // gathered in list order first and compared there.
 // Bound by HBM: 8 bytes per logit; the tokens are read once per chunk, from L2.  In place,
 // logits that nothing touches are neither read nor written.
-// Measured: 64 rows of 248320 with 4000 tokens at most, masks and 100 biases 29 us (a copy of
-// the logits takes 25), with 32000 tokens 40, with 1000 biases 33; one row 3.8.
+// Measured: 64 rows of 248320 with 4000 tokens at most, masks and 100 biases 26 us (a copy of
+// the logits takes 25), with 32000 tokens 39, with 1000 biases 32; one row 3.8.
 #include "ops.h"
 
 namespace q4moe {
@@ -32,17 +32,23 @@ struct __attribute__((packed, aligned(4))) Four {
     T v[4];
 };
 
-// Four logits at `at` of a row; the last ones may lie behind its end.
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+// Four logits at `at` of a row; the last ones may lie behind its end.  STREAM: not kept in the caches.
+template <bool STREAM>
 __device__ __forceinline__ Four<float> load4(const float* row, int at, int n) {
+    if (at + 4 <= n) {
+        if constexpr (STREAM) return __builtin_bit_cast(Four<float>, __builtin_nontemporal_load((const f32x4_any*)(row + at)));
+        else return *(const Four<float>*)(row + at);
+    }
     Four<float> f;
-    if (at + 4 <= n) return *(const Four<float>*)(row + at);
 #pragma unroll
     for (int i = 0; i < 4; ++i) f.v[i] = at + i < n ? row[at + i] : 0.0f;
     return f;
 }
 
 // NV pieces of four logits per thread: a chunk is 1024 NV logits.
-template <int NV, bool IN_PLACE>
+template <int NV, bool IN_PLACE, bool STREAM>
 __global__ __launch_bounds__(kThreads) void penalize_kernel(const PenalizeArgs a) {
     constexpr int kChunk = NV * 4 * kThreads;
     __shared__ u32x4 count4[kChunk / 4];
@@ -59,7 +65,7 @@ __global__ __launch_bounds__(kThreads) void penalize_kernel(const PenalizeArgs a
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int at = 4 * (tid + kThreads * j);
-        if constexpr (!IN_PLACE) l[j] = load4(in, at, n);
+        if constexpr (!IN_PLACE) l[j] = load4<STREAM>(in, at, n);
         allowed[j] = mask && at < n ? mask[(v0 + at) >> 5] : 0xFFFFFFFFu;
     }
     if (a.tokens || a.n_bias) {
@@ -118,7 +124,7 @@ __global__ __launch_bounds__(kThreads) void penalize_kernel(const PenalizeArgs a
         if (a.tokens) m = count4[tid + kThreads * j];
         if constexpr (IN_PLACE) {
             if (bits == 15u && ((m[0] | m[1] | m[2] | m[3]) & ~kBiased) == 0u) continue;
-            l[j] = load4(in, at, n);
+            l[j] = load4<STREAM>(in, at, n);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -132,7 +138,8 @@ __global__ __launch_bounds__(kThreads) void penalize_kernel(const PenalizeArgs a
             l[j].v[i] = (bits >> i) & 1u ? x : -INFINITY;
         }
         if (at + 4 <= n) {
-            *(Four<float>*)(out + at) = l[j];
+            if constexpr (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(f32x4_any, l[j]), (f32x4_any*)(out + at));
+            else *(Four<float>*)(out + at) = l[j];
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -191,11 +198,16 @@ __global__ __launch_bounds__(kThreads) void penalize_kernel(const PenalizeArgs a
     }
 }
 
+// 8 to 128 MB of logits pass the caches by: 64 rows 26 us instead of 29 into the buffer of the
+// call before and of 33 into a new one, with the sampler after it 98 and 97; 16 rows 10 and 12,
+// 52 and 53.  (Of 300 rows of 152000 the sampler loses more than that: 205 us for both instead of 200.)
 template <int NV>
 void launch(const PenalizeArgs& a, hipStream_t s) {
     const dim3 grid((a.V + NV * 4 * kThreads - 1) / (NV * 4 * kThreads), a.B);
-    if (a.out == a.logits) penalize_kernel<NV, true><<<grid, kThreads, 0, s>>>(a);
-    else penalize_kernel<NV, false><<<grid, kThreads, 0, s>>>(a);
+    const long long logits = (long long)a.B * a.V;
+    if (a.out == a.logits) penalize_kernel<NV, true, false><<<grid, kThreads, 0, s>>>(a);
+    else if (NV > 1 && logits >= 2LL << 20 && logits <= 32LL << 20) penalize_kernel<NV, false, NV != 1><<<grid, kThreads, 0, s>>>(a);
+    else penalize_kernel<NV, false, false><<<grid, kThreads, 0, s>>>(a);
 }
 
 }  // namespace

@@ -88,7 +88,8 @@ SHAPES = [(1, 1, 1, 0, 0.0), (1, 33, 7, 3, 0.5), (2, 1000, 0, 5, 0.0), (3, 3001,
           (5, 4096, 50, 0, 0.5), (4, 8195, 3000, 300, 0.99), (2, 50000, 20000, 7, 0.3),
           (1, 248320, 2000, 0, 0.0), (3, 70001, None, 1024, 0.5), (65, 2049, 90, 0, 0.2),
           (7, 30000, 400, 1, 0.0), (64, 20003, 100, 10, 0.7), (40, 220001, 9, 1000, 0.0),
-          (2, 6000, 300, 1024, 0.0), (34, 248320, 33000, 9, 0.3)]
+          (2, 6000, 300, 1024, 0.0), (34, 248320, 33000, 9, 0.3),
+          (11, 248319, 50, 5, 0.1)]
 
 
 @pytest.mark.parametrize("B,V,L,n_bias,masked", SHAPES)
