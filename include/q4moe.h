@@ -412,8 +412,10 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
    the matrix:
      y[t][n] = sum_b xs[t][b] * ws[n / 128][b] * sum_{k in block b} x[t][k] * w(n, k)
    with exact products, a block's sum in fp32 and the blocks added in
-   fp32; only for bf16 outputs (of calls large enough to be bound by the matrix cores) a
-   product may be cut at 2^-13 of the largest among its eight columns 8 i .. 8 i + 7.
+   fp32.  Only in bf16 outputs of calls of 128 rows or more (T >= 128; of experts T * k >=
+   128 * E), which the matrix cores bound, each product may lose its bits below 2^-13 of the
+   power of two in the largest product of its eight columns 8 i .. 8 i + 7: small products next
+   to large ones that cancel.
    A last block of columns or rows may be shorter than 128.  A NaN code or a scale that is
    not finite gives what the formula gives.
    y: fp32 [T][N], or bf16 (one rounding) with MOE_OUT_BF16, or with MOE_GATED 8 bits:

@@ -666,7 +666,8 @@ def linear_e4m3(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, x_scale
     """y [T, N] = x times the transposed matrix w, both e4m3: x [T, K] with x_scale
     [T, ceil(K / 128)], w [N, K] with w_scale [ceil(N / 128), ceil(K / 128)]; out_dtype
     bf16 or fp32.  gated: w is [2, I, K] (gate, up) with w_scale [2, ceil(I / 128), ...],
-    and (y e4m3 [T, I], y_scale [T, ceil(I / 128)]) of silu(gate) * up is returned."""
+    and (y e4m3 [T, I], y_scale [T, ceil(I / 128)]) of silu(gate) * up is returned.  In bf16
+    from T = 128 on, small products next to large ones that cancel may be lost: fp32 keeps them."""
     if stream is not None:
         return _on_stream(linear_e4m3, locals())
     T = x.shape[0]
@@ -696,7 +697,8 @@ def experts_e4m3(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, x_scal
                  gated: bool = False, y: torch.Tensor | None = None,
                  y_scale: torch.Tensor | None = None, stream=None):
     """linear_e4m3 over the expert-sorted rows of a routing (dispatch's), with a matrix per
-    expert: x [T * k, K], w [E, N, K] (gated: [E, 2, I, K]), the scales likewise."""
+    expert: x [T * k, K], w [E, N, K] (gated: [E, 2, I, K]), the scales likewise.  What it says
+    of T = 128 is so for 128 rows of an expert on average, T * k >= 128 * E."""
     if stream is not None:
         return _on_stream(experts_e4m3, locals())
     rows = x.shape[0]

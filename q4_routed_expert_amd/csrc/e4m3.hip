@@ -8,9 +8,11 @@
 // as B; then the block's fp32 sum is scaled and added by four fused multiply-adds.  The matrix
 // cores' own e4m3 products are twice as fast (3670 instead of 1830 TFLOP/s, nothing else
 // running), but they cut every product at 13 bits below the largest among eight columns: sums
-// of 128 normally distributed values came out 1.5e-5 off (2-norm), through bf16 9e-9.  That is
-// far below the rounding of a bf16 output (2e-3), and so those take them, where there is enough
-// work; fp32 outputs and the scales of gated ones would show it.
+// of 128 normally distributed values came out 1.5e-5 off (2-norm), through bf16 9e-9.  In usual sums
+// that is far below the rounding of a bf16 output (2e-3), but where large products cancel, small
+// ones next to them are lost.  So bf16 outputs take them from 128 rows (of an expert, on average)
+// on, where a product is bound by the matrix cores: 2 rows operations a byte of W at 1227 TFLOP/s
+// and 5.1 TB/s meet at 120.  fp32 outputs and the scales of gated ones would show them always.
 // A block's sum is the same in any order of its columns, as long as A and B hold the same
 // ones: lane (r = lane & 15, g = lane >> 4) holds columns 32 g .. + 31 of row r of both.  In D
 // lane (c, g) holds token c, weight rows 4 g .. + 3, so a lane's factor xs * ws is one number
@@ -289,7 +291,7 @@ __device__ __forceinline__ void tile_products(f32x4 (&d)[NT], const i32x8 (&w)[N
         d[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[i], x, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
 }
 
-// E4M3: the matrix cores' own 8-bit products (see the top), for bf16 outputs.
+// E4M3: the matrix cores' own 8-bit products (see the top).
 template <int BM, int BN, int WM, int WN, int S, bool E4M3, bool GATED, bool MAPPED>
 __global__ __launch_bounds__(WM * WN * 64) void product_tile_kernel(const ProductArgs a) {
     constexpr int kW = WM * WN;
@@ -590,8 +592,14 @@ int tiles_of(ProductArgs& a) {
 // product, smaller ones fill the chip.  Measured at the borders (us):
 //   experts, rows of an expert on average: gated, 2 x 512 rows, K = 2048: 32 rows 110 with tiles
 //     of 32 rows and two work groups a CU, 123 with one, 131 with tiles of 128; 64 rows 157, 178
-//     and 171; 128 rows 251, 292 and 232; 8 tokens (228 tiles) 25.8 and 25.1.  bf16, K = 512: 8
-//     rows 52 and 54; 16 rows 55 and 54; 64 rows 95 and 72.
+//     and 171; 128 rows 251, 292 and 232; 8 tokens (228 tiles) 25.8 and 25.1.  Not gated, tiles of
+//     32 rows and of 128: 256 experts, 2048 rows, K = 512 in bf16, 24 rows 59.6 and 60.1, 32 rows
+//     67.6 and 63.8, 40 rows 78 and 71, in fp32 66.8 and 64.6, 71.4 and 73.7, 87 and 76; 64 experts,
+//     700 rows, K = 1088, bf16, 24 rows 14.0 and 20.2, 32 rows 22.8 and 21.7; 8 experts, 4096 x 4096,
+//     24 rows 42 and 53, 32 rows 44 and 58.
+//   exact products of bf16 outputs and cut ones: 64 rows, 8192 x 8192 30 and 22, 40001 x 2048 26 and
+//     24; 128 rows, 4096 x 4096 16.7 and 12.7, 128256 x 4096 163 and 167; 256 rows of that 288 and
+//     179; experts, 2048 rows, K = 512: 32 rows 64.8 and 58.1, 64 rows 83 and 71, 128 rows 121 and 96.
 //   gated: 128 x 2 x 8192 x 2048 20 with tiles of 32 rows, 37 with 128; 512 rows 67 and 42;
 //     300 x 2 x 2048 x 2048 19, 25 with 64, 36 with 128.
 //   one token, 8192 x 8192: 15 in the few-token kernel, 30 in 32 x 64 tiles; 16 tokens, 16384 x
@@ -613,7 +621,8 @@ int tiles_of(ProductArgs& a) {
 hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
     ProductArgs a = a0;
     const int per = (a.rows + a.E - 1) / a.E;  // rows of an expert on average
-    const bool low = per <= (a.gated ? 96 : a.out_bf16 ? 16 : 32);  // mapped: tiles of 32 rows, else 128
+    const bool cut = a.out_bf16 && a.rows >= 128 * a.E;  // the matrix cores' own 8-bit products
+    const bool low = per <= (a.gated ? 96 : 32);  // mapped: tiles of 32 rows, else 128
     a.stream = per <= (!a.map ? 32 : low ? 24 : 64) &&
                (long long)min(a.rows, a.E) * (a.gated ? 2 : 1) * a.N * a.K >= 64ll << 20;
     auto tiles = [&](int m, int n) { return (long long)((a.rows + m - 1) / m) * ((a.N + n - 1) / n); };
@@ -626,7 +635,7 @@ hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
             else launch_tile<32, 256, 1, 8, 4, false, false, true>(a, tiles_of<32>(a), s);
         } else {
             if (a.gated) launch_tile<128, 256, 2, 4, 3, false, true, true>(a, tiles_of<128>(a), s);
-            else if (a.out_bf16) launch_tile<128, 256, 2, 4, 3, true, false, true>(a, tiles_of<128>(a), s);
+            else if (cut) launch_tile<128, 256, 2, 4, 3, true, false, true>(a, tiles_of<128>(a), s);
             else launch_tile<128, 256, 2, 4, 3, false, false, true>(a, tiles_of<128>(a), s);
         }
     } else if (a.gated) {
@@ -638,21 +647,21 @@ hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
     } else if (tiles(32, 16) <= kCus) {
         launch_split<2>(a, s);
     } else if (a.rows > 128 && tiles(256, 256) >= kCus) {
-        if (a.out_bf16) launch_tile<256, 256, 2, 4, 2, true, false, false>(a, tiles_of<256>(a), s);
+        if (cut) launch_tile<256, 256, 2, 4, 2, true, false, false>(a, tiles_of<256>(a), s);
         else launch_tile<128, 256, 2, 4, 3, false, false, false>(a, tiles_of<128>(a), s);
     } else if (a.rows > 64 && tiles(128, 128) > kCus) {
-        if (a.out_bf16) launch_tile<128, 128, 2, 4, 2, true, false, false>(a, tiles_of<128>(a), s);
+        if (cut) launch_tile<128, 128, 2, 4, 2, true, false, false>(a, tiles_of<128>(a), s);
         else launch_tile<128, 128, 2, 2, 2, false, false, false>(a, tiles_of<128>(a), s);
     } else if (a.rows > 32 && tiles(64, 128) >= 224) {
-        if (a.out_bf16) launch_tile<64, 128, 2, 4, 3, true, false, false>(a, tiles_of<64>(a), s);
+        if (cut) launch_tile<64, 128, 2, 4, 3, true, false, false>(a, tiles_of<64>(a), s);
         else launch_tile<64, 128, 2, 4, 2, false, false, false>(a, tiles_of<64>(a), s);
     } else if (a.rows > 32 && tiles(64, 64) >= 160) {
-        if (a.out_bf16) launch_tile<64, 64, 2, 4, 3, true, false, false>(a, tiles_of<64>(a), s);
+        if (cut) launch_tile<64, 64, 2, 4, 3, true, false, false>(a, tiles_of<64>(a), s);
         else launch_tile<64, 64, 2, 4, 3, false, false, false>(a, tiles_of<64>(a), s);
     } else if (a.rows <= 32 && tiles(32, 256) >= 2 * kCus) {
         launch_tile<32, 256, 1, 8, 4, false, false, false>(a, tiles_of<32>(a), s);
     } else {
-        if (a.out_bf16) launch_tile<32, 64, 2, 4, 4, true, false, false>(a, tiles_of<32>(a), s);
+        if (cut) launch_tile<32, 64, 2, 4, 4, true, false, false>(a, tiles_of<32>(a), s);
         else launch_tile<32, 64, 2, 4, 4, false, false, false>(a, tiles_of<32>(a), s);
     }
     trace_point(s);
