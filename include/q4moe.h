@@ -467,7 +467,8 @@ int moe_experts_scaled(const moe_e4m3mat* m, int32_t E, int32_t N, int32_t K, co
      d_rows[inv_perm[t * k + s]] = w[t][s] * dy[t]     bf16 [T * k][d], may be rows
      d_w[t][s] = sum over columns of rows[inv_perm[t * k + s]] * dy[t]   fp32 [T][k]
    (base's gradient is dy itself).  d_w is that of the weights as they are used, before
-   any renormalisation that made them. */
+   any renormalisation that made them; that of a slot of weight 0 is 0 where the sum is
+   not finite. */
 #define MOE_UNWEIGHTED 1u
 int moe_dispatch(const uint16_t* x, int32_t T, int32_t k, int32_t d, const moe_routing* r,
                  void* rows, float* rows_scale, void* stream);

@@ -769,7 +769,8 @@ def combine(rows: torch.Tensor, routing: DeviceRouting, weighted: bool = True,
 def combine_grad(dy: torch.Tensor, rows: torch.Tensor, routing: DeviceRouting,
                  d_rows: torch.Tensor | None = None, d_w: torch.Tensor | None = None, stream=None):
     """combine's gradients from dy [T, d] (bf16): (d_rows bf16 [T * k, d], d_w fp32 [T, k]).
-    d_rows may be rows; base's gradient is dy."""
+    d_rows may be rows; base's gradient is dy.  d_w of a slot of weight 0 is 0 where its row
+    makes it not finite."""
     if stream is not None:
         return _on_stream(combine_grad, locals())
     if dy.dim() != 2 or rows.dim() != 2 or dy.shape[1] != rows.shape[1]:

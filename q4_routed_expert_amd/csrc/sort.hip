@@ -162,6 +162,12 @@ __device__ __forceinline__ void grad_piece(const SortArgs& a, int t, int c, cons
     }
 }
 
+// d_w of a slot of weight w whose row and dy have the sum v: a slot of weight 0 counts for nothing,
+// so what its row holds (nothing that was ever written, say) makes no NaN or infinity here.
+__device__ __forceinline__ float weight_grad(float w, float v) {
+    return w == 0.0f && !__builtin_isfinite(v) ? 0.0f : v;
+}
+
 // Rows of up to 8 G columns: G lanes a token.
 template <int K, int G>
 __global__ __launch_bounds__(kThreads) void combine_grad_short_kernel(const SortArgs a) {
@@ -179,7 +185,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_short_kernel(const Sort
 #pragma unroll
     for (int s = 0; s < K; ++s) {
         const float v = group_sum<G>(dot[s]);
-        if (lane == 0 && t0 < a.T) a.d_w[(size_t)t * K + s] = v;
+        if (lane == 0 && t0 < a.T) a.d_w[(size_t)t * K + s] = weight_grad(w[s], v);
     }
 }
 
@@ -207,7 +213,8 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(const SortArgs a
         float v = part[threadIdx.x][0];
 #pragma unroll
         for (int i = 1; i < kThreads / 64; ++i) v += part[threadIdx.x][i];
-        a.d_w[(size_t)t * K + threadIdx.x] = v;
+        const size_t at = (size_t)t * K + threadIdx.x;
+        a.d_w[at] = weight_grad(a.w[at], v);
     }
 }
 
