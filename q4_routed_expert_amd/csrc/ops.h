@@ -139,14 +139,14 @@ struct SortArgs {
     int pieces;               // threads a token (the launchers set it)
     int T, k, d;
     const uint16_t* x;        // dispatch: bf16 [T][d]
-    void* rows_out;           // bf16 or e4m3 [T*k][d] (combine_grad: d_rows or NULL)
+    void* rows_out;           // bf16 or e4m3 [T*k][d] (combine_grad: d_rows)
     float* scale_out;         // dispatch in e4m3: [T*k][ceil(d/128)], or NULL
     const uint16_t* rows;     // combine, combine_grad: bf16 [T*k][d]
     const float* w;           // [T][k] or NULL (all 1)
     const uint16_t* base;     // combine: bf16 [T][d] or NULL
     uint16_t* y;              // combine: bf16 [T][d]
     const uint16_t* dy;       // combine_grad: bf16 [T][d]
-    float* d_w;               // combine_grad: [T][k] or NULL
+    float* d_w;               // combine_grad: [T][k]
 };
 hipError_t launch_dispatch(const SortArgs& a, hipStream_t s);
 hipError_t launch_combine(const SortArgs& a, hipStream_t s);
