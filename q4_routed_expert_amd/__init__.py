@@ -32,6 +32,10 @@ Experts in 8 bits (e4m3, a scale per token and 128 columns and per 128 x 128 wei
     h, h_s = experts_e4m3(w13, s13, rows, rows_s, r, gated=True)
     y = combine(experts_e4m3(w2, s2, h, h_s, r), r, base=shared)
     logits = linear_e4m3(w, s, *add_norm(x, w, e4m3=True, group=128)[1:])
+
+No call records an autograd graph.  dispatch and combine have gradients, as calls of their own
+(combine unweighted, combine_grad); where a graph is being recorded they refuse tensors that
+require a gradient (call them under torch.no_grad(), or from a torch.autograd.Function).
 """
 from __future__ import annotations
 
@@ -713,6 +717,14 @@ def experts_e4m3(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, x_scal
     return (y, y_scale) if gated else y
 
 
+def _no_graph(where: str, gradient: str, **tensors):
+    """Refuses inputs whose gradient would be lost unseen."""
+    for name, t in tensors.items():
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{where}: {name} requires a gradient, and the call records no graph: call "
+                             f"it under torch.no_grad() or from a torch.autograd.Function ({gradient})")
+
+
 def dispatch(x: torch.Tensor, routing: DeviceRouting, e4m3: bool = False,
              rows: torch.Tensor | None = None, rows_scale: torch.Tensor | None = None, stream=None):
     """Token rows x [T, d] (bf16) in expert order, k of each: (rows [T * k, d], None), or
@@ -735,6 +747,7 @@ def dispatch(x: torch.Tensor, routing: DeviceRouting, e4m3: bool = False,
     _need(rows, "rows", dt, n * d)
     if e4m3:
         _need(rows_scale, "rows_scale", torch.float32, n * _blocks(d))
+    _no_graph("dispatch", "its gradient is combine(d_rows, routing, weighted=False)", x=x)
     s = _launch_on("dispatch", x=x, rows=rows, rows_scale=rows_scale, inv_perm=routing.inv_perm)
     _check(_abi.lib().moe_dispatch(_ptr(x), T, routing.k, d, C.addressof(routing.struct),
                                    _ptr(rows), _ptr(rows_scale), s), "moe_dispatch")
@@ -759,6 +772,8 @@ def combine(rows: torch.Tensor, routing: DeviceRouting, weighted: bool = True,
     _need(rows, "rows", torch.bfloat16, n * d)
     if base is not None:
         _need(base, "base", torch.bfloat16, T * d)
+    _no_graph("combine", "its gradients are combine_grad's", rows=rows, base=base,
+              topk_w=routing.topk_w if weighted else None)
     s = _launch_on("combine", rows=rows, base=base, y=y, inv_perm=routing.inv_perm)
     _check(_abi.lib().moe_combine(rows.data_ptr(), T, routing.k, d, C.addressof(routing.struct),
                                   0 if weighted else _abi.MOE_UNWEIGHTED, _ptr(base), y.data_ptr(), s),
