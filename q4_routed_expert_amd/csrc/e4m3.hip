@@ -606,10 +606,15 @@ int tiles_of(ProductArgs& a) {
 //     4096: 22 and 18.  32 tokens, 4096 x 4096: 11 and 17; 128 tokens, 2048 x 2048: 13 and 10.
 //   2048 x 4096 x 4096, fp32: 79 with tiles of 128 x 128 (two work groups of four waves a CU; 88
 //     with one of eight), 90 with 64 x 128; bf16: 46 (two of eight waves; one: 52, two of four:
-//     50); 512 rows, fp32: 43 and 31;
-//     300 x 2048 x 2048: 16 with 64 x 128, 13.5 with 64 x 64, 14 with 32 x 64; 128 x 4096 x 4096:
-//     27, 21, 17.5.  64 x 128, two stages and three: 512 x 4096 x 4096 in fp32 29.6 and 30.6, in
-//     bf16 24.8 and 20.5 (half the work between two waits).
+//     50).  128 x 128 and 64 x 128: 512 rows of that, fp32 43 and 31, 1100 rows, fp32 62 and 56,
+//     bf16 39 and 41.
+//   The next larger of 32 x 64, 64 x 64 and 64 x 128 as soon as the smaller ones are more than the
+//     CUs, fp32 / bf16: 128 x 4096 x 2048 (256 of 32 x 64) 10.3 with those and 12.0 with 64 x 64 /
+//     8.2 and 9.1, 128 x 4608 x 2048 (288) 13.7 and 12.1 / 11.6 and 9.2, 128 x 5000 x 576 6.9 and
+//     5.9 / 6.1 and 5.0; 64 x 16384 x 4096 (256 of 64 x 64) 21.3 with those and 25.2 with 64 x 128,
+//     60 x 17000 x 4096 (266) 30.3 and 25.4, 256 x 5120 x 4096 (320) 31 and 26 / 21.4 and 18.0.
+//   64 x 128, two stages and three: 512 x 4096 x 4096 in fp32 29.6 and 30.6, in bf16 24.8 and 20.5
+//     (half the work between two waits).
 //   Matrices that one tile of rows reads, 64 MB and more: their loads ask not to be kept (nt).  With
 //     and without: gated experts, 8 tokens 23.9 and 24.7, 64 tokens 70 and 79, 512 tokens 96 and 105,
 //     768 99 and 104, 1024 111 and 110; tiles of 128
@@ -652,10 +657,10 @@ hipError_t launch_product(const ProductArgs& a0, hipStream_t s) {
     } else if (a.rows > 64 && tiles(128, 128) > kCus) {
         if (cut) launch_tile<128, 128, 2, 4, 2, true, false, false>(a, tiles_of<128>(a), s);
         else launch_tile<128, 128, 2, 2, 2, false, false, false>(a, tiles_of<128>(a), s);
-    } else if (a.rows > 32 && tiles(64, 128) >= 224) {
+    } else if (a.rows > 32 && tiles(64, 64) > kCus) {
         if (cut) launch_tile<64, 128, 2, 4, 3, true, false, false>(a, tiles_of<64>(a), s);
         else launch_tile<64, 128, 2, 4, 2, false, false, false>(a, tiles_of<64>(a), s);
-    } else if (a.rows > 32 && tiles(64, 64) >= 160) {
+    } else if (a.rows > 32 && tiles(32, 64) > kCus) {
         if (cut) launch_tile<64, 64, 2, 4, 3, true, false, false>(a, tiles_of<64>(a), s);
         else launch_tile<64, 64, 2, 4, 3, false, false, false>(a, tiles_of<64>(a), s);
     } else if (a.rows <= 32 && tiles(32, 256) >= 2 * kCus) {
