@@ -14,8 +14,9 @@
 // gathered in list order first and compared there.
 // Bound by HBM: 8 bytes per logit; the tokens are read once per chunk, from L2.  In place,
 // logits that nothing touches are neither read nor written.
-// Measured: 64 rows of 248320 with 4000 tokens at most, masks and 100 biases 26 us (a copy of
-// the logits takes 25), with 32000 tokens 39, with 1000 biases 32; one row 3.8.
+// Measured: 64 rows of 248320 with 4000 tokens at most, masks and 100 biases 32 us into a new buffer
+// and 28 into that of the call before (a copy of the logits takes 25), in place 25.5; with 32000
+// tokens 44, 39 and 34, with 1000 biases 37, 33 and 31; one row 3.8.
 #include "ops.h"
 
 namespace q4moe {
@@ -32,15 +33,9 @@ struct __attribute__((packed, aligned(4))) Four {
     T v[4];
 };
 
-typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-
-// Four logits at `at` of a row; the last ones may lie behind its end.  STREAM: not kept in the caches.
-template <bool STREAM>
+// Four logits at `at` of a row; the last ones may lie behind its end.
 __device__ __forceinline__ Four<float> load4(const float* row, int at, int n) {
-    if (at + 4 <= n) {
-        if constexpr (STREAM) return __builtin_bit_cast(Four<float>, __builtin_nontemporal_load((const f32x4_any*)(row + at)));
-        else return *(const Four<float>*)(row + at);
-    }
+    if (at + 4 <= n) return *(const Four<float>*)(row + at);
     Four<float> f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) f.v[i] = at + i < n ? row[at + i] : 0.0f;
@@ -48,7 +43,7 @@ __device__ __forceinline__ Four<float> load4(const float* row, int at, int n) {
 }
 
 // NV pieces of four logits per thread: a chunk is 1024 NV logits.
-template <int NV, bool IN_PLACE, bool STREAM>
+template <int NV, bool IN_PLACE>
 __global__ __launch_bounds__(kThreads) void penalize_kernel(const PenalizeArgs a) {
     constexpr int kChunk = NV * 4 * kThreads;
     __shared__ u32x4 count4[kChunk / 4];
@@ -65,7 +60,7 @@ __global__ __launch_bounds__(kThreads) void penalize_kernel(const PenalizeArgs a
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int at = 4 * (tid + kThreads * j);
-        if constexpr (!IN_PLACE) l[j] = load4<STREAM>(in, at, n);
+        if constexpr (!IN_PLACE) l[j] = load4(in, at, n);
         allowed[j] = mask && at < n ? mask[(v0 + at) >> 5] : 0xFFFFFFFFu;
     }
     if (a.tokens || a.n_bias) {
@@ -124,7 +119,7 @@ __global__ __launch_bounds__(kThreads) void penalize_kernel(const PenalizeArgs a
         if (a.tokens) m = count4[tid + kThreads * j];
         if constexpr (IN_PLACE) {
             if (bits == 15u && ((m[0] | m[1] | m[2] | m[3]) & ~kBiased) == 0u) continue;
-            l[j] = load4<STREAM>(in, at, n);
+            l[j] = load4(in, at, n);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -138,8 +133,7 @@ __global__ __launch_bounds__(kThreads) void penalize_kernel(const PenalizeArgs a
             l[j].v[i] = (bits >> i) & 1u ? x : -INFINITY;
         }
         if (at + 4 <= n) {
-            if constexpr (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(f32x4_any, l[j]), (f32x4_any*)(out + at));
-            else *(Four<float>*)(out + at) = l[j];
+            *(Four<float>*)(out + at) = l[j];
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -198,24 +192,23 @@ __global__ __launch_bounds__(kThreads) void penalize_kernel(const PenalizeArgs a
     }
 }
 
-// 8 to 128 MB of logits pass the caches by: 64 rows 26 us instead of 29 into the buffer of the
-// call before and of 33 into a new one, with the sampler after it 98 and 97; 16 rows 10 and 12,
-// 52 and 53.  (Of 300 rows of 152000 the sampler loses more than that: 205 us for both instead of 200.)
+// The logits stay in the caches for whoever reads them next.  Loads and stores that pass them by make
+// this call alone shorter (64 rows of 248320 26.5 us instead of 31.7) and the step longer: with the
+// sampler after it 98.7 instead of 96.8, with an argmax 122 instead of 100.
 template <int NV>
 void launch(const PenalizeArgs& a, hipStream_t s) {
     const dim3 grid((a.V + NV * 4 * kThreads - 1) / (NV * 4 * kThreads), a.B);
-    const long long logits = (long long)a.B * a.V;
-    if (a.out == a.logits) penalize_kernel<NV, true, false><<<grid, kThreads, 0, s>>>(a);
-    else if (NV > 1 && logits >= 2LL << 20 && logits <= 32LL << 20) penalize_kernel<NV, false, NV != 1><<<grid, kThreads, 0, s>>>(a);
-    else penalize_kernel<NV, false, false><<<grid, kThreads, 0, s>>>(a);
+    if (a.out == a.logits) penalize_kernel<NV, true><<<grid, kThreads, 0, s>>>(a);
+    else penalize_kernel<NV, false><<<grid, kThreads, 0, s>>>(a);
 }
 
 }  // namespace
 
-// Chunks of 4096 logits where there are enough of them (with 8192 there are too few work groups
-// a CU to hide the counting: 64 rows of 248320 with 4000 tokens 28.6 us instead of 30.5), of 8192
-// for long histories, which are read once per chunk (131072 tokens 82 us instead of 88, 32000
-// tokens 40 with both), down to 1024 so that one row of 248320 still has 243 work groups.
+// Chunks of 1024, 2048, 4096 and 8192 logits (us, 248320 logits a row, new buffers): larger ones read
+// the history less often, smaller ones are more work groups.  4000 tokens: 1 row (2000) 3.9, 4.4, 5.4,
+// 7.6; 4 rows 5.7, 6.2, 7.2, 9.4; 16 rows 12.9, 11.6, 12.0, 13.1; 32 rows 20.1, 17.6, 16.8, 17.5; 64
+// rows 46, 34, 33, 35.  64 rows with 32000 tokens 83, 57, 44.6, 45.4, 65000 130, 85, 64.4, 62.7,
+// 131072 211, 133, 95, 90.
 hipError_t launch_penalize(const PenalizeArgs& a, hipStream_t s) {
     const long long logits = (long long)a.B * a.V;
     if (logits >= 8192LL * 1024 && a.tokens && a.stride > 32768) launch<8>(a, s);
