@@ -417,7 +417,8 @@ int moe_add_norm(const uint16_t* x, int32_t T, int32_t d, const void* residual,
    power of two in the largest product of its eight columns 8 i .. 8 i + 7: small products next
    to large ones that cancel.
    A last block of columns or rows may be shorter than 128.  A NaN code or a scale that is
-   not finite gives what the formula gives.
+   not finite gives what the formula gives.  xs * ws is rounded to fp32 first: below 2^-125
+   bits of it are lost.
    y: fp32 [T][N], or bf16 (one rounding) with MOE_OUT_BF16, or with MOE_GATED 8 bits:
    then w and scale hold two matrices of I = N / 2 rows each, [2][I][K] and
    [2][ceil(I/128)][ceil(K/128)], the gate's and the up matrix's, and
@@ -456,8 +457,8 @@ int moe_experts_scaled(const moe_e4m3mat* m, int32_t E, int32_t N, int32_t K, co
    and d_rows as said below.
    moe_dispatch: rows[inv_perm[t * k + s]] = x[t] for every slot s.  x: bf16 [T][d]; rows:
    bf16 [T * k][d] with rows_scale NULL, else e4m3 codes [T * k][d] and rows_scale
-   [T * k][ceil(d/128)]: scale = max |x| / 448 over 128 columns, codes of x / scale to
-   nearest even, with moe_add_norm's rules for zeros, infinities and NaN.
+   [T * k][ceil(d/128)]: scale = max |x| / 448 over 128 columns, codes of the fp32 quotient
+   x / scale to nearest even, with moe_add_norm's rules for zeros, infinities and NaN.
    moe_combine: y[t] = sum_s w[t][s] * rows[inv_perm[t * k + s]] + base[t], in fp32,
    slots in order, base last, rounded once.  w = topk_w, or 1 with MOE_UNWEIGHTED (the
    gradient of moe_dispatch).  A slot of weight 0 is left out, whatever its row holds.
