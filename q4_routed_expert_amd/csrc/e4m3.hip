@@ -617,9 +617,9 @@ int tiles_of(ProductArgs& a) {
 //     (half the work between two waits).
 //   Matrices that one tile of rows reads, 64 MB and more: their loads ask not to be kept (nt).  With
 //     and without: gated experts, 8 tokens 23.9 and 24.7, 64 tokens 70 and 79, 512 tokens 96 and 105,
-//     768 99 and 104, 1024 111 and 110; tiles of 128
-//     rows, bf16, K = 512: 32 rows 58 and 62, 64 rows 71 and 73, 128 rows, skewed, 105 and 96;
-//     bf16, 64 tokens 37 and 43; 8 tokens, 248320 x 2048: 80 and 91.  Where tiles of rows share
+//     768 99 and 104, 1024 111 and 110; bf16, 2048 rows, K = 512, 64 tokens 37 and 43, rows of an
+//     expert 8 46 and 53, 24 61 and 62, 32 69 and 65.5, and in tiles of 128 rows 40 70.6 and 72.3,
+//     64 81 and 80.5, 128 106 and 95; 8 tokens, 248320 x 2048: 80 and 91.  Where tiles of rows share
 //     them it costs (64 rows an expert 176 and 157), and where the last-level cache may hold them
 //     from call to call (32 tokens, 2 x 8192 x 2048 gated 20 and 18).
 //   8 tokens, 248320 x 2048: 91 with 32 x 256, 97 with 32 x 64; 60000 rows: 28 and 26.
