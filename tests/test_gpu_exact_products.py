@@ -13,7 +13,7 @@ import torch
 
 import q4_routed_expert_amd as q4
 from oracle import operators as plain
-from routings import device_routing, selections, values
+from routings import device_routing, quantised_rows, selections, values
 
 pytestmark = pytest.mark.gpu
 f8 = torch.float8_e4m3fn
@@ -104,6 +104,19 @@ def experts(dev, rng, T, E, k, N, K, small, **how):
 def test_experts_of_few_rows_lose_no_product(dev, T, E, k, N, K):
     for y, x, w in experts(dev, np.random.default_rng(T + N), T, E, k, N, K, FEW):
         check(y, x, w)
+
+
+# the same bar for ordinary values and scales, whose factors xs * ws are rounded once
+@pytest.mark.parametrize("T,N,K", [(1, 16500, 192), (16, 40001, 128), (17, 1000, 512), (33, 257, 576),
+                                   (65, 4100, 256), (127, 130, 640), (127, 9000, 192)])
+def test_ordinary_values_of_few_tokens(dev, T, N, K):
+    rng = np.random.default_rng(T + N)
+    x, xs = quantised_rows(rng, T, K)
+    w, ws = q4.quantize_blocks(torch.from_numpy(rng.standard_normal((N, K)).astype(np.float32)))
+    want, size = plain.product(values(w), ws.numpy(), values(x), xs.numpy())
+    y = q4.linear_e4m3(w.to(dev), ws.to(dev), x.to(dev), xs.to(dev))
+    err = np.abs(y.float().cpu().numpy().astype(np.float64) - want)
+    assert (err <= bar_of(size, K) + np.abs(want) * 2.0 ** -8).all()
 
 
 # every tile of the calls that may lose something
